@@ -49,6 +49,15 @@ SIGNATURES = {
                                              _i64, _i64, _p]),
     "dg_fp8_quantize_1x128_gather": (ctypes.c_int, [_p, ctypes.c_int, _i64, _i64, _p, _p, _i64, _p, _i64,
                                                     _i64, _i64, _i64, _p]),
+    "dg_fp8_rmsnorm_quantize_1x128": (ctypes.c_int, [_p, ctypes.c_int, _i64, _p, ctypes.c_int, _i64, _p, _i64,
+                                                     _p, ctypes.c_int, ctypes.c_float, _p, _i64, _p, _i64,
+                                                     _p, _i64, _i64, _i64, _i64, _p]),
+    "dg_moe_gate_topk": (ctypes.c_int, [_p, ctypes.c_int, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_float,
+                                        _p, _p, _i64, _i64, _i64, _p]),
+    "dg_fp8_moe_layer": (ctypes.c_int, [_p, _i64, _p, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64, _i64,
+                                        _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _p, _p, _i64,
+                                        _i64, _i64, _i64, _i64, _i64, _p, _i64, _p]),
+    "dg_fp8_moe_layer_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64, _i64]),
     "dg_moe_route_contiguous": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p, _p, _i64, _p]),
     "dg_moe_contiguous_max_rows": (ctypes.c_int64, [_i64, _i64]),
     "dg_moe_unpermute": (ctypes.c_int, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p]),

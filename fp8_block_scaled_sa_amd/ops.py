@@ -461,3 +461,133 @@ def dg_fp8_grouped_gemm_masked_fmt(a, sa, b, sb, masked_m, a_fmt="e4m3", b_fmt="
         G, M_max, N, K, _stream(stream))
     _check(st, "dg_fp8_grouped_gemm_masked_fmt")
     return d
+
+
+def _rows(t, name, dtypes):
+    """Checks a 2-D row-contiguous tensor; returns its row stride (a single row's own stride is free in torch)."""
+    if t.dtype not in dtypes:
+        raise TypeError("%s must be %s" % (name, " or ".join(str(d).replace("torch.", "") for d in dtypes)))
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s must be 2-D with contiguous rows" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def dg_fp8_rmsnorm_quantize_1x128(x, weight, eps=1e-6, residual=None, residual_out=None, normed=False, y=None,
+                                  q=None, s=None, stream=None):
+    """Root-mean-square norm of x[M,K] + residual[M,K] (float32 or bfloat16
+    each, residual optional) times weight[K], as codes Q[M,K] and scales
+    S[M,K/128]. With a residual the sum is written to residual_out (new unless
+    given; the residual itself updates it in place). normed=True (or a given y)
+    also returns the normed rows in bfloat16. A new S is M-major. Returns
+    (q, s, residual_out, y), None for what was not asked for."""
+    ldx = _rows(x, "x", DTYPES)
+    M, K = x.shape
+    if weight.dtype not in DTYPES or tuple(weight.shape) != (K,) or weight.stride(0) != 1:
+        raise ValueError("weight must be a contiguous float32 or bfloat16 [K] tensor")
+    ldr = ldro = ldy = r_dtype = 0
+    if residual is not None:
+        ldr, r_dtype = _rows(residual, "residual", DTYPES), DTYPES[residual.dtype]
+        if residual_out is None:
+            residual_out = torch.empty((M, K), dtype=residual.dtype, device=x.device)
+        ldro = _rows(residual_out, "residual_out", (residual.dtype,))
+        if residual.shape != x.shape or residual_out.shape != x.shape:
+            raise ValueError("shape mismatch")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    if y is None and normed:
+        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
+    if y is not None:
+        ldy = _rows(y, "y", (torch.bfloat16,))
+        if y.shape != x.shape:
+            raise ValueError("shape mismatch")
+    if q is None:
+        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+    if s is None:
+        s = torch.empty((K // BLOCK, M), dtype=torch.float32, device=x.device).t()
+    ldq = _rows(q, "q", (torch.uint8, torch.float8_e4m3fn))
+    _scales(s, "s", 2)
+    if q.shape != x.shape or tuple(s.shape) != (M, K // BLOCK):
+        raise ValueError("shape mismatch")
+    st = _lib.load().dg_fp8_rmsnorm_quantize_1x128(
+        _dev(x, "x"), DTYPES[x.dtype], ldx,
+        None if residual is None else _dev(residual, "residual"), r_dtype, ldr,
+        None if residual is None else _dev(residual_out, "residual_out"), ldro,
+        _dev(weight, "weight"), DTYPES[weight.dtype], eps, None if y is None else _dev(y, "y"), ldy,
+        _dev(q, "q"), ldq, _dev(s, "s"), s.stride(0), s.stride(1), M, K, _stream(stream))
+    _check(st, "dg_fp8_rmsnorm_quantize_1x128")
+    return q, s, residual_out, y
+
+
+GATE_SCORES = {"softmax": 0, "sigmoid": 1}   # DG_GATE_SOFTMAX, DG_GATE_SIGMOID
+
+
+def _slots(t, name, dtype, T, top_k):
+    if t.dtype != dtype or tuple(t.shape) != (T, top_k) or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s [T, top_k] tensor" % (name, str(dtype).replace("torch.", "")))
+    return _dev(t, name)
+
+
+def dg_moe_gate_topk(logits, top_k, score="softmax", renormalize=True, factor=1.0, ids=None, weights=None,
+                     stream=None):
+    """The top_k largest logits[T,E] (float32 or bfloat16) of each token: expert
+    ids[T,top_k] (int32, equal logits in ascending order of expert, -1 where
+    only -inf or NaN are left) and weights[T,top_k] (float32): softmax over the
+    chosen experts (renormalize) or all of them, or sigmoid, divided by the
+    chosen ones' sum if renormalize; times factor. Returns (ids, weights)."""
+    ldl = _rows(logits, "logits", DTYPES)
+    if score not in GATE_SCORES:
+        raise ValueError("score must be one of %s" % ", ".join(GATE_SCORES))
+    T, E = logits.shape
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
+    st = _lib.load().dg_moe_gate_topk(
+        _dev(logits, "logits"), DTYPES[logits.dtype], ldl, GATE_SCORES[score], int(renormalize), factor,
+        _slots(ids, "ids", torch.int32, T, top_k), _slots(weights, "weights", torch.float32, T, top_k),
+        T, E, top_k, _stream(stream))
+    _check(st, "dg_moe_gate_topk")
+    return ids, weights
+
+
+def dg_fp8_moe_layer_workspace_bytes(T: int, top_k: int, H: int, I: int) -> int:  # noqa: E741
+    """Workspace bytes of dg_fp8_moe_layer for these sizes."""
+    return _query(_lib.load().dg_fp8_moe_layer_workspace_bytes(T, top_k, H, I), "dg_fp8_moe_layer_workspace_bytes")
+
+
+def dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, topk_ids, topk_weights, workspace, out=None, stream=None):
+    """A mixture-of-experts layer for up to 64 tokens: x[T,H] codes with scales
+    sx[T,H/128], w13[E,2I,H] (gate rows, then up rows) with s13[E,2I/128,H/128],
+    w2[E,H,I] with s2[E,H/128,I/128], topk_ids[T,top_k] int32 (outside [0, E):
+    slot skipped), topk_weights[T,top_k] float32 -> out[T,H] bfloat16 =
+    sum_j weight_j W2_e (silu(gate) * up). workspace: a device tensor of at
+    least dg_fp8_moe_layer_workspace_bytes(T, top_k, H, I) bytes."""
+    ldx = _rows(x, "x", (torch.uint8, torch.float8_e4m3fn))
+    _codes(w13, "w13", 3), _codes(w2, "w2", 3)
+    _scales(sx, "sx", 2), _scales(s13, "s13", 3), _scales(s2, "s2", 3)
+    T, H = x.shape
+    E, I2, _ = w13.shape
+    I = I2 // 2  # noqa: E741
+    if I2 % 2 or w13.shape[2] != H or tuple(w2.shape) != (E, H, I):
+        raise ValueError("shape mismatch")
+    if (tuple(sx.shape) != (T, H // BLOCK) or tuple(s13.shape) != (E, I2 // BLOCK, H // BLOCK)
+            or tuple(s2.shape) != (E, H // BLOCK, I // BLOCK)):
+        raise ValueError("scale shape mismatch")
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [T, top_k]")
+    top_k = topk_ids.shape[1]
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    ldo = _rows(out, "out", (torch.bfloat16,))
+    if out.shape != x.shape:
+        raise ValueError("shape mismatch")
+    wp, wb = _ws(workspace)
+    st = _lib.load().dg_fp8_moe_layer(
+        _dev(x, "x"), ldx, _dev(sx, "sx"), sx.stride(0), sx.stride(1),
+        _dev(w13, "w13"), w13.stride(1), w13.stride(0), _dev(s13, "s13"), s13.stride(0), s13.stride(1), s13.stride(2),
+        _dev(w2, "w2"), w2.stride(1), w2.stride(0), _dev(s2, "s2"), s2.stride(0), s2.stride(1), s2.stride(2),
+        _slots(topk_ids, "topk_ids", torch.int32, T, top_k),
+        _slots(topk_weights, "topk_weights", torch.float32, T, top_k),
+        _dev(out, "out"), ldo, T, top_k, E, H, I, wp, wb, _stream(stream))
+    _check(st, "dg_fp8_moe_layer")
+    return out

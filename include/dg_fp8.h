@@ -471,6 +471,114 @@ dg_status dg_moe_unpermute(const void *D, int64_t ldd, int64_t d_rows,
                            const int32_t *row_of_token, int64_t T, int64_t N,
                            void *out, int64_t ldo, void *stream);
 
+/*
+ * Residual addition and root-mean-square norm of activation rows, straight to
+ * the products' LHS: e4m3 codes and one scale per 1x128 block. For row m:
+ *   h     = X[m, :] + R[m, :]                        (h = X[m, :] when R is NULL)
+ *   R_out = h, rounded to R's type                   (the residual stream; not with R NULL)
+ *   y     = h / sqrt(mean(h^2) + eps) * W
+ *   Y     = y, rounded to bf16                       (NULL: not wanted)
+ *   Q, S  = the codes and scales of y as dg_fp8_quantize_1x128 defines them
+ * Everything between the loads and these roundings is fp32; the norm is taken
+ * of the unrounded h, the codes and Y of the unrounded y.
+ *   X [M, K] fp32 or bf16 (x_dtype: DG_DTYPE_F32, DG_DTYPE_BF16), row stride ldx
+ *   R, R_out [M, K] fp32 or bf16 (r_dtype), row strides ldr, ldro; both NULL: no residual
+ *   W [K] fp32 or bf16 (w_dtype)
+ *   Y [M, K] bf16, row stride ldy;  Q [M, K], row stride ldq;
+ *   S logical [M, K/128] at S[m*s_stride_m + kb*s_stride_kb]
+ * Non-finite inputs give what the formulas give in R_out and Y; the codes and
+ * scales of that row are unspecified (no fault).
+ * Constraints: 0 < K <= 65536 (DG_ERR_UNSUPPORTED above), K % 128 == 0, eps >= 0;
+ * X, R, R_out, W, Y, Q 16-byte aligned, row strides multiples of 16 bytes; S
+ * 4-byte aligned; strides at most 2^28 elements (DG_ERR_UNSUPPORTED above);
+ * scale slots distinct as in dg_fp8_quantize_1x128. The outputs lie apart from
+ * each other and from the inputs, but R_out may be R itself (same address and
+ * stride). Deterministic; M = 0 returns DG_OK without launching.
+ */
+dg_status dg_fp8_rmsnorm_quantize_1x128(const void *X, int x_dtype, int64_t ldx,
+                                        const void *R, int r_dtype, int64_t ldr,
+                                        void *R_out, int64_t ldro,
+                                        const void *W, int w_dtype, float eps,
+                                        void *Y, int64_t ldy,
+                                        void *Q, int64_t ldq,
+                                        float *S, int64_t s_stride_m, int64_t s_stride_kb,
+                                        int64_t M, int64_t K, void *stream);
+
+/* Scores of dg_moe_gate_topk. */
+#define DG_GATE_SOFTMAX 0
+#define DG_GATE_SIGMOID 1
+
+/*
+ * A mixture-of-experts router's choice: the top_k largest logits of each
+ * token, in descending order, and their weights.
+ *   logits  [T, E] fp32 or bf16 (l_dtype), row stride ldl
+ *   ids     [T, top_k] int32 (written), contiguous: the experts; of equal
+ *           logits the lower expert comes first
+ *   weights [T, top_k] fp32 (written), contiguous: factor times
+ *     DG_GATE_SOFTMAX  exp(l_j) / sum of exp(l) over the chosen experts
+ *                      (renormalize != 0) or over all E
+ *     DG_GATE_SIGMOID  1 / (1 + exp(-l_j)), divided by the chosen experts' sum
+ *                      when renormalize != 0
+ * A logit of -inf (an expert the token may not use) or NaN is never chosen and
+ * has no share in a sum; slots without a candidate get id -1 and weight 0,
+ * which dg_fp8_moe_layer skips. A logit of +inf is chosen first, with the
+ * weight that the formula gives (NaN for the softmax). fp32 throughout.
+ * With top_k = 1 the ids are the expert_of_token of dg_moe_route_contiguous.
+ * Constraints: 1 <= top_k <= min(E, 16), E <= 1024 (DG_ERR_UNSUPPORTED above
+ * 16 and 1024), ldl >= E and at most 2^28; pointers aligned to their element;
+ * outputs apart from each other and from logits. T = 0 returns DG_OK.
+ */
+dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
+                           int score, int renormalize, float factor,
+                           int32_t *ids, float *weights,
+                           int64_t T, int64_t E, int64_t top_k, void *stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens (T <= 64, one decode step
+ * of a batch), in two launches: for every token t and its slots j with expert
+ * e = topk_ids[t, j] in [0, E)
+ *   [g; u] = W13_e x_t      h = g / (1 + exp(-g)) * u
+ *   out_t  = bf16( sum_j topk_weights[t, j] * W2_e h )
+ * with x_t = sX[t, kb] X[t, k] and block-scaled weights as in the grouped
+ * calls. A slot whose id lies outside [0, E) (no expert, or another GPU's) adds
+ * nothing, whatever its weight; a token without any gets a row of zeros.
+ *   X   [T, H] e4m3, row stride ldx          sX logical [T, H/128]
+ *   W13 [E, 2 I, H] e4m3: expert e at W13 + e*w13_stride_e, row stride ld13;
+ *       rows [0, I) give g, rows [I, 2 I) give u      s13 logical [E, 2 I/128, H/128]
+ *   W2  [E, H, I] e4m3, w2_stride_e, ld2     s2 logical [E, H/128, I/128]
+ *   topk_ids [T, top_k] int32, topk_weights [T, top_k] fp32, contiguous (device);
+ *       as dg_moe_gate_topk writes them; a token may name an expert twice
+ *   out [T, H] bf16, row stride ldo (every row is written)
+ *   workspace  device memory of dg_fp8_moe_layer_workspace_bytes bytes or
+ *       more (DG_ERR_SCRATCH below), 16-byte aligned; its contents on entry do
+ *       not matter. Calls that use one workspace must be ordered (one stream).
+ * The ids and weights are read on the device: no synchronisation, safe to
+ * capture, and they may change between replays. A block's products are summed
+ * as in the grouped calls; h keeps 16 bits of mantissa; everything else is
+ * fp32 up to the one rounding of out. Each chosen expert's weights are read
+ * once per 64 of its tokens. Deterministic: fixed orders of summation.
+ * For more tokens: the contiguous grouped calls.
+ * Constraints: H % 128 == 0, I % 128 == 0; T <= 64, 1 <= top_k <= 16,
+ * 1 <= E <= 1024, H and I at most 2^20 (DG_ERR_UNSUPPORTED above); bases,
+ * ldx, ld13, ld2 and the expert strides as in the grouped calls (16-byte
+ * multiples), ldo a multiple of 8; row and scale strides at most 2^28. out and
+ * workspace lie apart from each other and from the inputs. T = 0 returns DG_OK.
+ */
+dg_status dg_fp8_moe_layer(const void *X, int64_t ldx,
+                           const float *sX, int64_t sx_stride_m, int64_t sx_stride_kb,
+                           const void *W13, int64_t ld13, int64_t w13_stride_e,
+                           const float *s13, int64_t s13_stride_e, int64_t s13_stride_nb, int64_t s13_stride_kb,
+                           const void *W2, int64_t ld2, int64_t w2_stride_e,
+                           const float *s2, int64_t s2_stride_e, int64_t s2_stride_nb, int64_t s2_stride_kb,
+                           const int32_t *topk_ids, const float *topk_weights,
+                           void *out, int64_t ldo,
+                           int64_t T, int64_t top_k, int64_t E, int64_t H, int64_t I,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes of dg_fp8_moe_layer for these sizes (T * top_k * I * 4); a
+ * negative value is -dg_status (bad or unsupported sizes). Needs no device. */
+int64_t dg_fp8_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I);
+
 #ifdef __cplusplus
 }
 #endif
