@@ -36,6 +36,11 @@ constexpr int kMaxTokens = 64;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kMaxExperts = 1024;
+// The kernels keep a lane's offsets in 32 bits: 63 rows of X or 15 rows of
+// weights, and both parts of h for all pairs, stay below 2^31 bytes.
+constexpr int kMaxWidth = 1 << 18;                // H and I
+constexpr int64_t kMaxRowStride = 1 << 25;
+constexpr int64_t kMaxTokenScaleStride = 1 << 22;
 
 struct LayerParams {
     const uint8_t *X;       // e4m3 [T, H]
@@ -54,14 +59,19 @@ struct LayerParams {
     const float *weights;   // [T, top_k]
     uint16_t *out;          // bf16 [T, H]
     int64_t ldo;
-    uint16_t *h;            // workspace: [pairs][I / 8][hi 8, lo 8] bf16
+    uint16_t *h;            // workspace: bf16 [hi, lo][pairs][I]
     int T, top_k, E, H, I;
 };
 
-__device__ __forceinline__ u32x4 load16(const uint8_t *p) { return *(const u32x4 *)p; }
-__device__ __forceinline__ u32x4 load16_once(const uint8_t *p)
+__device__ __forceinline__ u32x4 load16(const uint8_t *base, uint32_t offset)
 {
-    return __builtin_nontemporal_load((const u32x4 *)p);
+    return *(const u32x4 *)(base + offset);
+}
+
+// For data that is read once.
+__device__ __forceinline__ u32x4 load16_once(const uint8_t *base, uint32_t offset)
+{
+    return __builtin_nontemporal_load((const u32x4 *)(base + offset));
 }
 
 __device__ __forceinline__ v8i join(const u32x4 &a, const u32x4 &b)
@@ -69,9 +79,33 @@ __device__ __forceinline__ v8i join(const u32x4 &a, const u32x4 &b)
     return v8i{(int)a[0], (int)a[1], (int)a[2], (int)a[3], (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
 }
 
+// Offset of this lane's 16 bytes in load 0 of a block of 16 rows x 128 bytes
+// (load 1: 8 rows further on).
+__device__ __forceinline__ uint32_t block_offset(int lane, int64_t ld)
+{
+    return (uint32_t)((lane & 7) * (int)ld + 32 * (lane >> 4) + 16 * ((lane >> 3) & 1));
+}
+
+// From load order to operand order: lanes 8..15 of each 16 take a from lane ^ 8's b, lanes 0..7 b from its a.
+__device__ __forceinline__ void exchange_halves(u32x4 &a, u32x4 &b)
+{
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int va = (int)a[c], vb = (int)b[c];
+        a[c] = (uint32_t)__builtin_amdgcn_update_dpp(va, vb, 0x128, 0xF, 0xC, false);  // row_ror:8
+        b[c] = (uint32_t)__builtin_amdgcn_update_dpp(vb, va, 0x128, 0xF, 0x3, false);
+    }
+}
+
+__device__ __forceinline__ float from_lane_xor_8(float v)
+{
+    return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), 0x128, 0xF, 0xF, false));
+}
+
 // The pairs (token * top_k + slot) of expert e, in ascending order, into list;
 // returns how many. One wave.
-__device__ __forceinline__ int list_pairs(const int32_t *ids, int pairs, int e, int lane, uint16_t *list)
+template <typename Id>
+__device__ __forceinline__ int list_pairs(const Id *ids, int pairs, int e, int lane, uint16_t *list)
 {
     int n = 0;
     for (int c = 0; c < pairs; c += 64) {
@@ -101,19 +135,20 @@ template <int NT, int D>
 __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, const uint16_t *list, int base, int np,
                                          v4f (*red)[64])
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, lg = lane >> 4;
+    const int lane = threadIdx.x & 63, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     const int nkb = p.H >> 7;
-    const uint8_t *gate = p.W13 + e * p.w13_e + (n0 + (lane & 15)) * p.ld13 + 16 * lg;
+    const uint8_t *gate = p.W13 + e * p.w13_e + n0 * p.ld13;
     const uint8_t *up = gate + p.I * p.ld13;
+    const uint32_t row0 = block_offset(lane, p.ld13), row8 = row0 + 8 * (uint32_t)p.ld13;
     const float *sg = p.s13 + e * p.s13_e + (n0 >> 7) * p.s13_nb;
     const float *su = p.s13 + e * p.s13_e + ((p.I + n0) >> 7) * p.s13_nb;
-    const uint8_t *x[NT];
-    const float *sx[NT];
+    uint32_t xo[NT], so[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
         const int token = list[min(base + 16 * i + (lane & 15), np - 1)] / p.top_k;
-        x[i] = p.X + token * p.ldx + 16 * lg;
-        sx[i] = p.sX + token * p.sx_m;
+        xo[i] = (uint32_t)(token * (int)p.ldx + 32 * lg);
+        so[i] = (uint32_t)(token * (int)p.sx_m);
     }
     v4f ag[NT], au[NT];
 #pragma unroll
@@ -126,22 +161,23 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
     auto load = [&](int j, UpStage<NT> &s) {
         const int kb = min(wave + j * kUpWaves, nkb - 1);
         const int64_t k = (int64_t)kb * 128;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            s.g[c] = load16_once(gate + k + 64 * c);
-            s.u[c] = load16_once(up + k + 64 * c);
-        }
+        s.g[0] = load16_once(gate + k, row0);
+        s.g[1] = load16_once(gate + k, row8);
+        s.u[0] = load16_once(up + k, row0);
+        s.u[1] = load16_once(up + k, row8);
+        const float *sx = p.sX + kb * p.sx_kb;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                s.x[i][c] = load16(x[i] + k + 64 * c);
-            s.sx[i] = sx[i][kb * p.sx_kb];
+            s.x[i][0] = load16(p.X + k, xo[i]);
+            s.x[i][1] = load16(p.X + k + 16, xo[i]);
+            s.sx[i] = sx[so[i]];
         }
         s.sg = sg[kb * p.s13_kb];
         s.su = su[kb * p.s13_kb];
     };
-    auto compute = [&](const UpStage<NT> &s) {
+    auto compute = [&](UpStage<NT> &s) {
+        exchange_halves(s.g[0], s.g[1]);
+        exchange_halves(s.u[0], s.u[1]);
         const v8i wg = join(s.g[0], s.g[1]), wu = join(s.u[0], s.u[1]);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -162,7 +198,7 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
         }
     }
 
-    // red[wave][2 i + (0 gate, 1 up)][lane]: rows 4 lg .. 4 lg + 3 of token lane % 16
+    // red[wave][i][gate, up][lane]: rows 4 lg .. 4 lg + 3 of token lane % 16
     __syncthreads();  // the previous pass's reads
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
@@ -186,46 +222,55 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
                 hi[c] = dgk::bf16_rne(h);
                 lo[c] = dgk::bf16_rne(h - __uint_as_float(hi[c] << 16));
             }
-            const int row = n0 + 4 * lg;
-            uint16_t *to = p.h + ((int64_t)list[at] * p.I + (row & ~7)) * 2 + (row & 7);
+            uint16_t *to = p.h + (int64_t)list[at] * p.I + n0 + 4 * lg;
             *(u32x2 *)to = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
-            *(u32x2 *)(to + 8) = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+            to += (int64_t)p.T * p.top_k * p.I;
+            *(u32x2 *)to = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
         }
     }
 }
 
 // One workgroup per 16 columns of h of one expert. by_pair: slot s of the grid
 // is the expert of pair s, if no earlier pair has it (fewer pairs than
-// experts); else slot s is expert s.
-template <int NT, int D>
+// experts); else slot s is expert s. With up to 64 pairs every wave lists the
+// expert's pairs for itself.
+template <int NT, int D, bool FEW>
 __global__ __launch_bounds__(kUpThreads) void gate_up_kernel(LayerParams p, int by_pair)
 {
-    __shared__ uint16_t list[kMaxPairs];
+    __shared__ uint16_t list[FEW ? 64 * kUpWaves : kMaxPairs];
     __shared__ int count;
     __shared__ v4f red[kUpWaves * NT * 2][64];
-    const int tiles = p.I >> 4;
+    const int tiles = p.I >> 4, pairs = p.T * p.top_k;
     const int slot = blockIdx.x / tiles, n0 = (blockIdx.x - slot * tiles) * 16;
-    const int e = by_pair ? p.ids[slot] : slot;
+    const int e = __builtin_amdgcn_readfirstlane(by_pair ? p.ids[slot] : slot);
     if (e < 0 || e >= p.E)
         return;
-    if (threadIdx.x < 64) {
-        const int n = list_pairs(p.ids, p.T * p.top_k, e, threadIdx.x, list);
-        if (threadIdx.x == 0)
-            count = n;
+    int np;
+    uint16_t *mine = list;
+    if (FEW) {
+        mine = list + 64 * (threadIdx.x >> 6);
+        np = list_pairs(p.ids, pairs, e, threadIdx.x & 63, mine);
+    } else {
+        if (threadIdx.x < 64) {
+            const int n = list_pairs(p.ids, pairs, e, threadIdx.x, list);
+            if (threadIdx.x == 0)
+                count = n;
+        }
+        __syncthreads();
+        np = count;
     }
-    __syncthreads();
-    const int np = count;
-    if (np == 0 || (by_pair && list[0] != slot))
+    np = __builtin_amdgcn_readfirstlane(np);
+    if (np == 0 || (by_pair && mine[0] != slot))
         return;
     int base = 0;
     if (NT >= 4)
         for (; np - base > 32; base += 64)
-            up_tiles<NT, D>(p, e, n0, list, base, np, red);
+            up_tiles<NT, D>(p, e, n0, mine, base, np, red);
     if (NT >= 2)
         for (; np - base > 16; base += 32)
-            up_tiles<NT < 2 ? NT : 2, D>(p, e, n0, list, base, np, red);
+            up_tiles<NT < 2 ? NT : 2, D>(p, e, n0, mine, base, np, red);
     for (; base < np; base += 16)
-        up_tiles<1, D>(p, e, n0, list, base, np, red);
+        up_tiles<1, D>(p, e, n0, mine, base, np, red);
 }
 
 // ---------------------------------------------------------------- down
@@ -252,158 +297,219 @@ __device__ __forceinline__ void to_bf16(const u32x4 &w, bf16x8 *out)
 
 template <int NT, int NR>
 struct DownStage {
-    u32x4 w[NR];            // 16 NR rows, 64 bytes of K
-    u32x4 h[NT][2][2];      // NT x 16 pairs: [operand][hi, lo]
+    u32x4 w[NR][2];         // 16 NR rows, 128 bytes of K
+    u32x4 h[NT][4];         // NT x 8 pairs, hi and lo: this lane's 32 of 128 values
+    float s;
 };
 
-// Pairs base .. base + 16 NT of expert e's list against rows n0 .. n0 + 16 NR
+// Pairs base .. base + 8 NT of expert e's list against rows n0 .. n0 + 16 NR
 // of W2, K blocks [kb0, kb1): res[pair][16 NR] = weight * product.
 template <int NT, int NR, int D>
 __device__ __forceinline__ void down_tiles(const LayerParams &p, int e, int n0, const uint16_t *list, int base, int np,
                                            int kb0, int kb1, float *res)
 {
-    const int lane = threadIdx.x & 63, lg = lane >> 4;
-    const uint8_t *w = p.W2 + e * p.w2_e + (n0 + (lane & 15)) * p.ld2 + 16 * lg;
+    const int lane = threadIdx.x & 63, lg = lane >> 4, col = lane & 15;
+    const uint8_t *w = p.W2 + e * p.w2_e + n0 * p.ld2;
+    const uint32_t row0 = block_offset(lane, p.ld2), row8 = row0 + 8 * (uint32_t)p.ld2;
     const float *sw = p.s2 + e * p.s2_e + (n0 >> 7) * p.s2_nb;
-    const uint16_t *h[NT];
+    const uint8_t *h = (const uint8_t *)p.h;
+    uint32_t ho[NT];
     int pair[NT];
+    float weight[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        pair[i] = list[min(base + 16 * i + (lane & 15), np - 1)];
-        h[i] = p.h + (int64_t)pair[i] * p.I * 2 + 32 * lg;
+        pair[i] = list[min(base + 8 * i + (col & 7), np - 1)];
+        weight[i] = p.weights[pair[i]];
+        // column col: the hi (col < 8) or lo part of pair col % 8
+        ho[i] = (uint32_t)(((col >> 3) * p.T * p.top_k + pair[i]) * p.I * 2 + 64 * lg);
     }
-    v4f acc[NT][NR], part[NT][NR];
+    v4f acc[NT][NR];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int r = 0; r < NR; ++r)
-            acc[i][r] = part[i][r] = v4f{0.f, 0.f, 0.f, 0.f};
+            acc[i][r] = v4f{0.f, 0.f, 0.f, 0.f};
     DownStage<NT, NR> st[D];
-    const int first = 2 * kb0, last = 2 * kb1;  // halves of K blocks
-    auto load = [&](int half, DownStage<NT, NR> &s) {
-        const int64_t k = (int64_t)min(half, last - 1) * 64;
+    auto load = [&](int j, DownStage<NT, NR> &s) {
+        const int kb = min(j, kb1 - 1);
+        const int64_t k = (int64_t)kb * 128;
 #pragma unroll
-        for (int r = 0; r < NR; ++r)
-            s.w[r] = load16_once(w + 16 * r * p.ld2 + k);
+        for (int r = 0; r < NR; ++r) {
+            s.w[r][0] = load16_once(w + 16 * r * p.ld2 + k, row0);
+            s.w[r][1] = load16_once(w + 16 * r * p.ld2 + k, row8);
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    s.h[i][m][c] = *(const u32x4 *)(h[i] + 2 * k + 16 * m + 8 * c);
+            for (int q = 0; q < 4; ++q)
+                s.h[i][q] = load16(h + 2 * k + 16 * q, ho[i]);
+        s.s = sw[kb * p.s2_kb];
     };
-    auto compute = [&](const DownStage<NT, NR> &s) {
+    auto compute = [&](DownStage<NT, NR> &s) {
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            bf16x8 wr[2];
-            to_bf16(s.w[r], wr);
+            exchange_halves(s.w[r][0], s.w[r][1]);
+            bf16x8 wr[4];
+            to_bf16(s.w[r][0], wr);
+            to_bf16(s.w[r][1], wr + 2);
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i) {
+                v4f part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        part[i][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            wr[m], __builtin_bit_cast(bf16x8, s.h[i][m][c]), part[i][r], 0, 0, 0);
+                for (int q = 0; q < 4; ++q)
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wr[q], __builtin_bit_cast(bf16x8, s.h[i][q]), part,
+                                                                   0, 0, 0);
+                acc[i][r] += part * s.s;
+            }
         }
     };
 #pragma unroll
     for (int d = 0; d < D; ++d)
-        load(first + d, st[d]);
-    for (int half = first; half < last; half += D) {
+        load(kb0 + d, st[d]);
+    for (int j = kb0; j < kb1; j += D) {
 #pragma unroll
-        for (int d = 0; d < D; ++d) {   // D is even: a K block's two halves are in one turn
-            if (half + d < last)
+        for (int d = 0; d < D; ++d) {
+            if (j + d < kb1)
                 compute(st[d]);
-            load(half + d + D, st[d]);
-            if (d % 2 && half + d < last) {
-                const float s = sw[((half + d) >> 1) * p.s2_kb];
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        acc[i][r] += part[i][r] * s;
-                        part[i][r] = v4f{0.f, 0.f, 0.f, 0.f};
-                    }
-            }
+            load(j + d + D, st[d]);
         }
     }
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-        if (base + 16 * i + (lane & 15) < np) {
-            const float weight = p.weights[pair[i]];
+    for (int i = 0; i < NT; ++i) {
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
-                *(v4f *)(res + pair[i] * 16 * NR + 16 * r + 4 * lg) = acc[i][r] * weight;
+        for (int r = 0; r < NR; ++r) {
+            v4f sum;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                sum[c] = (acc[i][r][c] + from_lane_xor_8(acc[i][r][c])) * weight[i];
+            if (col < 8 && base + 8 * i + col < np)
+                *(v4f *)(res + pair[i] * 16 * NR + 16 * r + 4 * lg) = sum;
         }
+    }
 }
 
-// One workgroup per 16 NR columns of out, for all chosen experts: its waves
-// take the items (expert, slice of K), each result goes to its place in LDS,
-// and the sum over a token's slots and slices runs in a fixed order.
-template <int NR, int PAIRS, int RES>
+// One workgroup per 16 NR columns of out, for all chosen experts. Their K
+// blocks, one expert's after the other's, are dealt to the waves in equal
+// runs; each wave's part of an expert goes to a place of its own in LDS, and
+// the sum over a token's slots and an expert's parts runs in a fixed order.
+template <int NR, int PAIRS, int RES, int NT, int D>
 __global__ __launch_bounds__(kDownThreads) void down_kernel(LayerParams p)
 {
-    __shared__ float res[RES];          // [slice][pair][16 NR]
-    __shared__ int ids[PAIRS];
-    __shared__ int first[kMaxExperts];  // each expert's first pair
-    __shared__ int active[PAIRS];       // the chosen experts
+    constexpr bool kFew = PAIRS <= 64;
+    __shared__ float res[RES];                // [part][pair][16 NR]
+    __shared__ int16_t active_of[PAIRS];      // each pair's place in active, -1 without an expert
     __shared__ uint16_t list[kDownWaves][PAIRS];
+    __shared__ int16_t ids[kFew ? 1 : PAIRS];
+    __shared__ int16_t active[kFew ? 1 : PAIRS];       // the chosen experts
+    __shared__ int first[kFew ? 1 : kMaxExperts];      // each expert's first pair
+    __shared__ int16_t place[kFew ? 1 : kMaxExperts];  // ... and its place in active
+    static_assert(RES >= 2 * PAIRS * 16 * NR, "an expert has two parts where the waves' runs cut it");
     __shared__ int count;
     const int pairs = p.T * p.top_k;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n0 = blockIdx.x * 16 * NR;
-    for (int i = tid; i < p.E; i += kDownThreads)
-        first[i] = kMaxPairs;
-    __syncthreads();
-    for (int i = tid; i < pairs; i += kDownThreads) {
-        const int e = p.ids[i];
-        const bool in = e >= 0 && e < p.E;
-        ids[i] = in ? e : -1;
-        if (in)
-            atomicMin(&first[e], i);
-    }
-    __syncthreads();
-    if (wave == 0) {
-        int n = 0;
-        for (int c = 0; c < pairs; c += 64) {
-            const int e = c + lane < pairs ? ids[c + lane] : -1;
-            const bool lead = e >= 0 && first[e] == c + lane;
-            const uint64_t m = __ballot(lead);
-            if (lead)
-                active[n + __popcll(m & ((1ull << lane) - 1))] = e;
-            n += __popcll(m);
+
+    int nact = 0;
+    int my_expert = -1;                       // kFew: lane a's chosen expert a ...
+    uint64_t my_pairs = 0;                    // ... and the pairs that have it
+    if (kFew) {
+        int id = lane < pairs ? p.ids[lane] : -1;
+        if (id >= p.E)
+            id = -1;
+        int at = -1;
+        for (uint64_t left = __ballot(id >= 0); left; ++nact) {
+            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+            const uint64_t m = __ballot(id == e);
+            left &= ~m;
+            if (id == e)
+                at = nact;
+            if (lane == nact) {
+                my_expert = e;
+                my_pairs = m;
+            }
         }
-        if (lane == 0)
-            count = n;
+        if (wave == 0 && lane < pairs)
+            active_of[lane] = (int16_t)at;
+    } else {
+        for (int i = tid; i < p.E; i += kDownThreads)
+            first[i] = kMaxPairs;
+        __syncthreads();
+        for (int i = tid; i < pairs; i += kDownThreads) {
+            const int e = p.ids[i];
+            const bool in = e >= 0 && e < p.E;
+            ids[i] = (int16_t)(in ? e : -1);
+            if (in)
+                atomicMin(&first[e], i);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            int n = 0;
+            for (int c = 0; c < pairs; c += 64) {
+                const int e = c + lane < pairs ? ids[c + lane] : -1;
+                const bool lead = e >= 0 && first[e] == c + lane;
+                const uint64_t m = __ballot(lead);
+                if (lead) {
+                    const int at = n + __popcll(m & ((1ull << lane) - 1));
+                    active[at] = (int16_t)e;
+                    place[e] = (int16_t)at;
+                }
+                n += __popcll(m);
+            }
+            if (lane == 0)
+                count = n;
+        }
+        __syncthreads();
+        nact = count;
+        for (int i = tid; i < pairs; i += kDownThreads)
+            active_of[i] = ids[i] >= 0 ? place[ids[i]] : (int16_t)-1;
     }
-    __syncthreads();
-    const int nact = count, nkb = p.I >> 7;
-    int slices = 1;
-    if (nact > 0)
-        slices = max(1, min(min((kDownWaves + nact - 1) / nact, nkb), RES / (pairs * 16 * NR)));
-    for (int item = wave; item < nact * slices; item += kDownWaves) {
-        const int a = item / slices, sl = item - a * slices;
-        const int e = __builtin_amdgcn_readfirstlane(active[a]);
-        const int np = __builtin_amdgcn_readfirstlane(list_pairs(ids, pairs, e, lane, list[wave]));
-        const int kb0 = nkb * sl / slices, kb1 = nkb * (sl + 1) / slices;
-        float *to = res + sl * pairs * 16 * NR;
-        int base = 0;
-        for (; np - base > 16; base += 32)
-            down_tiles<2, NR, 2>(p, e, n0, list[wave], base, np, kb0, kb1, to);
-        for (; base < np; base += 16)
-            down_tiles<1, NR, 2>(p, e, n0, list[wave], base, np, kb0, kb1, to);
+    nact = __builtin_amdgcn_readfirstlane(nact);
+
+    // Waves in use: an expert's parts, (waves / nact rounded up) + 1 at most, have to fit res.
+    const int nkb = p.I >> 7, total = nact * nkb;
+    const int parts_cap = RES / (pairs * 16 * NR);
+    const int waves = max(1, min(min(kDownWaves, total), nact * (parts_cap - 1)));
+    if (wave < waves && nact > 0) {
+        int b = total * wave / waves;
+        const int end = total * (wave + 1) / waves;
+        while (b < end) {
+            const int a = b / nkb, kb0 = b - a * nkb, kb1 = min(nkb, kb0 + end - b);
+            int e, np;
+            if (kFew) {
+                e = __builtin_amdgcn_readlane(my_expert, a);
+                const uint64_t m = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_pairs, a) |
+                                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_pairs >> 32), a) << 32;
+                if (m >> lane & 1)
+                    list[wave][__popcll(m & ((1ull << lane) - 1))] = (uint16_t)lane;
+                __builtin_amdgcn_wave_barrier();
+                np = __popcll(m);
+            } else {
+                e = __builtin_amdgcn_readfirstlane(active[a]);
+                np = __builtin_amdgcn_readfirstlane(list_pairs(ids, pairs, e, lane, list[wave]));
+            }
+            // the part's number: this wave among those that have blocks of the expert
+            const int part = wave - ((a * nkb + 1) * waves - 1) / total;
+            float *to = res + part * pairs * 16 * NR;
+            int base = 0;
+            if (NT >= 2)
+                for (; np - base > 8; base += 16)
+                    down_tiles<NT < 2 ? NT : 2, NR, D>(p, e, n0, list[wave], base, np, kb0, kb1, to);
+            for (; base < np; base += 8)
+                down_tiles<1, NR, D>(p, e, n0, list[wave], base, np, kb0, kb1, to);
+            b += kb1 - kb0;
+        }
     }
     __syncthreads();
     for (int i = tid; i < p.T * 4 * NR; i += kDownThreads) {
         const int t = i / (4 * NR), c = (i - t * 4 * NR) * 4;
         v4f sum = {0.f, 0.f, 0.f, 0.f};
         for (int j = 0; j < p.top_k; ++j) {
-            const int pair = t * p.top_k + j;
-            if (ids[pair] < 0)
+            const int pair = t * p.top_k + j, a = active_of[pair];
+            if (a < 0)
                 continue;
-            for (int s = 0; s < slices; ++s)
+            const int parts = ((a + 1) * nkb * waves - 1) / total - ((a * nkb + 1) * waves - 1) / total + 1;
+            for (int s = 0; s < parts; ++s)
                 sum += *(const v4f *)(res + (s * pairs + pair) * 16 * NR + c);
         }
         const uint2 packed = dgk::pack_bf16x4(sum);

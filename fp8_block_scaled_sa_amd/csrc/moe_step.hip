@@ -100,7 +100,8 @@ int check_layer_sizes(int64_t T, int64_t top_k, int64_t E, int64_t H, int64_t I)
 {
     if (T < 0 || top_k <= 0 || E <= 0 || H <= 0 || I <= 0 || H % 128 || I % 128)
         return DG_ERR_BAD_SHAPE;
-    if (T > dge::kMaxTokens || top_k > dge::kMaxTopK || E > dge::kMaxExperts || H > (1 << 20) || I > (1 << 20))
+    if (T > dge::kMaxTokens || top_k > dge::kMaxTopK || E > dge::kMaxExperts ||
+        H > dge::kMaxWidth || I > dge::kMaxWidth)
         return DG_ERR_UNSUPPORTED;
     return DG_OK;
 }
@@ -112,21 +113,25 @@ int launch_layer(const dge::LayerParams &p, hipStream_t stream)
     const int pairs = p.T * p.top_k;
     const int by_pair = pairs < p.E;
     const dim3 grid((unsigned)((by_pair ? pairs : p.E) * (p.I / 16))), block(dge::kUpThreads);
-    if (p.T <= 16)
-        hipLaunchKernelGGL((dge::gate_up_kernel<1, 2>), grid, block, 0, stream, p, by_pair);
+    const bool few = pairs <= 64;
+    if (p.T <= 16 && few)
+        hipLaunchKernelGGL((dge::gate_up_kernel<1, 2, true>), grid, block, 0, stream, p, by_pair);
+    else if (p.T <= 16)
+        hipLaunchKernelGGL((dge::gate_up_kernel<1, 2, false>), grid, block, 0, stream, p, by_pair);
     else if (p.T <= 32)
-        hipLaunchKernelGGL((dge::gate_up_kernel<2, 2>), grid, block, 0, stream, p, by_pair);
+        hipLaunchKernelGGL((dge::gate_up_kernel<2, 2, false>), grid, block, 0, stream, p, by_pair);
     else
-        hipLaunchKernelGGL((dge::gate_up_kernel<4, 1>), grid, block, 0, stream, p, by_pair);
+        hipLaunchKernelGGL((dge::gate_up_kernel<4, 1, false>), grid, block, 0, stream, p, by_pair);
     const int st = launched();
     if (st != DG_OK)
         return st;
-    if (pairs <= 64)
-        hipLaunchKernelGGL((dge::down_kernel<1, 64, 4096>), dim3(p.H / 16), dim3(dge::kDownThreads), 0, stream, p);
+    const dim3 threads(dge::kDownThreads);
+    if (few)
+        hipLaunchKernelGGL((dge::down_kernel<1, 64, 4096, 1, 3>), dim3(p.H / 16), threads, 0, stream, p);
     else if (pairs <= 512)
-        hipLaunchKernelGGL((dge::down_kernel<2, 512, 16384>), dim3(p.H / 32), dim3(dge::kDownThreads), 0, stream, p);
+        hipLaunchKernelGGL((dge::down_kernel<2, 512, 32768, 2, 3>), dim3(p.H / 32), threads, 0, stream, p);
     else
-        hipLaunchKernelGGL((dge::down_kernel<1, 1024, 16384>), dim3(p.H / 16), dim3(dge::kDownThreads), 0, stream, p);
+        hipLaunchKernelGGL((dge::down_kernel<1, 1024, 32768, 2, 3>), dim3(p.H / 16), threads, 0, stream, p);
     return launched();
 }
 
@@ -262,8 +267,8 @@ dg_status dg_fp8_moe_layer(const void *X, int64_t ldx, const float *sX, int64_t 
     if (ldx < H || ld13 < H || ld2 < I || ldo < H || sx_stride_m < 0 || sx_stride_kb < 0 || s13_stride_e < 0 ||
         s13_stride_nb < 0 || s13_stride_kb < 0 || s2_stride_e < 0 || s2_stride_nb < 0 || s2_stride_kb < 0)
         return DG_ERR_BAD_STRIDE;
-    if (!strides_fit({ldx, ld13, ld2, ldo, sx_stride_m, sx_stride_kb, s13_stride_nb, s13_stride_kb, s2_stride_nb,
-                      s2_stride_kb}))
+    if (!strides_fit({sx_stride_kb, s13_stride_nb, s13_stride_kb, s2_stride_nb, s2_stride_kb}) ||
+        std::max({ldx, ld13, ld2, ldo}) > dge::kMaxRowStride || sx_stride_m > dge::kMaxTokenScaleStride)
         return DG_ERR_UNSUPPORTED;
     const int64_t last13 = (2 * I - 1) * ld13 + H - 1, last2 = (H - 1) * ld2 + I - 1;
     const int64_t last_s13 = (2 * I / 128 - 1) * s13_stride_nb + (H / 128 - 1) * s13_stride_kb;

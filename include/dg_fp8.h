@@ -559,10 +559,12 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
  * once per 64 of its tokens. Deterministic: fixed orders of summation.
  * For more tokens: the contiguous grouped calls.
  * Constraints: H % 128 == 0, I % 128 == 0; T <= 64, 1 <= top_k <= 16,
- * 1 <= E <= 1024, H and I at most 2^20 (DG_ERR_UNSUPPORTED above); bases,
+ * 1 <= E <= 1024, H and I at most 2^18 (DG_ERR_UNSUPPORTED above); bases,
  * ldx, ld13, ld2 and the expert strides as in the grouped calls (16-byte
- * multiples), ldo a multiple of 8; row and scale strides at most 2^28. out and
- * workspace lie apart from each other and from the inputs. T = 0 returns DG_OK.
+ * multiples), ldo a multiple of 8; row strides at most 2^25, sx_stride_m 2^22,
+ * other scale strides 2^28, expert strides 2^50 (DG_ERR_UNSUPPORTED above). out
+ * and workspace lie apart from each other and from the inputs. T = 0 returns
+ * DG_OK.
  */
 dg_status dg_fp8_moe_layer(const void *X, int64_t ldx,
                            const float *sX, int64_t sx_stride_m, int64_t sx_stride_kb,

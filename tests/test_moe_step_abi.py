@@ -73,11 +73,15 @@ def test_gate_accepted_and_empty():
         assert gate(**kw) in GOT_TO_THE_DEVICE
 
 
+def ws_bytes(T, k, H, I):  # noqa: E741
+    return _lib.load().dg_fp8_moe_layer_workspace_bytes(T, k, H, I)
+
+
 def layer(**kw):
     E, H, I = 4, 512, 256  # noqa: E741
     args = dict(X=X, ldx=H, sX=S, sx_m=1, sx_kb=8, W13=W, ld13=H, w13_e=2 * I * H, s13=Y, s13_e=16, s13_nb=4, s13_kb=1,
                 W2=W2, ld2=I, w2_e=H * I, s2=S2, s2_e=8, s2_nb=2, s2_kb=1, ids=IDS, wts=WTS, out=OUT, ldo=H,
-                T=8, k=2, E=E, H=H, I=I, ws=WS, ws_bytes=8 * 2 * I * 4, stream=None)
+                T=8, k=2, E=E, H=H, I=I, ws=WS, ws_bytes=ws_bytes(8, 2, H, I), stream=None)
     args.update(kw)
     return _lib.load().dg_fp8_moe_layer(*args.values())
 
@@ -86,8 +90,9 @@ def layer(**kw):
     (dict(T=-1), SHAPE), (dict(k=0), SHAPE), (dict(E=0), SHAPE), (dict(H=500), SHAPE), (dict(I=200), SHAPE),
     (dict(I=0), SHAPE),
     (dict(T=65), UNSUPPORTED), (dict(k=17), UNSUPPORTED), (dict(E=1025), UNSUPPORTED),
-    (dict(H=2 ** 20 + 128, ldx=2 ** 21, ld13=2 ** 21, ldo=2 ** 21), UNSUPPORTED),
-    (dict(ld13=2 ** 28 + 16, w13_e=2 ** 40), UNSUPPORTED), (dict(w2_e=2 ** 51), UNSUPPORTED),
+    (dict(H=2 ** 18 + 128, ldx=2 ** 21, ld13=2 ** 21, ldo=2 ** 21), UNSUPPORTED),
+    (dict(ld13=2 ** 25 + 16, w13_e=2 ** 40), UNSUPPORTED), (dict(sx_m=2 ** 22 + 1), UNSUPPORTED),
+    (dict(ldo=2 ** 25 + 8), UNSUPPORTED), (dict(w2_e=2 ** 51), UNSUPPORTED),
     (dict(sx_kb=2 ** 29), UNSUPPORTED),
 ] + [(dict([(n, None)]), NULL) for n in ("X", "sX", "W13", "s13", "W2", "s2", "ids", "wts", "out", "ws")] + [
     (dict(ldx=256), STRIDE), (dict(ld13=496), STRIDE), (dict(ld2=128), STRIDE), (dict(ldo=256), STRIDE),
@@ -97,7 +102,7 @@ def layer(**kw):
     (dict(out=OUT + 8), MISALIGNED), (dict(ws=WS + 8), MISALIGNED), (dict(sX=S + 2), MISALIGNED),
     (dict(ids=IDS + 2), MISALIGNED), (dict(wts=WTS + 2), MISALIGNED), (dict(ldx=520), MISALIGNED),
     (dict(ld13=520, w13_e=512 * 520), MISALIGNED), (dict(ldo=516), MISALIGNED), (dict(w2_e=512 * 256 + 8), MISALIGNED),
-    (dict(ws_bytes=8 * 2 * 256 * 4 - 1), SCRATCH), (dict(ws_bytes=0), SCRATCH), (dict(ws_bytes=-1), SCRATCH),
+    (dict(ws_bytes=ws_bytes(8, 2, 512, 256) - 1), SCRATCH), (dict(ws_bytes=0), SCRATCH), (dict(ws_bytes=-1), SCRATCH),
     (dict(out=X), ALIASING), (dict(out=W + 4096), ALIASING), (dict(out=IDS), ALIASING), (dict(ws=OUT), ALIASING),
     (dict(ws=X), ALIASING), (dict(ws=WTS - 4096), ALIASING), (dict(out=S2), ALIASING),
 ])
@@ -112,7 +117,7 @@ def test_layer_accepted_and_empty():
 
 
 def test_layer_workspace_bytes():
-    assert ops.dg_fp8_moe_layer_workspace_bytes(64, 8, 7168, 2048) == 64 * 8 * 2048 * 4
+    assert ops.dg_fp8_moe_layer_workspace_bytes(64, 8, 7168, 2048) >= 64 * 8 * 2048 * 4
     assert ops.dg_fp8_moe_layer_workspace_bytes(0, 8, 7168, 2048) == 0
     for bad, status in (((65, 8, 7168, 2048), UNSUPPORTED), ((1, 8, 7168, 200), SHAPE), ((-1, 1, 128, 128), SHAPE)):
         with pytest.raises(DGError) as e:
