@@ -6,7 +6,7 @@
 //   out_t = bf16( sum_j w_tj W2_e h )
 //
 // A few tokens leave the layer bound by the chosen experts' weights, which
-// have to come from HBM once: 3 H I bytes an expert. The two kernels stream
+// have to come from HBM once: 3 H I bytes an expert. Two kernels stream
 // them as operand A of the matrix instructions (16 rows of weights), with up
 // to 16 of the expert's tokens as operand B. Each weight row is read by one
 // workgroup only, for all of the expert's tokens.
@@ -36,6 +36,8 @@ constexpr int kMaxTokens = 64;
 constexpr int kMaxTopK = 16;
 constexpr int kMaxPairs = kMaxTokens * kMaxTopK;
 constexpr int kMaxExperts = 1024;
+constexpr int kDownWaves = 8;
+constexpr int kDownRows = 16 * kDownWaves;
 // The kernels keep a lane's offsets in 32 bits: 63 rows of X or 15 rows of
 // weights, and both parts of h for all pairs, stay below 2^31 bytes.
 constexpr int kMaxWidth = 1 << 18;                // H and I
@@ -60,6 +62,7 @@ struct LayerParams {
     uint16_t *out;          // bf16 [T, H]
     int64_t ldo;
     uint16_t *h;            // workspace: bf16 [hi, lo][pairs][I]
+    float *part;            // and fp32 [pairs][H], each pair's weighted product
     int T, top_k, E, H, I;
 };
 
@@ -104,12 +107,12 @@ __device__ __forceinline__ float from_lane_xor_8(float v)
 
 // The pairs (token * top_k + slot) of expert e, in ascending order, into list;
 // returns how many. One wave.
-template <typename Id>
-__device__ __forceinline__ int list_pairs(const Id *ids, int pairs, int e, int lane, uint16_t *list)
+__device__ __forceinline__ int list_pairs(const LayerParams &p, int e, int lane, uint16_t *list)
 {
+    const int pairs = p.T * p.top_k;
     int n = 0;
     for (int c = 0; c < pairs; c += 64) {
-        const bool hit = c + lane < pairs && ids[c + lane] == e;
+        const bool hit = c + lane < pairs && p.ids[c + lane] == e;
         const uint64_t m = __ballot(hit);
         if (hit)
             list[n + __popcll(m & ((1ull << lane) - 1))] = (uint16_t)(c + lane);
@@ -119,10 +122,34 @@ __device__ __forceinline__ int list_pairs(const Id *ids, int pairs, int e, int l
     return n;
 }
 
+// The expert of one slot of the grid, or -1: by_pair (fewer pairs than experts)
+// slot s has the expert of pair s, else slot s is expert s.
+__device__ __forceinline__ int slot_expert(const LayerParams &p, int by_pair, int slot)
+{
+    const int e = __builtin_amdgcn_readfirstlane(by_pair ? p.ids[slot] : slot);
+    return e >= 0 && e < p.E ? e : -1;
+}
+
 // ---------------------------------------------------------------- gate and up
 
 constexpr int kUpWaves = 4;
 constexpr int kUpThreads = 64 * kUpWaves;
+
+// Four consecutive values of h of one pair, from row on.
+__device__ __forceinline__ void store_h(const LayerParams &p, int pair, int row, const v4f &g, const v4f &u)
+{
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const float h = g[c] / (1.0f + __expf(-g[c])) * u[c];
+        hi[c] = dgk::bf16_rne(h);
+        lo[c] = dgk::bf16_rne(h - __uint_as_float(hi[c] << 16));
+    }
+    uint16_t *to = p.h + (int64_t)pair * p.I + row;
+    *(u32x2 *)to = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
+    to += (int64_t)p.T * p.top_k * p.I;
+    *(u32x2 *)to = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+}
 
 template <int NT>
 struct UpStage {
@@ -156,6 +183,7 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
         ag[i] = au[i] = v4f{0.f, 0.f, 0.f, 0.f};
 
     // This wave's K blocks: wave, wave + kUpWaves, ...; D of them in flight.
+    // Past the last one the last block of K is read again (a wave may have none).
     const int n = (nkb - wave + kUpWaves - 1) / kUpWaves;
     UpStage<NT> st[D];
     auto load = [&](int j, UpStage<NT> &s) {
@@ -214,45 +242,33 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
             u += red[(w * NT + i) * 2 + 1][lane];
         }
         const int at = base + 16 * i + (lane & 15);
-        if (at < np) {
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float h = g[c] / (1.0f + __expf(-g[c])) * u[c];
-                hi[c] = dgk::bf16_rne(h);
-                lo[c] = dgk::bf16_rne(h - __uint_as_float(hi[c] << 16));
-            }
-            uint16_t *to = p.h + (int64_t)list[at] * p.I + n0 + 4 * lg;
-            *(u32x2 *)to = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
-            to += (int64_t)p.T * p.top_k * p.I;
-            *(u32x2 *)to = u32x2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
-        }
+        if (at < np)
+            store_h(p, list[at], n0 + 4 * lg, g, u);
     }
 }
 
-// One workgroup per 16 columns of h of one expert. by_pair: slot s of the grid
-// is the expert of pair s, if no earlier pair has it (fewer pairs than
-// experts); else slot s is expert s. With up to 64 pairs every wave lists the
-// expert's pairs for itself.
+// One workgroup per 16 columns of h of one expert (a later pair with an
+// expert that an earlier one has leaves it to that one's slot). With up to 64
+// pairs every wave lists the expert's pairs for itself.
 template <int NT, int D, bool FEW>
 __global__ __launch_bounds__(kUpThreads) void gate_up_kernel(LayerParams p, int by_pair)
 {
     __shared__ uint16_t list[FEW ? 64 * kUpWaves : kMaxPairs];
     __shared__ int count;
     __shared__ v4f red[kUpWaves * NT * 2][64];
-    const int tiles = p.I >> 4, pairs = p.T * p.top_k;
+    const int tiles = p.I >> 4;
     const int slot = blockIdx.x / tiles, n0 = (blockIdx.x - slot * tiles) * 16;
-    const int e = __builtin_amdgcn_readfirstlane(by_pair ? p.ids[slot] : slot);
-    if (e < 0 || e >= p.E)
+    const int e = slot_expert(p, by_pair, slot);
+    if (e < 0)
         return;
     int np;
     uint16_t *mine = list;
     if (FEW) {
         mine = list + 64 * (threadIdx.x >> 6);
-        np = list_pairs(p.ids, pairs, e, threadIdx.x & 63, mine);
+        np = list_pairs(p, e, threadIdx.x & 63, mine);
     } else {
         if (threadIdx.x < 64) {
-            const int n = list_pairs(p.ids, pairs, e, threadIdx.x, list);
+            const int n = list_pairs(p, e, threadIdx.x, list);
             if (threadIdx.x == 0)
                 count = n;
         }
@@ -275,7 +291,6 @@ __global__ __launch_bounds__(kUpThreads) void gate_up_kernel(LayerParams p, int 
 
 // ---------------------------------------------------------------- down
 
-constexpr int kDownWaves = 8;
 constexpr int kDownThreads = 64 * kDownWaves;
 
 // 16 e4m3 codes as two operands of 8 bf16 numbers (exact).
@@ -295,226 +310,205 @@ __device__ __forceinline__ void to_bf16(const u32x4 &w, bf16x8 *out)
     }
 }
 
-template <int NT, int NR>
-struct DownStage {
-    u32x4 w[NR][2];         // 16 NR rows, 128 bytes of K
-    u32x4 h[NT][4];         // NT x 8 pairs, hi and lo: this lane's 32 of 128 values
-    float s;
-};
-
-// Pairs base .. base + 8 NT of expert e's list against rows n0 .. n0 + 16 NR
-// of W2, K blocks [kb0, kb1): res[pair][16 NR] = weight * product.
-template <int NT, int NR, int D>
-__device__ __forceinline__ void down_tiles(const LayerParams &p, int e, int n0, const uint16_t *list, int base, int np,
-                                           int kb0, int kb1, float *res)
+// LDS writes of all waves before, LDS reads after. Loads in flight stay in
+// flight, which __syncthreads would wait for.
+__device__ __forceinline__ void lds_barrier()
 {
-    const int lane = threadIdx.x & 63, lg = lane >> 4, col = lane & 15;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Pairs base .. base + 8 NT of expert e's list against this wave's 16 rows
+// of W2: part[pair][row] = weight * product.
+//
+// All waves read the same h, so it goes through LDS in chunks of KC blocks
+// of K, two buffers deep: the chunk after the present one is loaded to
+// registers before the present one's products and stored after them. (Read
+// from L2 by each wave, h took four loads beside the two of a block's weights,
+// and the load path became the bound.) A chunk's 16-byte units lie
+// [block][tile][unit][column], the column exchanged by the unit's number so
+// that neither the stores (a row's units) nor the reads (a unit's columns)
+// meet in a bank. Column c of a tile is the hi (c < 8) or lo part of pair c % 8.
+template <int NT, int KC>
+__device__ __forceinline__ void down_tiles(const LayerParams &p, int e, int n0, const uint16_t *list, int base, int np,
+                                           u32x4 *lds)
+{
+    constexpr int kUnits = KC * NT * 256;             // of 16 bytes, in one buffer
+    constexpr int kMine = kUnits / kDownThreads;
+    static_assert(kUnits % kDownThreads == 0, "");
+    const int tid = threadIdx.x, lane = tid & 63, lg = lane >> 4, col = lane & 15;
+    const int nkb = p.I >> 7, nch = (nkb + KC - 1) / KC;
+    const int turn = (int)(blockIdx.x % nch);
     const uint8_t *w = p.W2 + e * p.w2_e + n0 * p.ld2;
     const uint32_t row0 = block_offset(lane, p.ld2), row8 = row0 + 8 * (uint32_t)p.ld2;
     const float *sw = p.s2 + e * p.s2_e + (n0 >> 7) * p.s2_nb;
     const uint8_t *h = (const uint8_t *)p.h;
-    uint32_t ho[NT];
-    int pair[NT];
-    float weight[NT];
+    // This thread's units: n = 0, 1, ... are kRowStep rows (of columns) apart, unit and block are the same.
+    constexpr int kRowStep = kDownThreads / (KC * 16);
+    const int unit = tid % 16, hd = tid / 16 % KC, hrow = tid / (KC * 16);
+    uint32_t ho[kMine];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-        pair[i] = list[min(base + 8 * i + (col & 7), np - 1)];
-        weight[i] = p.weights[pair[i]];
-        // column col: the hi (col < 8) or lo part of pair col % 8
-        ho[i] = (uint32_t)(((col >> 3) * p.T * p.top_k + pair[i]) * p.I * 2 + 64 * lg);
+    for (int n = 0; n < kMine; ++n) {
+        const int row = hrow + n * kRowStep, c = row % 16;
+        const int pair = list[min(base + row / 16 * 8 + (c & 7), np - 1)];
+        ho[n] = (uint32_t)(((c >> 3) * p.T * p.top_k + pair) * p.I * 2 + 16 * unit);
     }
-    v4f acc[NT][NR];
+    v4f acc[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int r = 0; r < NR; ++r)
-            acc[i][r] = v4f{0.f, 0.f, 0.f, 0.f};
-    DownStage<NT, NR> st[D];
-    auto load = [&](int j, DownStage<NT, NR> &s) {
-        const int kb = min(j, kb1 - 1);
-        const int64_t k = (int64_t)kb * 128;
-#pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            s.w[r][0] = load16_once(w + 16 * r * p.ld2 + k, row0);
-            s.w[r][1] = load16_once(w + 16 * r * p.ld2 + k, row8);
-        }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                s.h[i][q] = load16(h + 2 * k + 16 * q, ho[i]);
-        s.s = sw[kb * p.s2_kb];
+        acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    u32x4 st[KC][2], hs[kMine];
+    float sc[KC];
+    // first block of the c-th chunk of this workgroup's order
+    auto chunk = [&](int c) {
+        c = min(c, nch - 1) + turn;
+        return (c >= nch ? c - nch : c) * KC;
     };
-    auto compute = [&](DownStage<NT, NR> &s) {
+    auto load_w = [&](int d, int kb0) {
+        const int kb = min(kb0 + d, nkb - 1);
+        st[d][0] = load16_once(w + (int64_t)kb * 128, row0);
+        st[d][1] = load16_once(w + (int64_t)kb * 128, row8);
+        sc[d] = sw[kb * p.s2_kb];
+    };
+    auto load_h = [&](int kb0) {
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            exchange_halves(s.w[r][0], s.w[r][1]);
-            bf16x8 wr[4];
-            to_bf16(s.w[r][0], wr);
-            to_bf16(s.w[r][1], wr + 2);
+        for (int n = 0; n < kMine; ++n)
+            hs[n] = load16(h, ho[n] + (uint32_t)min(kb0 + hd, nkb - 1) * 256);
+    };
+    auto store_h = [&](u32x4 *to) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                v4f part = {0.f, 0.f, 0.f, 0.f};
+        for (int n = 0; n < kMine; ++n) {
+            const int row = hrow + n * kRowStep;
+            to[((hd * NT + row / 16) * 16 + unit) * 16 + (row % 16 ^ unit)] = hs[n];
+        }
+    };
+    load_h(chunk(0));
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wr[q], __builtin_bit_cast(bf16x8, s.h[i][q]), part,
-                                                                   0, 0, 0);
-                acc[i][r] += part * s.s;
+    for (int d = 0; d < KC; ++d)
+        load_w(d, chunk(0));
+    lds_barrier();  // the previous pass's reads
+    store_h(lds);
+    lds_barrier();
+    for (int c = 0; c < nch; ++c) {
+        const u32x4 *from = lds + (c & 1) * kUnits;
+        const int kb0 = chunk(c), next = chunk(c + 1);
+        load_h(next);
+#pragma unroll
+        for (int d = 0; d < KC; ++d) {
+            if (kb0 + d < nkb) {
+                exchange_halves(st[d][0], st[d][1]);
+                bf16x8 wr[4];
+                to_bf16(st[d][0], wr);
+                to_bf16(st[d][1], wr + 2);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    v4f part = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int u = 4 * lg + q;
+                        const u32x4 b = from[((d * NT + i) * 16 + u) * 16 + (col ^ u)];
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wr[q], __builtin_bit_cast(bf16x8, b), part, 0,
+                                                                       0, 0);
+                    }
+                    acc[i] += part * sc[d];
+                }
             }
+            if (c + 1 < nch)
+                load_w(d, next);
         }
-    };
-#pragma unroll
-    for (int d = 0; d < D; ++d)
-        load(kb0 + d, st[d]);
-    for (int j = kb0; j < kb1; j += D) {
-#pragma unroll
-        for (int d = 0; d < D; ++d) {
-            if (j + d < kb1)
-                compute(st[d]);
-            load(j + d + D, st[d]);
-        }
+        store_h(lds + ((c + 1) & 1) * kUnits);
+        lds_barrier();
     }
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
+        v4f sum;
+        const int at = base + 8 * i + col;
+        const bool mine = col < 8 && at < np;
+        const int pair = list[min(at, np - 1)];
+        const float weight = p.weights[pair];
 #pragma unroll
-        for (int r = 0; r < NR; ++r) {
-            v4f sum;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                sum[c] = (acc[i][r][c] + from_lane_xor_8(acc[i][r][c])) * weight[i];
-            if (col < 8 && base + 8 * i + col < np)
-                *(v4f *)(res + pair[i] * 16 * NR + 16 * r + 4 * lg) = sum;
-        }
+        for (int c = 0; c < 4; ++c)
+            sum[c] = (acc[i][c] + from_lane_xor_8(acc[i][c])) * weight;
+        if (mine)
+            *(v4f *)(p.part + (int64_t)pair * p.H + n0 + 4 * lg) = sum;
     }
 }
 
-// One workgroup per 16 NR columns of out, for all chosen experts. Their K
-// blocks, one expert's after the other's, are dealt to the waves in equal
-// runs; each wave's part of an expert goes to a place of its own in LDS, and
-// the sum over a token's slots and an expert's parts runs in a fixed order.
-template <int NR, int PAIRS, int RES, int NT, int D>
-__global__ __launch_bounds__(kDownThreads) void down_kernel(LayerParams p)
+// One workgroup per 128 columns of out and expert, 16 columns a wave. Every
+// pair's product goes to the workspace.
+template <int NT, bool FEW>
+__global__ __launch_bounds__(kDownThreads, 4) void down_kernel(LayerParams p, int by_pair)
 {
-    constexpr bool kFew = PAIRS <= 64;
-    __shared__ float res[RES];                // [part][pair][16 NR]
-    __shared__ int16_t active_of[PAIRS];      // each pair's place in active, -1 without an expert
-    __shared__ uint16_t list[kDownWaves][PAIRS];
-    __shared__ int16_t ids[kFew ? 1 : PAIRS];
-    __shared__ int16_t active[kFew ? 1 : PAIRS];       // the chosen experts
-    __shared__ int first[kFew ? 1 : kMaxExperts];      // each expert's first pair
-    __shared__ int16_t place[kFew ? 1 : kMaxExperts];  // ... and its place in active
-    static_assert(RES >= 2 * PAIRS * 16 * NR, "an expert has two parts where the waves' runs cut it");
+    __shared__ u32x4 lds[NT >= 2 ? 4096 : 2048];
+    __shared__ uint16_t list[FEW ? 64 * kDownWaves : kMaxPairs];
     __shared__ int count;
-    const int pairs = p.T * p.top_k;
-    const int tid = threadIdx.x, lane = tid & 63;
+    const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16 * NR;
-
-    int nact = 0;
-    int my_expert = -1;                       // kFew: lane a's chosen expert a ...
-    uint64_t my_pairs = 0;                    // ... and the pairs that have it
-    if (kFew) {
-        int id = lane < pairs ? p.ids[lane] : -1;
-        if (id >= p.E)
-            id = -1;
-        int at = -1;
-        for (uint64_t left = __ballot(id >= 0); left; ++nact) {
-            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-            const uint64_t m = __ballot(id == e);
-            left &= ~m;
-            if (id == e)
-                at = nact;
-            if (lane == nact) {
-                my_expert = e;
-                my_pairs = m;
-            }
-        }
-        if (wave == 0 && lane < pairs)
-            active_of[lane] = (int16_t)at;
+    const int blocks = p.H / kDownRows;
+    const int slot = blockIdx.x / blocks, n0 = (blockIdx.x - slot * blocks) * kDownRows + 16 * wave;
+    const int e = slot_expert(p, by_pair, slot);
+    if (e < 0)
+        return;
+    int np;
+    uint16_t *mine = list;
+    if (FEW) {
+        mine = list + 64 * wave;
+        np = list_pairs(p, e, tid & 63, mine);
     } else {
-        for (int i = tid; i < p.E; i += kDownThreads)
-            first[i] = kMaxPairs;
-        __syncthreads();
-        for (int i = tid; i < pairs; i += kDownThreads) {
-            const int e = p.ids[i];
-            const bool in = e >= 0 && e < p.E;
-            ids[i] = (int16_t)(in ? e : -1);
-            if (in)
-                atomicMin(&first[e], i);
-        }
-        __syncthreads();
-        if (wave == 0) {
-            int n = 0;
-            for (int c = 0; c < pairs; c += 64) {
-                const int e = c + lane < pairs ? ids[c + lane] : -1;
-                const bool lead = e >= 0 && first[e] == c + lane;
-                const uint64_t m = __ballot(lead);
-                if (lead) {
-                    const int at = n + __popcll(m & ((1ull << lane) - 1));
-                    active[at] = (int16_t)e;
-                    place[e] = (int16_t)at;
-                }
-                n += __popcll(m);
-            }
-            if (lane == 0)
+        if (tid < 64) {
+            const int n = list_pairs(p, e, tid, list);
+            if (tid == 0)
                 count = n;
         }
         __syncthreads();
-        nact = count;
-        for (int i = tid; i < pairs; i += kDownThreads)
-            active_of[i] = ids[i] >= 0 ? place[ids[i]] : (int16_t)-1;
+        np = count;
     }
-    nact = __builtin_amdgcn_readfirstlane(nact);
+    np = __builtin_amdgcn_readfirstlane(np);
+    if (np == 0 || (by_pair && mine[0] != slot))
+        return;
+    int base = 0;
+    if (NT >= 4) {
+        for (; np - base > 24; base += 32)
+            down_tiles<4, 2>(p, e, n0, mine, base, np, lds);
+        for (; np - base > 16; base += 24)
+            down_tiles<3, 2>(p, e, n0, mine, base, np, lds);
+    }
+    if (NT >= 2)
+        for (; np - base > 8; base += 16)
+            down_tiles<2, 2>(p, e, n0, mine, base, np, lds);
+    for (; base < np; base += 8)
+        down_tiles<1, 4>(p, e, n0, mine, base, np, lds);
+}
 
-    // Waves in use: an expert's parts, (waves / nact rounded up) + 1 at most, have to fit res.
-    const int nkb = p.I >> 7, total = nact * nkb;
-    const int parts_cap = RES / (pairs * 16 * NR);
-    const int waves = max(1, min(min(kDownWaves, total), nact * (parts_cap - 1)));
-    if (wave < waves && nact > 0) {
-        int b = total * wave / waves;
-        const int end = total * (wave + 1) / waves;
-        while (b < end) {
-            const int a = b / nkb, kb0 = b - a * nkb, kb1 = min(nkb, kb0 + end - b);
-            int e, np;
-            if (kFew) {
-                e = __builtin_amdgcn_readlane(my_expert, a);
-                const uint64_t m = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)my_pairs, a) |
-                                   (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(my_pairs >> 32), a) << 32;
-                if (m >> lane & 1)
-                    list[wave][__popcll(m & ((1ull << lane) - 1))] = (uint16_t)lane;
-                __builtin_amdgcn_wave_barrier();
-                np = __popcll(m);
-            } else {
-                e = __builtin_amdgcn_readfirstlane(active[a]);
-                np = __builtin_amdgcn_readfirstlane(list_pairs(ids, pairs, e, lane, list[wave]));
-            }
-            // the part's number: this wave among those that have blocks of the expert
-            const int part = wave - ((a * nkb + 1) * waves - 1) / total;
-            float *to = res + part * pairs * 16 * NR;
-            int base = 0;
-            if (NT >= 2)
-                for (; np - base > 8; base += 16)
-                    down_tiles<NT < 2 ? NT : 2, NR, D>(p, e, n0, list[wave], base, np, kb0, kb1, to);
-            for (; base < np; base += 8)
-                down_tiles<1, NR, D>(p, e, n0, list[wave], base, np, kb0, kb1, to);
-            b += kb1 - kb0;
+// ---------------------------------------------------------------- sum over a token's slots
+
+// Four columns of out a thread, the slots' products added in their order. A
+// slot without an expert has no product: what its place holds is not used.
+constexpr int kSumThreads = 256;
+
+__global__ __launch_bounds__(kSumThreads) void sum_slots_kernel(LayerParams p)
+{
+    const int t = blockIdx.y, at = (blockIdx.x * kSumThreads + threadIdx.x) * 4;
+    if (at >= p.H)
+        return;
+    const float *part = p.part + (int64_t)t * p.top_k * p.H + at;
+    v4f sum = {0.f, 0.f, 0.f, 0.f};
+    for (int j0 = 0; j0 < p.top_k; j0 += 4) {
+        v4f v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[j] = *(const v4f *)(part + (int64_t)min(j0 + j, p.top_k - 1) * p.H);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int id = p.ids[t * p.top_k + min(j0 + j, p.top_k - 1)];
+            if (j0 + j < p.top_k && id >= 0 && id < p.E)
+                sum += v[j];
         }
     }
-    __syncthreads();
-    for (int i = tid; i < p.T * 4 * NR; i += kDownThreads) {
-        const int t = i / (4 * NR), c = (i - t * 4 * NR) * 4;
-        v4f sum = {0.f, 0.f, 0.f, 0.f};
-        for (int j = 0; j < p.top_k; ++j) {
-            const int pair = t * p.top_k + j, a = active_of[pair];
-            if (a < 0)
-                continue;
-            const int parts = ((a + 1) * nkb * waves - 1) / total - ((a * nkb + 1) * waves - 1) / total + 1;
-            for (int s = 0; s < parts; ++s)
-                sum += *(const v4f *)(res + (s * pairs + pair) * 16 * NR + c);
-        }
-        const uint2 packed = dgk::pack_bf16x4(sum);
-        *(u32x2 *)(p.out + t * p.ldo + n0 + c) = u32x2{packed.x, packed.y};
-    }
+    const uint2 packed = dgk::pack_bf16x4(sum);
+    *(u32x2 *)(p.out + t * p.ldo + at) = u32x2{packed.x, packed.y};
 }
 
 }  // namespace dge

@@ -106,7 +106,8 @@ int check_layer_sizes(int64_t T, int64_t top_k, int64_t E, int64_t H, int64_t I)
     return DG_OK;
 }
 
-int64_t layer_bytes(int64_t T, int64_t top_k, int64_t I) { return T * top_k * I * 4; }
+// Both bf16 parts of h, and the pairs' products.
+int64_t layer_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I) { return T * top_k * (4 * I + 4 * H); }
 
 int launch_layer(const dge::LayerParams &p, hipStream_t stream)
 {
@@ -122,16 +123,22 @@ int launch_layer(const dge::LayerParams &p, hipStream_t stream)
         hipLaunchKernelGGL((dge::gate_up_kernel<2, 2, false>), grid, block, 0, stream, p, by_pair);
     else
         hipLaunchKernelGGL((dge::gate_up_kernel<4, 1, false>), grid, block, 0, stream, p, by_pair);
-    const int st = launched();
+    int st = launched();
     if (st != DG_OK)
         return st;
-    const dim3 threads(dge::kDownThreads);
-    if (few)
-        hipLaunchKernelGGL((dge::down_kernel<1, 64, 4096, 1, 3>), dim3(p.H / 16), threads, 0, stream, p);
-    else if (pairs <= 512)
-        hipLaunchKernelGGL((dge::down_kernel<2, 512, 32768, 2, 3>), dim3(p.H / 32), threads, 0, stream, p);
+    const dim3 dgrid((unsigned)((by_pair ? pairs : p.E) * (p.H / dge::kDownRows))), threads(dge::kDownThreads);
+    if (p.T <= 8 && few)
+        hipLaunchKernelGGL((dge::down_kernel<1, true>), dgrid, threads, 0, stream, p, by_pair);
+    else if (few)
+        hipLaunchKernelGGL((dge::down_kernel<2, true>), dgrid, threads, 0, stream, p, by_pair);
+    else if (p.T <= 16)
+        hipLaunchKernelGGL((dge::down_kernel<2, false>), dgrid, threads, 0, stream, p, by_pair);
     else
-        hipLaunchKernelGGL((dge::down_kernel<1, 1024, 32768, 2, 3>), dim3(p.H / 16), threads, 0, stream, p);
+        hipLaunchKernelGGL((dge::down_kernel<4, false>), dgrid, threads, 0, stream, p, by_pair);
+    if ((st = launched()) != DG_OK)
+        return st;
+    hipLaunchKernelGGL(dge::sum_slots_kernel, dim3((p.H / 4 + dge::kSumThreads - 1) / dge::kSumThreads, p.T),
+                       dim3(dge::kSumThreads), 0, stream, p);
     return launched();
 }
 
@@ -246,7 +253,7 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl, int sco
 int64_t dg_fp8_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I)
 {
     const int st = check_layer_sizes(T, top_k, 1, H, I);
-    return st == DG_OK ? layer_bytes(T, top_k, I) : -st;
+    return st == DG_OK ? layer_bytes(T, top_k, H, I) : -st;
 }
 
 dg_status dg_fp8_moe_layer(const void *X, int64_t ldx, const float *sX, int64_t sx_stride_m, int64_t sx_stride_kb,
@@ -284,7 +291,7 @@ dg_status dg_fp8_moe_layer(const void *X, int64_t ldx, const float *sX, int64_t 
         !aligned(topk_weights, 4) || ldx % 16 || ld13 % 16 || ld2 % 16 || ldo % 8 ||
         (E > 1 && (w13_stride_e % 16 || w2_stride_e % 16)))
         return DG_ERR_MISALIGNED;
-    if (workspace_bytes < layer_bytes(T, top_k, I))
+    if (workspace_bytes < layer_bytes(T, top_k, H, I))
         return DG_ERR_SCRATCH;
     const Extent ins[8] = {
         extent(X, 1, (T - 1) * ldx + H - 1),
@@ -309,6 +316,7 @@ dg_status dg_fp8_moe_layer(const void *X, int64_t ldx, const float *sX, int64_t 
     p.s2 = s2; p.s2_e = s2_stride_e; p.s2_nb = s2_stride_nb; p.s2_kb = s2_stride_kb;
     p.ids = topk_ids; p.weights = topk_weights; p.out = (uint16_t *)out; p.ldo = ldo;
     p.h = (uint16_t *)workspace;
+    p.part = (float *)workspace + T * top_k * I;
     p.T = (int)T; p.top_k = (int)top_k; p.E = (int)E; p.H = (int)H; p.I = (int)I;
     return (dg_status)launch_layer(p, (hipStream_t)stream);
 }

@@ -535,7 +535,7 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
 
 /*
  * A whole mixture-of-experts layer for a few tokens (T <= 64, one decode step
- * of a batch), in two launches: for every token t and its slots j with expert
+ * of a batch), in three launches: for every token t and its slots j with expert
  * e = topk_ids[t, j] in [0, E)
  *   [g; u] = W13_e x_t      h = g / (1 + exp(-g)) * u
  *   out_t  = bf16( sum_j topk_weights[t, j] * W2_e h )
@@ -577,8 +577,9 @@ dg_status dg_fp8_moe_layer(const void *X, int64_t ldx,
                            int64_t T, int64_t top_k, int64_t E, int64_t H, int64_t I,
                            void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Workspace bytes of dg_fp8_moe_layer for these sizes (T * top_k * I * 4); a
- * negative value is -dg_status (bad or unsupported sizes). Needs no device. */
+/* Workspace bytes of dg_fp8_moe_layer for these sizes (4 * T * top_k *
+ * (H + I)); a negative value is -dg_status (bad or unsupported sizes). Needs no
+ * device. */
 int64_t dg_fp8_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I);
 
 #ifdef __cplusplus

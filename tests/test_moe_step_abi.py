@@ -117,7 +117,7 @@ def test_layer_accepted_and_empty():
 
 
 def test_layer_workspace_bytes():
-    assert ops.dg_fp8_moe_layer_workspace_bytes(64, 8, 7168, 2048) >= 64 * 8 * 2048 * 4
+    assert ops.dg_fp8_moe_layer_workspace_bytes(64, 8, 7168, 2048) >= 64 * 8 * (7168 + 2048) * 4
     assert ops.dg_fp8_moe_layer_workspace_bytes(0, 8, 7168, 2048) == 0
     for bad, status in (((65, 8, 7168, 2048), UNSUPPORTED), ((1, 8, 7168, 200), SHAPE), ((-1, 1, 128, 128), SHAPE)):
         with pytest.raises(DGError) as e:
