@@ -47,7 +47,8 @@ def _scales(t: torch.Tensor, name: str, ndim: int) -> torch.Tensor:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle, without building a Stream object for it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -463,13 +464,38 @@ def dg_fp8_grouped_gemm_masked_fmt(a, sa, b, sb, masked_m, a_fmt="e4m3", b_fmt="
     return d
 
 
+# The calls below are made for single tokens too, where the host's time counts:
+# each tensor's shape and strides are fetched once, outputs come from the
+# cheapest of torch's allocating calls (norm 22 -> 12 us of host time, router
+# 9 -> 6, layer 18 -> 12), and the tensors made here are not checked again.
+CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
 def _rows(t, name, dtypes):
-    """Checks a 2-D row-contiguous tensor; returns its row stride (a single row's own stride is free in torch)."""
+    """Row stride and shape of a 2-D tensor with contiguous rows (a single row's own stride is free in torch)."""
     if t.dtype not in dtypes:
         raise TypeError("%s must be %s" % (name, " or ".join(str(d).replace("torch.", "") for d in dtypes)))
-    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         raise ValueError("%s must be 2-D with contiguous rows" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return stride[0] if shape[0] > 1 else shape[1], shape
+
+
+def _like(t, name, dtype, shape):
+    """Row stride of a tensor that has to have this type and shape."""
+    ld, got = _rows(t, name, (dtype,))
+    if got != shape:
+        raise ValueError("shape mismatch: %s" % name)
+    return ld
+
+
+def _scale_table(t, name, shape):
+    """Strides of a float32 scale table that has to have this shape."""
+    if t.dtype != torch.float32:
+        raise TypeError("%s must be float32" % name)
+    if t.shape != shape:
+        raise ValueError("scale shape mismatch: %s must be %s" % (name, list(shape)))
+    return t.stride()
 
 
 def dg_fp8_rmsnorm_quantize_1x128(x, weight, eps=1e-6, residual=None, residual_out=None, normed=False, y=None,
@@ -480,40 +506,49 @@ def dg_fp8_rmsnorm_quantize_1x128(x, weight, eps=1e-6, residual=None, residual_o
     given; the residual itself updates it in place). normed=True (or a given y)
     also returns the normed rows in bfloat16. A new S is M-major. Returns
     (q, s, residual_out, y), None for what was not asked for."""
-    ldx = _rows(x, "x", DTYPES)
-    M, K = x.shape
-    if weight.dtype not in DTYPES or tuple(weight.shape) != (K,) or weight.stride(0) != 1:
+    ldx, shape = _rows(x, "x", DTYPES)
+    M, K = shape
+    ldr = ldro = ldy = ldq = K
+    s_m, s_kb = 1, M
+    r_dtype = 0
+    rp = rop = yp = None
+    if weight.dtype not in DTYPES or weight.shape != shape[1:] or weight.stride(0) != 1:
         raise ValueError("weight must be a contiguous float32 or bfloat16 [K] tensor")
-    ldr = ldro = ldy = r_dtype = 0
     if residual is not None:
-        ldr, r_dtype = _rows(residual, "residual", DTYPES), DTYPES[residual.dtype]
-        if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=residual.dtype, device=x.device)
-        ldro = _rows(residual_out, "residual_out", (residual.dtype,))
-        if residual.shape != x.shape or residual_out.shape != x.shape:
-            raise ValueError("shape mismatch")
+        ldr, r_shape = _rows(residual, "residual", DTYPES)
+        if r_shape != shape:
+            raise ValueError("shape mismatch: residual")
+        r_dtype = DTYPES[residual.dtype]
+        if residual_out is not None:
+            ldro = _like(residual_out, "residual_out", residual.dtype, shape)
     elif residual_out is not None:
         raise ValueError("residual_out needs a residual")
-    if y is None and normed:
-        y = torch.empty((M, K), dtype=torch.bfloat16, device=x.device)
     if y is not None:
-        ldy = _rows(y, "y", (torch.bfloat16,))
-        if y.shape != x.shape:
-            raise ValueError("shape mismatch")
+        ldy = _like(y, "y", torch.bfloat16, shape)
+    if q is not None:
+        ldq, q_shape = _rows(q, "q", CODE_TYPES)
+        if q_shape != shape:
+            raise ValueError("shape mismatch: q")
+    if s is not None:
+        s_m, s_kb = _scale_table(s, "s", (M, K // BLOCK))
+    xp, wp = _dev(x, "x"), _dev(weight, "weight")
+    if residual is not None:
+        rp = _dev(residual, "residual")
+        if residual_out is None:
+            residual_out = torch.empty_like(residual, memory_format=torch.contiguous_format)
+        rop = _dev(residual_out, "residual_out")
+    if normed and y is None:
+        y = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+    if y is not None:
+        yp = _dev(y, "y")
     if q is None:
-        q = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+        q = torch.empty_like(x, dtype=torch.uint8, memory_format=torch.contiguous_format)
     if s is None:
-        s = torch.empty((K // BLOCK, M), dtype=torch.float32, device=x.device).t()
-    ldq = _rows(q, "q", (torch.uint8, torch.float8_e4m3fn))
-    _scales(s, "s", 2)
-    if q.shape != x.shape or tuple(s.shape) != (M, K // BLOCK):
-        raise ValueError("shape mismatch")
+        s = torch.empty_strided((M, K // BLOCK), (1, M), dtype=torch.float32, device=x.device)
+    qp, sp = _dev(q, "q"), _dev(s, "s")
     st = _lib.load().dg_fp8_rmsnorm_quantize_1x128(
-        _dev(x, "x"), DTYPES[x.dtype], ldx,
-        None if residual is None else _dev(residual, "residual"), r_dtype, ldr,
-        None if residual is None else _dev(residual_out, "residual_out"), ldro,
-        _dev(weight, "weight"), DTYPES[weight.dtype], eps, None if y is None else _dev(y, "y"), ldy,
-        _dev(q, "q"), ldq, _dev(s, "s"), s.stride(0), s.stride(1), M, K, _stream(stream))
+        xp, DTYPES[x.dtype], ldx, rp, r_dtype, ldr, rop, ldro, wp, DTYPES[weight.dtype], eps, yp, ldy, qp, ldq,
+        sp, s_m, s_kb, M, K, _stream(stream))
     _check(st, "dg_fp8_rmsnorm_quantize_1x128")
     return q, s, residual_out, y
 
@@ -521,8 +556,8 @@ def dg_fp8_rmsnorm_quantize_1x128(x, weight, eps=1e-6, residual=None, residual_o
 GATE_SCORES = {"softmax": 0, "sigmoid": 1}   # DG_GATE_SOFTMAX, DG_GATE_SIGMOID
 
 
-def _slots(t, name, dtype, T, top_k):
-    if t.dtype != dtype or tuple(t.shape) != (T, top_k) or not t.is_contiguous():
+def _slots(t, name, dtype, shape):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s [T, top_k] tensor" % (name, str(dtype).replace("torch.", "")))
     return _dev(t, name)
 
@@ -534,18 +569,18 @@ def dg_moe_gate_topk(logits, top_k, score="softmax", renormalize=True, factor=1.
     only -inf or NaN are left) and weights[T,top_k] (float32): softmax over the
     chosen experts (renormalize) or all of them, or sigmoid, divided by the
     chosen ones' sum if renormalize; times factor. Returns (ids, weights)."""
-    ldl = _rows(logits, "logits", DTYPES)
+    ldl, (T, E) = _rows(logits, "logits", DTYPES)
     if score not in GATE_SCORES:
         raise ValueError("score must be one of %s" % ", ".join(GATE_SCORES))
-    T, E = logits.shape
+    lp = _dev(logits, "logits")
+    slots = (T, top_k)
     if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=logits.device)
+        ids = torch.empty_strided(slots, (top_k, 1), dtype=torch.int32, device=logits.device)
     if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=logits.device)
-    st = _lib.load().dg_moe_gate_topk(
-        _dev(logits, "logits"), DTYPES[logits.dtype], ldl, GATE_SCORES[score], int(renormalize), factor,
-        _slots(ids, "ids", torch.int32, T, top_k), _slots(weights, "weights", torch.float32, T, top_k),
-        T, E, top_k, _stream(stream))
+        weights = torch.empty_strided(slots, (top_k, 1), dtype=torch.float32, device=logits.device)
+    ip, wp = _slots(ids, "ids", torch.int32, slots), _slots(weights, "weights", torch.float32, slots)
+    st = _lib.load().dg_moe_gate_topk(lp, DTYPES[logits.dtype], ldl, GATE_SCORES[score], int(renormalize), factor,
+                                      ip, wp, T, E, top_k, _stream(stream))
     _check(st, "dg_moe_gate_topk")
     return ids, weights
 
@@ -555,6 +590,15 @@ def dg_fp8_moe_layer_workspace_bytes(T: int, top_k: int, H: int, I: int) -> int:
     return _query(_lib.load().dg_fp8_moe_layer_workspace_bytes(T, top_k, H, I), "dg_fp8_moe_layer_workspace_bytes")
 
 
+def _expert_codes(t, name):
+    if t.dtype not in CODE_TYPES:
+        raise TypeError("%s must hold e4m3 codes (uint8 or float8_e4m3fn)" % name)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1:
+        raise ValueError("%s must be 3-D with a contiguous last dimension" % name)
+    return shape, stride
+
+
 def dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, topk_ids, topk_weights, workspace, out=None, stream=None):
     """A mixture-of-experts layer for up to 64 tokens: x[T,H] codes with scales
     sx[T,H/128], w13[E,2I,H] (gate rows, then up rows) with s13[E,2I/128,H/128],
@@ -562,32 +606,31 @@ def dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, topk_ids, topk_weights, workspace,
     slot skipped), topk_weights[T,top_k] float32 -> out[T,H] bfloat16 =
     sum_j weight_j W2_e (silu(gate) * up). workspace: a device tensor of at
     least dg_fp8_moe_layer_workspace_bytes(T, top_k, H, I) bytes."""
-    ldx = _rows(x, "x", (torch.uint8, torch.float8_e4m3fn))
-    _codes(w13, "w13", 3), _codes(w2, "w2", 3)
-    _scales(sx, "sx", 2), _scales(s13, "s13", 3), _scales(s2, "s2", 3)
-    T, H = x.shape
-    E, I2, _ = w13.shape
+    ldx, x_shape = _rows(x, "x", CODE_TYPES)
+    T, H = x_shape
+    (E, I2, H13), (w13_e, ld13, _) = _expert_codes(w13, "w13")
+    w2_shape, (w2_e, ld2, _) = _expert_codes(w2, "w2")
     I = I2 // 2  # noqa: E741
-    if I2 % 2 or w13.shape[2] != H or tuple(w2.shape) != (E, H, I):
+    if I2 % 2 or H13 != H or w2_shape != (E, H, I):
         raise ValueError("shape mismatch")
-    if (tuple(sx.shape) != (T, H // BLOCK) or tuple(s13.shape) != (E, I2 // BLOCK, H // BLOCK)
-            or tuple(s2.shape) != (E, H // BLOCK, I // BLOCK)):
-        raise ValueError("scale shape mismatch")
-    if topk_ids.dim() != 2:
+    sx_m, sx_kb = _scale_table(sx, "sx", (T, H // BLOCK))
+    s13_e, s13_nb, s13_kb = _scale_table(s13, "s13", (E, I2 // BLOCK, H // BLOCK))
+    s2_e, s2_nb, s2_kb = _scale_table(s2, "s2", (E, H // BLOCK, I // BLOCK))
+    slots = topk_ids.shape
+    if len(slots) != 2 or slots[0] != T:
         raise ValueError("topk_ids must be [T, top_k]")
-    top_k = topk_ids.shape[1]
+    xp, w13p, w2p = _dev(x, "x"), _dev(w13, "w13"), _dev(w2, "w2")
+    sxp, s13p, s2p = _dev(sx, "sx"), _dev(s13, "s13"), _dev(s2, "s2")
+    ip = _slots(topk_ids, "topk_ids", torch.int32, slots)
+    wp = _slots(topk_weights, "topk_weights", torch.float32, slots)
+    ldo = H
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    ldo = _rows(out, "out", (torch.bfloat16,))
-    if out.shape != x.shape:
-        raise ValueError("shape mismatch")
-    wp, wb = _ws(workspace)
+        out = torch.empty_like(x, dtype=torch.bfloat16, memory_format=torch.contiguous_format)
+    else:
+        ldo = _like(out, "out", torch.bfloat16, x_shape)
+    wsp, ws_bytes = _ws(workspace)
     st = _lib.load().dg_fp8_moe_layer(
-        _dev(x, "x"), ldx, _dev(sx, "sx"), sx.stride(0), sx.stride(1),
-        _dev(w13, "w13"), w13.stride(1), w13.stride(0), _dev(s13, "s13"), s13.stride(0), s13.stride(1), s13.stride(2),
-        _dev(w2, "w2"), w2.stride(1), w2.stride(0), _dev(s2, "s2"), s2.stride(0), s2.stride(1), s2.stride(2),
-        _slots(topk_ids, "topk_ids", torch.int32, T, top_k),
-        _slots(topk_weights, "topk_weights", torch.float32, T, top_k),
-        _dev(out, "out"), ldo, T, top_k, E, H, I, wp, wb, _stream(stream))
+        xp, ldx, sxp, sx_m, sx_kb, w13p, ld13, w13_e, s13p, s13_e, s13_nb, s13_kb, w2p, ld2, w2_e, s2p, s2_e, s2_nb,
+        s2_kb, ip, wp, _dev(out, "out"), ldo, T, slots[1], E, H, I, wsp, ws_bytes, _stream(stream))
     _check(st, "dg_fp8_moe_layer")
     return out

@@ -1,10 +1,15 @@
 """The serving step's operators (residual norm to codes, router top-k, expert
 layer) reject bad arguments on the host, through the C ABI and through the
 Python binding; none of these calls reaches a device."""
+import os
+import re
+
 import pytest
 import torch
 
 from fp8_block_scaled_sa_amd import DGError, _lib, ops
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "dg_fp8.h")
 
 OK, NULL, SHAPE, MISALIGNED, STRIDE, UNSUPPORTED, HIP, ALIASING, SCRATCH = range(9)
 GOT_TO_THE_DEVICE = (OK, UNSUPPORTED, HIP)
@@ -165,3 +170,86 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     for name in ("x", "w13", "sx"):
         with pytest.raises(TypeError):
             ops.dg_fp8_moe_layer(**{**good, name: good[name].double()})
+
+
+def parameters(name):
+    """Parameter names of an entry point, from the header."""
+    text = re.search(r"^dg_status %s\((.*?)\);" % name, open(HEADER).read(), re.M | re.S).group(1)
+    return [p.split()[-1].lstrip("*") for p in text.split(",")]
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """Calls of the binding on host tensors, as {parameter: argument} by the header's names."""
+    calls = []
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                names = parameters(name)
+                assert len(names) == len(args) == len(_lib.SIGNATURES[name][1])
+                calls.append(dict(zip(names, args)))
+                return OK
+            return call
+
+    monkeypatch.setattr(_lib, "_lib", Library())
+    monkeypatch.setattr(ops, "_dev", lambda t, name: t.data_ptr())
+    return calls
+
+
+def test_norm_binding_passes_every_argument_by_its_name(recorded):
+    M, K = 3, 512
+    x = torch.zeros((M, K + 8), dtype=torch.bfloat16)[:, :K]
+    r, w = torch.zeros((M, K + 4))[:, :K], torch.ones(K, dtype=torch.bfloat16)
+    q, s, ro, y = ops.dg_fp8_rmsnorm_quantize_1x128(x, w, 0.25, residual=r, normed=True, stream=77)
+    assert recorded.pop() == dict(
+        X=x.data_ptr(), x_dtype=1, ldx=K + 8, R=r.data_ptr(), r_dtype=0, ldr=K + 4, R_out=ro.data_ptr(), ldro=K,
+        W=w.data_ptr(), w_dtype=1, eps=0.25, Y=y.data_ptr(), ldy=K, Q=q.data_ptr(), ldq=K, S=s.data_ptr(),
+        s_stride_m=1, s_stride_kb=M, M=M, K=K, stream=77)
+    assert [(t.dtype, tuple(t.shape), t.stride()) for t in (q, s, ro, y)] == [
+        (torch.uint8, (M, K), (K, 1)), (torch.float32, (M, 4), (1, M)), (torch.float32, (M, K), (K, 1)),
+        (torch.bfloat16, (M, K), (K, 1))]
+    given = dict(q=torch.zeros((M, K + 16), dtype=torch.uint8)[:, :K], s=torch.zeros((M, 6))[:, :4],
+                 y=torch.zeros((M, K + 24), dtype=torch.bfloat16)[:, :K])
+    out = ops.dg_fp8_rmsnorm_quantize_1x128(x, w, residual=r, residual_out=r, stream=1, **given)
+    assert out[0] is given["q"] and out[1] is given["s"] and out[2] is r and out[3] is given["y"]
+    c = recorded.pop()
+    assert (c["ldq"], c["s_stride_m"], c["s_stride_kb"], c["ldy"], c["ldro"], c["R_out"]) == (
+        K + 16, 6, 1, K + 24, K + 4, r.data_ptr())
+    assert ops.dg_fp8_rmsnorm_quantize_1x128(x, w, stream=1)[2:] == (None, None)
+    c = recorded.pop()
+    assert c["R"] is None and c["R_out"] is None and c["Y"] is None
+    # a single row's stride means nothing in torch
+    ops.dg_fp8_rmsnorm_quantize_1x128(torch.zeros((K, 1), dtype=torch.bfloat16).t(), w, stream=1)
+    assert recorded.pop()["ldx"] == K
+
+
+def test_gate_binding_passes_every_argument_by_its_name(recorded):
+    logits = torch.zeros((5, 40))[:, :32]
+    ids, weights = ops.dg_moe_gate_topk(logits, 4, score="sigmoid", renormalize=False, factor=2.5, stream=3)
+    assert recorded.pop() == dict(logits=logits.data_ptr(), l_dtype=0, ldl=40, score=1, renormalize=0, factor=2.5,
+                                  ids=ids.data_ptr(), weights=weights.data_ptr(), T=5, E=32, top_k=4, stream=3)
+    assert ids.dtype == torch.int32 and weights.dtype == torch.float32
+    assert tuple(ids.shape) == tuple(weights.shape) == (5, 4) and ids.is_contiguous() and weights.is_contiguous()
+
+
+def test_layer_binding_passes_every_argument_by_its_name(recorded, monkeypatch):
+    monkeypatch.setattr(ops, "_ws", lambda w: (w.data_ptr(), w.numel()))
+    T, k, E, H, I = 3, 2, 4, 256, 384  # noqa: E741
+    code = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
+    x, sx = code(T, H + 16)[:, :H], torch.zeros((2, T)).t()
+    w13, s13 = code(E, 2 * I + 1, H + 32)[:, :2 * I, :H], torch.zeros((E, 7, 2))[:, :6]
+    w2, s2 = code(E, H + 2, I + 48)[:, :H, :I], torch.zeros((E, 3, 2)).transpose(1, 2)
+    ids, weights, ws = torch.zeros((T, k), dtype=torch.int32), torch.zeros((T, k)), code(100)
+    out = ops.dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, ids, weights, ws, stream=9)
+    assert recorded.pop() == dict(
+        X=x.data_ptr(), ldx=H + 16, sX=sx.data_ptr(), sx_stride_m=1, sx_stride_kb=T,
+        W13=w13.data_ptr(), ld13=H + 32, w13_stride_e=(2 * I + 1) * (H + 32), s13=s13.data_ptr(), s13_stride_e=14,
+        s13_stride_nb=2, s13_stride_kb=1, W2=w2.data_ptr(), ld2=I + 48, w2_stride_e=(H + 2) * (I + 48),
+        s2=s2.data_ptr(), s2_stride_e=6, s2_stride_nb=1, s2_stride_kb=2, topk_ids=ids.data_ptr(),
+        topk_weights=weights.data_ptr(), out=out.data_ptr(), ldo=H, T=T, top_k=k, E=E, H=H, I=I,
+        workspace=ws.data_ptr(), workspace_bytes=100, stream=9)
+    assert out.dtype == torch.bfloat16 and tuple(out.shape) == (T, H) and out.is_contiguous()
+    wide = torch.zeros((T, H + 8), dtype=torch.bfloat16)[:, :H]
+    assert ops.dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, ids, weights, ws, out=wide, stream=9) is wide
+    assert recorded.pop()["ldo"] == H + 8
