@@ -85,3 +85,15 @@ def load() -> ctypes.CDLL:
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+def address(name: str) -> int:
+    """Address of an entry point of the loaded library, for the compiled binding."""
+    lib = load()
+    try:
+        return lib._addresses[name]
+    except AttributeError:
+        lib._addresses = {}
+    except KeyError:
+        pass
+    return lib._addresses.setdefault(name, ctypes.cast(getattr(lib, name), ctypes.c_void_p).value)

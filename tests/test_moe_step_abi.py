@@ -1,8 +1,10 @@
 """The serving step's operators (residual norm to codes, router top-k, expert
 layer) reject bad arguments on the host, through the C ABI and through the
 Python binding; none of these calls reaches a device."""
+import ctypes
 import os
 import re
+import sys
 
 import pytest
 import torch
@@ -182,19 +184,26 @@ def parameters(name):
 def recorded(monkeypatch):
     """Calls of the binding on host tensors, as {parameter: argument} by the header's names."""
     calls = []
+    kept = []
+
+    def entry(name):
+        names = parameters(name)
+        res, types = _lib.SIGNATURES[name]
+        assert len(names) == len(types)
+
+        def call(*args):
+            calls.append(dict(zip(names, args)))
+            return OK
+        kept.append(ctypes.CFUNCTYPE(res, *types)(call))
+        return ctypes.cast(kept[-1], ctypes.c_void_p).value
 
     class Library:
-        def __getattr__(self, name):
-            def call(*args):
-                names = parameters(name)
-                assert len(names) == len(args) == len(_lib.SIGNATURES[name][1])
-                calls.append(dict(zip(names, args)))
-                return OK
-            return call
+        _addresses = {n: entry(n) for n in ("dg_fp8_rmsnorm_quantize_1x128", "dg_moe_gate_topk", "dg_fp8_moe_layer")}
 
     monkeypatch.setattr(_lib, "_lib", Library())
-    monkeypatch.setattr(ops, "_dev", lambda t, name: t.data_ptr())
-    return calls
+    ops._binding().any_device(True)
+    yield calls
+    ops._binding().any_device(False)
 
 
 def test_norm_binding_passes_every_argument_by_its_name(recorded):
@@ -233,8 +242,7 @@ def test_gate_binding_passes_every_argument_by_its_name(recorded):
     assert tuple(ids.shape) == tuple(weights.shape) == (5, 4) and ids.is_contiguous() and weights.is_contiguous()
 
 
-def test_layer_binding_passes_every_argument_by_its_name(recorded, monkeypatch):
-    monkeypatch.setattr(ops, "_ws", lambda w: (w.data_ptr(), w.numel()))
+def test_layer_binding_passes_every_argument_by_its_name(recorded):
     T, k, E, H, I = 3, 2, 4, 256, 384  # noqa: E741
     code = lambda *s: torch.zeros(s, dtype=torch.uint8)  # noqa: E731
     x, sx = code(T, H + 16)[:, :H], torch.zeros((2, T)).t()
@@ -253,3 +261,39 @@ def test_layer_binding_passes_every_argument_by_its_name(recorded, monkeypatch):
     wide = torch.zeros((T, H + 8), dtype=torch.bfloat16)[:, :H]
     assert ops.dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, ids, weights, ws, out=wide, stream=9) is wide
     assert recorded.pop()["ldo"] == H + 8
+
+
+def test_binding_raises_the_status(recorded, monkeypatch):
+    """Through the real entry point: a host pointer never gets past the argument checks here (K % 128)."""
+    monkeypatch.undo()
+    ops._binding().any_device(True)
+    with pytest.raises(DGError) as e:
+        ops.dg_fp8_rmsnorm_quantize_1x128(torch.zeros((2, 200)), torch.ones(200), s=torch.zeros((2, 1)))
+    assert e.value.status == SHAPE
+    with pytest.raises(DGError) as e:
+        ops.dg_moe_gate_topk(torch.zeros((2, 8)), 9)
+    assert e.value.status == SHAPE
+    with pytest.raises(DGError):
+        ops.dg_moe_gate_topk(torch.zeros((2, 8)), -1)
+
+
+def test_binding_refuses_what_is_no_tensor_or_number():
+    x, w = torch.zeros((2, 256)), torch.ones(256)
+    for call in (lambda: ops.dg_fp8_rmsnorm_quantize_1x128([1.0], w), lambda: ops.dg_moe_gate_topk(None, 2),
+                 lambda: ops.dg_fp8_rmsnorm_quantize_1x128(x, w, eps="a"), lambda: ops.dg_moe_gate_topk(x, "2"),
+                 lambda: ops.dg_fp8_moe_layer(*[None] * 9)):
+        with pytest.raises(TypeError):
+            call()
+
+
+def test_outputs_are_not_leaked(recorded):
+    """Reference counts of given and returned objects after many calls."""
+    x, w = torch.zeros((2, 256)), torch.ones(256)
+    q = torch.zeros((2, 256), dtype=torch.uint8)
+    before = sys.getrefcount(q), sys.getrefcount(x), sys.getrefcount(w)
+    for _ in range(50):
+        out = ops.dg_fp8_rmsnorm_quantize_1x128(x, w, q=q, stream=1)
+    count = sys.getrefcount(out[1])
+    assert count == 2       # the tuple's, and the argument's
+    del out
+    assert (sys.getrefcount(q), sys.getrefcount(x), sys.getrefcount(w)) == before
