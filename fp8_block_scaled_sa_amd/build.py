@@ -11,13 +11,10 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "dg_fp8.hip"), os.path.join(HERE, "csrc", "moe_step.hip")]
-DEPS = SOURCES + [os.path.join(HERE, "csrc", "kernels.hpp"), os.path.join(HERE, "csrc", "quant.hpp"),
-        os.path.join(HERE, "csrc", "moe.hpp"), os.path.join(HERE, "csrc", "mfma.hpp"),
-        os.path.join(HERE, "csrc", "host.hpp"),
-        os.path.join(HERE, "csrc", "norm.hpp"), os.path.join(HERE, "csrc", "gate.hpp"),
-        os.path.join(HERE, "csrc", "experts.hpp"),
-        os.path.join(ROOT, "include", "dg_fp8.h")]
+SOURCES = [os.path.join(HERE, "csrc", "library.hip")]
+DEPS = SOURCES + [os.path.join(HERE, "csrc", f) for f in (
+    "dg_fp8.hip", "kernels.hpp", "quant.hpp", "moe.hpp", "moe_step.hip", "norm.hpp", "gate.hpp", "experts.hpp")
+        ] + [os.path.join(ROOT, "include", "dg_fp8.h")]
 LIBRARY = os.path.join(HERE, "libdg_fp8.so")
 DEBUG_LIBRARY = os.path.join(HERE, "libdg_fp8_O1.so")
 BINDING_SOURCE = os.path.join(HERE, "csrc", "binding.cpp")

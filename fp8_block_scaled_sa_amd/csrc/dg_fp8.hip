@@ -14,14 +14,23 @@
 #include <string.h>
 
 #include "dg_fp8.h"
-#include "host.hpp"
 #include "kernels.hpp"
 #include "moe.hpp"
 #include "quant.hpp"
 
 namespace {
 
-using namespace dgh;
+thread_local int g_last_hip_error = 0;
+
+struct DeviceInfo {
+    bool known = false;
+    bool gfx950 = false;
+    int cus = 0;
+};
+
+constexpr int kMaxDevices = 64;
+DeviceInfo g_devices[kMaxDevices];
+std::mutex g_devices_mu;
 
 // Scratch memory of dg_fp8_gemm_nt_noalloc, for callers that cannot
 // allocate: a fixed array in the library's code object. Each GPU the library
@@ -67,6 +76,36 @@ uint8_t *device_scratch(int &status)
     return g_scratch_ptr[dev];
 }
 
+int fail_hip(hipError_t e)
+{
+    g_last_hip_error = (int)e;
+    return DG_ERR_HIP;
+}
+
+// Checks that the current device is gfx950 and caches its CU count.
+int current_device(DeviceInfo &out)
+{
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess)
+        return fail_hip(e);
+    if (dev < 0 || dev >= kMaxDevices)
+        return DG_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> lk(g_devices_mu);
+    DeviceInfo &d = g_devices[dev];
+    if (!d.known) {
+        hipDeviceProp_t prop;
+        e = hipGetDeviceProperties(&prop, dev);
+        if (e != hipSuccess)
+            return fail_hip(e);
+        d.gfx950 = strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+        d.cus = prop.multiProcessorCount;
+        d.known = true;
+    }
+    out = d;
+    return d.gfx950 ? DG_OK : DG_ERR_UNSUPPORTED;
+}
+
 // One call's launch context: the device's CU count, the caller's stream and
 // the caller's workspace. The library owns no device memory: every step that
 // can use scratch (split-K partial sums, segment offsets derived on the
@@ -101,6 +140,23 @@ size_t ws_round(size_t b) { return (b + kWsAlign - 1) / kWsAlign * kWsAlign; }
 
 // Most experts for which the contiguous call given only ids derives segment offsets.
 constexpr int64_t kDeriveMaxExperts = 128;
+
+bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// [lo, hi) byte extent of a strided 2-D/3-D operand (all strides >= 0).
+struct Extent {
+    uintptr_t lo, hi;
+};
+
+Extent extent(const void *p, int64_t elem, int64_t last_index)
+{
+    const uintptr_t lo = (uintptr_t)p;
+    return Extent{lo, lo + (uintptr_t)((last_index + 1) * elem)};
+}
+
+bool overlaps(Extent a, Extent b) { return a.lo < b.hi && b.lo < a.hi; }
+
+constexpr int64_t kInt32Max = 0x7fffffff;
 
 int check_common_shape(int64_t M, int64_t N, int64_t K)
 {
@@ -548,6 +604,23 @@ int quantize_impl(const void *X, int x_dtype, int64_t ldx, int64_t x_rows, const
         hipLaunchKernelGGL(dgq::quantize_1x128_kernel<false>, grid, block, 0, (hipStream_t)stream, p);
     const hipError_t e = hipGetLastError();
     return e == hipSuccess ? DG_OK : fail_hip(e);
+}
+
+// A caller workspace must be 16-byte aligned, have a non-negative size and
+// lie apart from the call's output and inputs.
+int check_workspace(const void *ws, int64_t ws_bytes, std::initializer_list<Extent> others)
+{
+    if (ws_bytes < 0)
+        return DG_ERR_BAD_SHAPE;
+    if (!ws || ws_bytes == 0)
+        return DG_OK;
+    if (!aligned(ws, 16))
+        return DG_ERR_MISALIGNED;
+    const Extent ew = extent(ws, 1, ws_bytes - 1);
+    for (const Extent &e : others)
+        if (e.hi > e.lo && overlaps(ew, e))
+            return DG_ERR_ALIASING;
+    return DG_OK;
 }
 
 // Validation and kernel arguments of a dense call. Returns DG_OK with `p`

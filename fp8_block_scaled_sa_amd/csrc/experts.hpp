@@ -19,7 +19,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "mfma.hpp"
+#include "kernels.hpp"
 
 namespace dge {
 

@@ -29,9 +29,10 @@
 
 #include <type_traits>
 
-#include "mfma.hpp"
-
 namespace dgk {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
 
 enum Layout { kDense = 0, kContiguous = 1, kMasked = 2 };
 
@@ -77,6 +78,15 @@ struct Params {
     const int32_t *gate;
 };
 
+// One e4m3 x e4m3 -> fp32 MFMA over a 16x16x128 block, C = 0 + A.B.
+// Format selectors 0/0 = OCP e4m3 for both operands; zero scale operands make
+// the compiler emit the plain (unscaled) v_mfma_f32_16x16x128_f8f6f4.
+__device__ __forceinline__ v4f mfma_e4m3_16x16x128(const v8i &a, const v8i &b)
+{
+    const v4f zero = {0.f, 0.f, 0.f, 0.f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
 // Operand formats of the tile kernel: bit 0 set = the GEMM's A holds e5m2,
 // bit 1 set = B holds e5m2 (else e4m3). The MFMA takes them as its format
 // selectors (0 = e4m3, 1 = e5m2): the first MFMA operand is fed from B, the
@@ -86,6 +96,24 @@ __device__ __forceinline__ v4f mfma_fmt_16x16x128(const v8i &b_rows, const v8i &
 {
     const v4f zero = {0.f, 0.f, 0.f, 0.f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b_rows, a_rows, zero, (F >> 1) & 1, F & 1, 0, 0, 0, 0);
+}
+
+// fp32 -> bf16 bits, round to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_rne(float f)
+{
+    uint32_t u = __float_as_uint(f);
+    if ((u & 0x7fffffffu) > 0x7f800000u)
+        return 0x7fc0u;
+    u += 0x7fffu + ((u >> 16) & 1u);
+    return u >> 16;
+}
+
+__device__ __forceinline__ uint2 pack_bf16x4(const v4f &v)
+{
+    uint2 r;
+    r.x = bf16_rne(v[0]) | (bf16_rne(v[1]) << 16);
+    r.y = bf16_rne(v[2]) | (bf16_rne(v[3]) << 16);
+    return r;
 }
 
 __device__ __forceinline__ v8i join(const uint4 &lo, const uint4 &hi)

@@ -2,7 +2,8 @@
 // mixture-of-experts serving step (declared in include/dg_fp8.h): the residual
 // norm to codes, the router's choice and the expert layer for a few tokens.
 // Host-side validation, kernel choice and launch; nothing is allocated and no
-// stream is synchronised.
+// stream is synchronised. Compiled behind dg_fp8.hip (library.hip), whose
+// device check, argument checks and error record it shares.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -12,12 +13,9 @@
 #include "dg_fp8.h"
 #include "experts.hpp"
 #include "gate.hpp"
-#include "host.hpp"
 #include "norm.hpp"
 
 namespace {
-
-using namespace dgh;
 
 // Strides up to this keep every byte offset below 2^62 (sizes are int32).
 constexpr int64_t kMaxStride = (int64_t)1 << 28;
