@@ -143,7 +143,8 @@ __device__ __forceinline__ void store_h(const LayerParams &p, int pair, int row,
     for (int c = 0; c < 4; ++c) {
         const float h = g[c] / (1.0f + __expf(-g[c])) * u[c];
         hi[c] = dgk::bf16_rne(h);
-        lo[c] = dgk::bf16_rne(h - __uint_as_float(hi[c] << 16));
+        const float rest = h - __uint_as_float(hi[c] << 16);
+        lo[c] = dgk::bf16_rne(rest == rest ? rest : 0.0f);  // an infinite h is its hi part alone
     }
     uint16_t *to = p.h + (int64_t)pair * p.I + row;
     *(u32x2 *)to = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};

@@ -433,6 +433,20 @@ def test_layer_skipped_slots_read_nothing(gpu_device):
         assert np.all((got[3] & 0x7FFF) > 0x7F80)
 
 
+def test_layer_infinite_h(gpu_device):
+    """g * u beyond fp32 is infinite, and so is what positive weights make of
+    it, not NaN; the other token is not touched."""
+    T, k, E, H, I = 2, 1, 1, 128, 128  # noqa: E741
+    one = torch.full((E, 2 * I, H), 0x38, dtype=torch.uint8)        # code of 1
+    x = torch.full((T, H), 0x38, dtype=torch.uint8)
+    sx = torch.tensor([[2.0 ** 70], [1.0]])
+    a = [t.cuda() for t in (x, sx, one, torch.ones((E, 2, 1)), one[:, :H, :I].contiguous(), torch.ones((E, 1, 1)),
+                            torch.zeros((T, k), dtype=torch.int32), torch.ones((T, k)))]
+    out = run_layer(a).float().cpu()
+    assert bool((out[0] == math.inf).all())
+    assert bool((out[1] == 128.0 ** 3).all())
+
+
 def test_layer_same_on_every_run_and_stream(gpu_device):
     a = make_layer(24, 4, 8, 512, 384, 51)
     want = bits(run_layer(a))
