@@ -6,14 +6,37 @@
 //   out_t = bf16( sum_j w_tj W2_e h )
 //
 // A few tokens leave the layer bound by the chosen experts' weights, which
-// have to come from HBM once: 3 H I bytes an expert. Two kernels stream
-// them as operand A of the matrix instructions (16 rows of weights), with up
-// to 16 of the expert's tokens as operand B. Each weight row is read by one
-// workgroup only, for all of the expert's tokens.
+// have to come from HBM once: 3 H I bytes an expert. Two kernels stream them as
+// operand A of the matrix instructions (16 rows of weights), with up to 16 of
+// the expert's tokens as operand B: each weight row is read by one workgroup
+// only, for all of the expert's tokens. A third, small one adds a token's slots.
+// Doing that in the second kernel, by the workgroup of a column block that
+// arrives last, took three times the second kernel's time: the device-wide
+// fences write back and drop what the XCDs' L2s hold.
+//
+// Lane order of the weight loads. The matrix instructions want lane l to hold
+// row l % 16 and the K bytes of group g = l / 16, 32 a lane. A load in that
+// order takes half of each 128-byte line and leaves the other half to the next
+// load, which costs a quarter of the bandwidth. So load p of a 16 x 128 byte
+// block reads the rows 8p + l % 8 and the 16 bytes 2g + l / 8 % 2 of the line
+// (whole lines: 6.6 to 7.2 TB/s in a kernel that only reads, against 4.9 for
+// 16 rows x 64 bytes, both non-temporal; 6.1 against 4.7 in the first kernel
+// for one token, 38.5 against 49.9 us), and the two registers' halves are then
+// exchanged between lanes l and l ^ 8, two DPP moves for each pair of dwords.
 //
 // h is kept as the sum of two bf16 numbers (its rounding to bf16, and the
 // rounding of what that leaves: 16 bits of mantissa), so that no rounding
-// comes between the products but the last one to bf16.
+// comes between the products but the last one to bf16. The second product
+// takes them as 8 + 8 columns of one operand and adds the two results.
+//
+// Measured for H 7168, I 2048, in graph replays under the kernel trace:
+//   1 token, 8 of 32 experts:    67 us (first kernel 38.5, second 22.7), 352 MB
+//   8 tokens, 8 of 32:          230 us (first kernel 137), 1268 MB
+//   64 tokens, 8 of 32:         345 us (first kernel 215 to 220), 1410 MB
+// With one tile of tokens the kernels run at 5 to 6 TB/s, near what a kernel
+// that only reads reaches; with more, they fall to 4 to 4.4 TB/s: in the first
+// the waves split K and each reads its own tokens' blocks from L2, two loads a
+// tile beside the four of the weights, in the second the chunks get shorter.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -249,8 +272,12 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
 }
 
 // One workgroup per 16 columns of h of one expert (a later pair with an
-// expert that an earlier one has leaves it to that one's slot). With up to 64
-// pairs every wave lists the expert's pairs for itself.
+// expert that an earlier one has leaves it to that one's slot), its waves
+// taking the K blocks in turn: for one token and 8 experts of I = 2048 that
+// makes 1024 workgroups, 16 waves a CU, each with D = 2 blocks of 32 rows (8 KB)
+// in flight. D = 3 changed nothing there (38.6 us) and cost a tenth where K is
+// short (19.6 against 22.9 us at H 2048). With up to 64 pairs every wave lists
+// the expert's pairs for itself, in one ballot and without a barrier.
 template <int NT, int D, bool FEW>
 __global__ __launch_bounds__(kUpThreads) void gate_up_kernel(LayerParams p, int by_pair)
 {
@@ -325,9 +352,10 @@ __device__ __forceinline__ void lds_barrier()
 //
 // All waves read the same h, so it goes through LDS in chunks of KC blocks
 // of K, two buffers deep: the chunk after the present one is loaded to
-// registers before the present one's products and stored after them. (Read
+// registers before the present one's products and stored after them. Read
 // from L2 by each wave, h took four loads beside the two of a block's weights,
-// and the load path became the bound.) A chunk's 16-byte units lie
+// and the load path became the bound: a copy of such a form without the h
+// loads ran 74 instead of 104 us (8 tokens, 8 of 32 experts). A chunk's 16-byte units lie
 // [block][tile][unit][column], the column exchanged by the unit's number so
 // that neither the stores (a row's units) nor the reads (a unit's columns)
 // meet in a bank. Column c of a tile is the hi (c < 8) or lo part of pair c % 8.
@@ -437,8 +465,12 @@ __device__ __forceinline__ void down_tiles(const LayerParams &p, int e, int n0, 
     }
 }
 
-// One workgroup per 128 columns of out and expert, 16 columns a wave. Every
-// pair's product goes to the workspace.
+// One workgroup per 128 columns of out and expert, 16 columns a wave: 448
+// workgroups of 8 waves for one token, 8 experts and H = 7168, two a CU (so at
+// most 128 registers). Every pair's product goes to the workspace: fp32, 4 H
+// bytes a pair, little beside an expert's weights. 22.7 us for one token against
+// 34.6 with one workgroup per 16 columns that went through all experts and
+// needed no sum after it; for 64 tokens the whole layer went from 481 to 345 us.
 template <int NT, bool FEW>
 __global__ __launch_bounds__(kDownThreads, 4) void down_kernel(LayerParams p, int by_pair)
 {

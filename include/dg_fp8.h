@@ -486,8 +486,10 @@ dg_status dg_moe_unpermute(const void *D, int64_t ldd, int64_t d_rows,
  *   W [K] fp32 or bf16 (w_dtype)
  *   Y [M, K] bf16, row stride ldy;  Q [M, K], row stride ldq;
  *   S logical [M, K/128] at S[m*s_stride_m + kb*s_stride_kb]
- * Non-finite inputs give what the formulas give in R_out and Y; the codes and
- * scales of that row are unspecified (no fault).
+ * mean(h^2) is formed in fp32: rows whose squares pass its range (values of
+ * about 2^63 and more) come out as zeros, and a row of zeros with eps = 0 as
+ * NaN. Non-finite inputs give what the formulas give in R_out and Y; the codes
+ * and scales of a row that is not finite in Y are unspecified (no fault).
  * Constraints: 0 < K <= 65536 (DG_ERR_UNSUPPORTED above), K % 128 == 0, eps >= 0;
  * X, R, R_out, W, Y, Q 16-byte aligned, row strides multiples of 16 bytes; S
  * 4-byte aligned; strides at most 2^28 elements (DG_ERR_UNSUPPORTED above);
@@ -555,8 +557,8 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
  * The ids and weights are read on the device: no synchronisation, safe to
  * capture, and they may change between replays. A block's products are summed
  * as in the grouped calls; h keeps 16 bits of mantissa; everything else is
- * fp32 up to the one rounding of out. Each chosen expert's weights are read
- * once per 64 of its tokens. Deterministic: fixed orders of summation.
+ * fp32 up to the one rounding of out. Of each chosen expert W13 is read once
+ * per 64 of its tokens, W2 once per 32. Deterministic: fixed orders of summation.
  * For more tokens: the contiguous grouped calls.
  * Constraints: H % 128 == 0, I % 128 == 0; T <= 64, 1 <= top_k <= 16,
  * 1 <= E <= 1024, H and I at most 2^18 (DG_ERR_UNSUPPORTED above); bases,

@@ -512,3 +512,22 @@ def test_step_in_a_graph(gpu_device):
 def test_guard_band_helper_sees_writes(gpu_device):
     out = sentinel_bf16((2, 128))
     assert guards_intact(out) and GUARD > 0
+
+
+def test_example_step(gpu_device):
+    """examples/moe_decode_step.py on a small block: the step is its own 64-bit form up to the output's rounding."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_decode_step.py")
+    spec = importlib.util.spec_from_file_location("moe_decode_step", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    block = example.MoeBlock(hidden=512, width=256, experts=8, top_k=3, max_tokens=20)
+    x, residual = normal((20, 512), 5).to(BF16).cuda(), normal((20, 512), 6).to(BF16).cuda()
+    exact = block.reference(x, residual)
+    total = (x.float() + residual.float()).to(BF16)
+    out = block.step(x, residual)
+    torch.cuda.synchronize()
+    assert torch.equal(residual, total)
+    # the norm of a sum of rounding errors of half a step each
+    assert float((out.double() - exact).norm()) <= half(BF16) * float(exact.norm())
