@@ -112,7 +112,12 @@ int64_t layer_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I) { return T *
 // Grid slots are pairs or experts, whichever are fewer. The kernels' tiles of
 // tokens follow T, the most tokens an expert can have (a token that names an
 // expert twice only makes it take another pass): fewer tiles, fewer registers,
-// more waves (gate_up: 98 registers for 16 tokens, 130 for 32, 140 for 64).
+// more waves (gate_up: 98 registers for 16 tokens, 130 for 32, 140 for 64). For
+// 64 tokens gate_up keeps one block of K in flight: two (208 registers) took
+// 220 instead of 215 us at 16 tokens an expert and 28 instead of 26 on a share
+// of the experts, but 89 instead of 99 where every expert has 64. The lists
+// without barriers for up to 64 pairs came with the whole-line loads and were
+// not timed apart from them.
 int launch_layer(const dge::LayerParams &p, hipStream_t stream)
 {
     const int pairs = p.T * p.top_k;
