@@ -119,6 +119,14 @@ float real(PyObject *o)
     return (float)v;
 }
 
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw python_error();
+    return v != 0;
+}
+
 void *address(PyObject *o)
 {
     void *p = PyLong_AsVoidPtr(o);
@@ -166,7 +174,7 @@ PyObject *rmsnorm_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
     const Tensor r = optional(a[4], "residual");
     Tensor ro = optional(a[5], "residual_out"), y = optional(a[7], "y"), q = optional(a[8], "q"),
            s = optional(a[9], "s");
-    const int normed = PyObject_IsTrue(a[6]);
+    const bool normed = truth(a[6]);
     void *stream = address(a[10]);
 
     const int xt = float_type(x, "x"), wt = float_type(w, "weight");
@@ -238,7 +246,7 @@ PyObject *gate_topk(PyObject *, PyObject *const *a, Py_ssize_t n)
     const auto entry = reinterpret_cast<decltype(&dg_moe_gate_topk)>(address(a[0]));
     const Tensor logits = tensor(a[1], "logits");
     const int64_t top_k = integer(a[2]);
-    const int score = (int)integer(a[3]), renormalize = PyObject_IsTrue(a[4]);
+    const int score = (int)integer(a[3]), renormalize = truth(a[4]);
     const float factor = real(a[5]);
     Tensor ids = optional(a[6], "ids"), weights = optional(a[7], "weights");
     void *stream = address(a[8]);
@@ -333,8 +341,10 @@ PyObject *moe_layer(PyObject *, PyObject *const *a, Py_ssize_t n)
 
 PyObject *any_device(PyObject *, PyObject *on)
 {
-    g_any_device = PyObject_IsTrue(on) == 1;
+    HANDLE_TH_ERRORS
+    g_any_device = truth(on);
     Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
 }
 
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>

@@ -277,11 +277,16 @@ def test_binding_raises_the_status(recorded, monkeypatch):
         ops.dg_moe_gate_topk(torch.zeros((2, 8)), -1)
 
 
+class NoTruth:
+    def __bool__(self):
+        raise TypeError("neither")
+
+
 def test_binding_refuses_what_is_no_tensor_or_number():
     x, w = torch.zeros((2, 256)), torch.ones(256)
     for call in (lambda: ops.dg_fp8_rmsnorm_quantize_1x128([1.0], w), lambda: ops.dg_moe_gate_topk(None, 2),
                  lambda: ops.dg_fp8_rmsnorm_quantize_1x128(x, w, eps="a"), lambda: ops.dg_moe_gate_topk(x, "2"),
-                 lambda: ops.dg_fp8_moe_layer(*[None] * 9)):
+                 lambda: ops.dg_moe_gate_topk(x, 2, renormalize=NoTruth()), lambda: ops.dg_fp8_moe_layer(*[None] * 9)):
         with pytest.raises(TypeError):
             call()
 
