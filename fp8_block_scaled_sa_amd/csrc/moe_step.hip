@@ -28,6 +28,9 @@ bool strides_fit(std::initializer_list<int64_t> strides)
     return true;
 }
 
+// A launch takes fewer than 2^32 threads in all.
+bool threads_fit(int64_t workgroups, int64_t threads) { return workgroups * threads < ((int64_t)1 << 32); }
+
 int launched()
 {
     const hipError_t e = hipGetLastError();
@@ -37,6 +40,9 @@ int launched()
 bool is_float_type(int t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
 
 // ---------------------------------------------------------------- norm
+
+// Threads that a row takes (see launch_norm).
+int64_t norm_row_threads(int64_t K) { return K <= 1024 ? 64 : K <= 8192 ? 256 : 1024; }
 
 // Row layouts of the norm kernel: ROW threads per row, NC chunks of 8 a thread:
 // the fewest threads whose registers hold the row, so that short rows share a
@@ -165,6 +171,8 @@ dg_status dg_fp8_rmsnorm_quantize_1x128(const void *X, int x_dtype, int64_t ldx,
     if (!is_float_type(x_dtype) || (R && !is_float_type(r_dtype)) || !is_float_type(w_dtype) || M > kInt32Max ||
         K > kNormMaxK)
         return DG_ERR_UNSUPPORTED;
+    if (!threads_fit(M + 3, norm_row_threads(K)))
+        return DG_ERR_UNSUPPORTED;
     if (M == 0)
         return DG_OK;
     if (!X || !W || !Q || !S || (R && !R_out))
@@ -230,7 +238,7 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl, int sco
     if (T < 0 || E <= 0 || top_k <= 0 || top_k > E)
         return DG_ERR_BAD_SHAPE;
     if (!is_float_type(l_dtype) || (score != DG_GATE_SOFTMAX && score != DG_GATE_SIGMOID) || E > dgg::kMaxExperts ||
-        top_k > dgg::kMaxTopK || T > kInt32Max)
+        top_k > dgg::kMaxTopK || T > kInt32Max || !threads_fit(T + dgg::kTokens, dgg::kThreads / dgg::kTokens))
         return DG_ERR_UNSUPPORTED;
     if (T == 0)
         return DG_OK;
@@ -276,6 +284,8 @@ dg_status dg_fp8_moe_layer(const void *X, int64_t ldx, const float *sX, int64_t 
     int st = check_layer_sizes(T, top_k, E, H, I);
     if (st != DG_OK)
         return (dg_status)st;
+    if (!threads_fit(std::min(T * top_k, E) * (I / 16), dge::kUpThreads))
+        return DG_ERR_UNSUPPORTED;
     if (T == 0)
         return DG_OK;
     if (!X || !sX || !W13 || !s13 || !W2 || !s2 || !topk_ids || !topk_weights || !out || !workspace)

@@ -475,6 +475,42 @@ def test_layer_empty(gpu_device):
     assert ops.dg_fp8_moe_layer(*a, None).shape == (0, 256)
 
 
+# ---------------------------------------------------------------- offsets past 32 bits
+
+def test_norm_offsets_past_32_bits(gpu_device):
+    """More than 2^31 elements: the last rows are what a call on them alone gives."""
+    M, K = 270000, 8192
+    x = torch.empty((M, K), dtype=BF16, device="cuda")
+    x[-4:] = normal((4, K), 7).to(BF16).cuda()
+    w = torch.ones(K, dtype=BF16, device="cuda")
+    q, s, _, _ = ops.dg_fp8_rmsnorm_quantize_1x128(x, w)
+    q2, s2, _, _ = ops.dg_fp8_rmsnorm_quantize_1x128(x[-4:].clone(), w)
+    assert torch.equal(q[-4:], q2) and torch.equal(s[-4:], s2)
+
+
+def test_gate_offsets_past_32_bits(gpu_device):
+    T, E = 2200000, 1024
+    logits = torch.empty((T, E), dtype=BF16, device="cuda")
+    logits[-5:] = normal((5, E), 8).to(BF16).cuda()
+    ids, weights = ops.dg_moe_gate_topk(logits, 8)
+    ids2, weights2 = ops.dg_moe_gate_topk(logits[-5:].clone(), 8)
+    assert torch.equal(ids[-5:], ids2) and torch.equal(weights[-5:], weights2)
+
+
+def test_layer_offsets_past_32_bits(gpu_device):
+    """Experts more than 4 GiB apart."""
+    T, k, E, H, I = 3, 2, 3, 256, 128  # noqa: E741
+    a = make_layer(T, k, E, H, I, 91)
+    want = bits(run_layer(a))
+    apart = (1 << 32) + 4096
+    pool = torch.empty(2 * apart + (2 << 20), dtype=torch.uint8, device="cuda")
+    for i, rows, cols in ((2, 2 * I, H), (4, H, I)):
+        far = pool.as_strided((E, rows, cols), (apart, cols, 1), 0 if i == 2 else 1 << 20)
+        far.copy_(a[i])
+        a[i] = far
+    assert np.array_equal(bits(run_layer(a)), want)
+
+
 # ---------------------------------------------------------------- together
 
 def test_step_in_a_graph(gpu_device):

@@ -32,7 +32,9 @@ def norm(**kw):
     (dict(eps=float("nan")), SHAPE),
     (dict(xt=2), UNSUPPORTED), (dict(rt=-1), UNSUPPORTED), (dict(wt=7), UNSUPPORTED), (dict(M=2 ** 31), UNSUPPORTED),
     (dict(K=65664, ldx=65664, ldr=65664, ldro=65664, ldy=65664, ldq=65664), UNSUPPORTED),
-    (dict(ldx=2 ** 28 + 16), UNSUPPORTED),
+    (dict(ldx=2 ** 28 + 16), UNSUPPORTED), (dict(M=2 ** 26), UNSUPPORTED),
+    (dict(M=2 ** 24, K=1152, ldx=1152, ldr=1152, ldro=1152, ldy=1152, ldq=1152), UNSUPPORTED),
+    (dict(M=2 ** 22, K=8320, ldx=8320, ldr=8320, ldro=8320, ldy=8320, ldq=8320), UNSUPPORTED),
     (dict(X=None), NULL), (dict(W=None), NULL), (dict(Q=None), NULL), (dict(S=None), NULL), (dict(RO=None), NULL),
     (dict(ldx=504), STRIDE), (dict(ldr=256), STRIDE), (dict(ldro=256), STRIDE), (dict(ldy=256), STRIDE),
     (dict(ldq=496), STRIDE), (dict(s_m=-1), STRIDE), (dict(s_m=0), STRIDE), (dict(s_m=1, s_kb=32), STRIDE),
@@ -65,6 +67,7 @@ def gate(**kw):
     (dict(T=-1), SHAPE), (dict(E=0), SHAPE), (dict(k=0), SHAPE), (dict(k=9, E=8), SHAPE),
     (dict(E=1025, ldl=1025), UNSUPPORTED), (dict(k=17), UNSUPPORTED), (dict(lt=2), UNSUPPORTED),
     (dict(score=2), UNSUPPORTED), (dict(T=2 ** 31), UNSUPPORTED), (dict(ldl=2 ** 29), UNSUPPORTED),
+    (dict(T=2 ** 28), UNSUPPORTED),
     (dict(logits=None), NULL), (dict(ids=None), NULL), (dict(weights=None), NULL),
     (dict(ldl=255), STRIDE),
     (dict(logits=X + 2), MISALIGNED), (dict(ids=IDS + 2), MISALIGNED), (dict(weights=WTS + 1), MISALIGNED),
@@ -100,7 +103,7 @@ def layer(**kw):
     (dict(H=2 ** 18 + 128, ldx=2 ** 21, ld13=2 ** 21, ldo=2 ** 21), UNSUPPORTED),
     (dict(ld13=2 ** 25 + 16, w13_e=2 ** 40), UNSUPPORTED), (dict(sx_m=2 ** 22 + 1), UNSUPPORTED),
     (dict(ldo=2 ** 25 + 8), UNSUPPORTED), (dict(w2_e=2 ** 51), UNSUPPORTED),
-    (dict(sx_kb=2 ** 29), UNSUPPORTED),
+    (dict(sx_kb=2 ** 29), UNSUPPORTED), (dict(T=64, k=16, E=1024, I=2 ** 18), UNSUPPORTED),
 ] + [(dict([(n, None)]), NULL) for n in ("X", "sX", "W13", "s13", "W2", "s2", "ids", "wts", "out", "ws")] + [
     (dict(ldx=256), STRIDE), (dict(ld13=496), STRIDE), (dict(ld2=128), STRIDE), (dict(ldo=256), STRIDE),
     (dict(w13_e=512 * 512 - 16), STRIDE), (dict(w2_e=512 * 256 - 16), STRIDE), (dict(w2_e=0), STRIDE),
