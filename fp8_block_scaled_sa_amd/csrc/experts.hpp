@@ -40,6 +40,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include "kernels.hpp"
@@ -158,17 +159,27 @@ __device__ __forceinline__ int slot_expert(const LayerParams &p, int by_pair, in
 constexpr int kUpWaves = 4;
 constexpr int kUpThreads = 64 * kUpWaves;
 
+// h as two bf16 numbers. A finite h that rounds to infinity keeps bf16's largest
+// number as hi, and its lo the rest of it; an infinite or NaN h has no rest (hi +
+// lo would be NaN). That is decided from hi, not from h - hi: the compiler fuses
+// h's last product into that subtraction, which leaves an infinity where h and hi
+// are both infinite (and makes lo the rest of the product before its rounding).
+__device__ __forceinline__ void split_bf16(float h, uint32_t &hi, uint32_t &lo)
+{
+    hi = dgk::bf16_rne(h);
+    if ((hi & 0x7fffu) == 0x7f80u && __builtin_fabsf(h) < INFINITY)
+        hi -= 1;
+    const float rest = h - __uint_as_float(hi << 16);
+    lo = (hi & 0x7f80u) == 0x7f80u ? 0 : dgk::bf16_rne(rest);
+}
+
 // Four consecutive values of h of one pair, from row on.
 __device__ __forceinline__ void store_h(const LayerParams &p, int pair, int row, const v4f &g, const v4f &u)
 {
     uint32_t hi[4], lo[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const float h = g[c] / (1.0f + __expf(-g[c])) * u[c];
-        hi[c] = dgk::bf16_rne(h);
-        const float rest = h - __uint_as_float(hi[c] << 16);
-        lo[c] = dgk::bf16_rne(rest == rest ? rest : 0.0f);  // an infinite h is its hi part alone
-    }
+    for (int c = 0; c < 4; ++c)
+        split_bf16(g[c] / (1.0f + __expf(-g[c])) * u[c], hi[c], lo[c]);
     uint16_t *to = p.h + (int64_t)pair * p.I + row;
     *(u32x2 *)to = u32x2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
     to += (int64_t)p.T * p.top_k * p.I;

@@ -1,0 +1,52 @@
+"""The serving step's operators on the GPU at the borders of their ranges."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import bits
+from tests.test_gpu_moe_step import BF16, F8, run_layer
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- layer: the two parts of h at the end of bf16's range
+
+# h = (0x1.FE + c 2^-8) 2^127: bf16's largest number for c = 0, from c = 1 on
+# nearer to 2^128 than to it (or as near), past fp32's range for c = 4.
+PARTS = [0.0, 0.5, 0.875, 1.0, 1.125, 1.875, 4.0]
+
+
+def layer_at_the_border(T):
+    """One expert, h_0 = +-(0x1.FE + c 2^-8) 2^127 and h_1 = -+0x1.FE 2^127, each a product of g = 2^64 (where
+    silu(g) is g) and u; even rows of W2 take h_0, odd ones h_0 + h_1, all times 2^-100. Every sum is exact."""
+    H, I = 384, 128  # noqa: E741
+    c = torch.tensor(PARTS).repeat_interleave(2).repeat(T)[:T]
+    sign = torch.tensor([1.0, -1.0]).repeat(T)[:T]
+    x = torch.zeros((T, H))
+    x[:, 0], x[:, 1], x[:, 129], x[:, 257] = 1, sign, sign, sign * c
+    sx = torch.tensor([2.0 ** 32, 2.0 ** 28, 2.0 ** 24]).expand(T, 3).contiguous()
+    w13 = torch.zeros((1, 2 * I, H))
+    w13[0, :2, 0] = 1                                               # g
+    w13[0, I, 1], w13[0, I, 129], w13[0, I, 257] = 1.875, 1.875, 1  # 1.875 (1 + 2^-4) = 0x1.FE
+    w13[0, I + 1, 1], w13[0, I + 1, 129] = -1.875, -1.875
+    s13 = torch.tensor([2.0 ** 32, 2.0 ** 31])[None, :, None].expand(1, 2, 3).contiguous()
+    w2 = torch.zeros((1, H, I))
+    w2[0, :, 0], w2[0, 1::2, 1] = 1, 1
+    code = lambda v: v.to(F8).view(torch.uint8)  # noqa: E731
+    a = [t.cuda() for t in (code(x), sx, code(w13), s13, code(w2), torch.full((1, 3, 1), 2.0 ** -100),
+                            torch.zeros((T, 1), dtype=torch.int32), torch.ones((T, 1)))]
+    # in fp64; bf16 of it is one rounding (the sums have at most 12 bits)
+    h0 = torch.where(c >= 4, math.inf, (0x1FE / 256 + c.double() / 256) * 2.0 ** 127)
+    even, odd = sign * h0 * 2.0 ** -100, sign * (h0 - 0x1FE / 256 * 2.0 ** 127) * 2.0 ** -100
+    ref = torch.stack([even, odd], 1).repeat(1, H // 2).float().to(BF16)
+    return a, ref
+
+
+@pytest.mark.parametrize("T", [1, 8, 14, 33, 64])
+def test_layer_h_at_the_end_of_bf16(gpu_device, T):
+    a, ref = layer_at_the_border(T)
+    got = bits(run_layer(a))
+    # a zero's sign is that of the sum's order
+    assert np.array_equal(np.where(got == 0x8000, 0, got), np.where(bits(ref) == 0x8000, 0, bits(ref)))
