@@ -12,6 +12,8 @@
 // where it is not DG_OK.
 #include <Python.h>
 
+#include <dlfcn.h>
+
 #include <ATen/ATen.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -36,8 +38,13 @@ constexpr int64_t kBlock = 128;
 [[noreturn]] void bad_value(const std::string &what) { refuse(PyExc_ValueError, what); }
 [[noreturn]] void bad_type(const std::string &what) { refuse(PyExc_TypeError, what); }
 
-// Set by tests that call these functions with host tensors and an entry point of their own.
-bool g_any_device = false;
+// Set by tests that call these functions with host tensors and an entry point of their own (this thread's calls).
+thread_local bool t_any_device = false;
+// The call's entry point is such a callback: code that no loaded file holds.
+thread_local bool t_callback = false;
+
+// An address that every entry point refuses as misaligned, before any launch.
+void *const kNoAddress = reinterpret_cast<void *>(1);
 
 Tensor tensor(PyObject *o, const char *name)
 {
@@ -50,9 +57,11 @@ Tensor optional(PyObject *o, const char *name) { return o == Py_None ? Tensor() 
 
 void *pointer(const Tensor &t, const char *name)
 {
-    if (!t.is_cuda() && !g_any_device)
+    if (t.is_cuda())
+        return t.data_ptr();
+    if (!t_any_device)
         bad_value(std::string(name) + " must be a device tensor");
-    return t.data_ptr();
+    return t_callback ? t.data_ptr() : kNoAddress;  // a host address never reaches the library
 }
 
 // DG_DTYPE_F32 or DG_DTYPE_BF16 of a tensor of activations.
@@ -135,6 +144,18 @@ void *address(PyObject *o)
     return p;
 }
 
+// The entry point that a call's first argument holds.
+template <typename Entry>
+Entry entry_point(PyObject *o)
+{
+    void *const p = address(o);
+    if (t_any_device) {
+        Dl_info info;
+        t_callback = dladdr(p, &info) == 0;
+    }
+    return reinterpret_cast<Entry>(p);
+}
+
 void need_arguments(Py_ssize_t got, Py_ssize_t want)
 {
     if (got != want)
@@ -168,7 +189,7 @@ PyObject *rmsnorm_quantize(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     need_arguments(n, 11);
-    const auto entry = reinterpret_cast<decltype(&dg_fp8_rmsnorm_quantize_1x128)>(address(a[0]));
+    const auto entry = entry_point<decltype(&dg_fp8_rmsnorm_quantize_1x128)>(a[0]);
     const Tensor x = tensor(a[1], "x"), w = tensor(a[2], "weight");
     const float eps = real(a[3]);
     const Tensor r = optional(a[4], "residual");
@@ -243,7 +264,7 @@ PyObject *gate_topk(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     need_arguments(n, 9);
-    const auto entry = reinterpret_cast<decltype(&dg_moe_gate_topk)>(address(a[0]));
+    const auto entry = entry_point<decltype(&dg_moe_gate_topk)>(a[0]);
     const Tensor logits = tensor(a[1], "logits");
     const int64_t top_k = integer(a[2]);
     const int score = (int)integer(a[3]), renormalize = truth(a[4]);
@@ -279,7 +300,7 @@ PyObject *moe_layer(PyObject *, PyObject *const *a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
     need_arguments(n, 12);
-    const auto entry = reinterpret_cast<decltype(&dg_fp8_moe_layer)>(address(a[0]));
+    const auto entry = entry_point<decltype(&dg_fp8_moe_layer)>(a[0]);
     const Tensor x = tensor(a[1], "x"), sx = tensor(a[2], "sx"), w13 = tensor(a[3], "w13"), s13 = tensor(a[4], "s13"),
                  w2 = tensor(a[5], "w2"), s2 = tensor(a[6], "s2"), ids = tensor(a[7], "topk_ids"),
                  weights = tensor(a[8], "topk_weights"), ws = optional(a[9], "workspace");
@@ -342,7 +363,7 @@ PyObject *moe_layer(PyObject *, PyObject *const *a, Py_ssize_t n)
 PyObject *any_device(PyObject *, PyObject *on)
 {
     HANDLE_TH_ERRORS
-    g_any_device = truth(on);
+    t_any_device = truth(on);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -357,7 +378,7 @@ PyMethodDef methods[] = {
     {"rmsnorm_quantize", fast<rmsnorm_quantize>(), METH_FASTCALL, nullptr},
     {"gate_topk", fast<gate_topk>(), METH_FASTCALL, nullptr},
     {"moe_layer", fast<moe_layer>(), METH_FASTCALL, nullptr},
-    {"any_device", any_device, METH_O, "Tests only: take host tensors too."},
+    {"any_device", any_device, METH_O, "Tests only: this thread's calls take host tensors too."},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods};
