@@ -4,9 +4,15 @@ Argument marshalling only: every step of the GEMM runs in the HIP library.
 Operands are CUDA (HIP) tensors: e4m3 codes as ``torch.uint8`` or
 ``torch.float8_e4m3fn``, scales ``torch.float32`` (any strides, read through
 the logical index), routing arrays ``torch.int32``, output ``torch.bfloat16``.
-The call is enqueued on torch's current stream unless ``stream`` is given.
+The call is enqueued on torch's current stream unless ``stream`` is given (a
+torch.cuda.Stream, or a raw handle as an int). Outputs that the call allocates
+belong to the stream that writes them, and may be dropped at any time on either
+stream; to read them on another stream the caller orders the two, as ever.
 """
 from __future__ import annotations
+
+import functools
+import inspect
 
 import torch
 
@@ -54,11 +60,50 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+def _on_device(t) -> bool:
+    return getattr(t, "is_cuda", False)
+
+
+def _call_on(stream, call, *args):
+    """call(*args) with stream as torch's current one. What it allocates comes from
+    that stream's memory: memory of the current stream could still be in use there,
+    and could be handed out again there while the call's kernels write it. The
+    current stream, which may read the outputs later, is recorded on them."""
+    side = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(side):
+        out = call(*args)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None and not any(t is a for a in args):
+            t.record_stream(here)
+    return out
+
+
+def _takes_stream(call):
+    """call, whose first parameter is a tensor and whose last one is stream, by _call_on where a stream is given."""
+    signature = inspect.signature(call)
+    last = len(signature.parameters) - 1
+    assert list(signature.parameters)[last] == "stream"
+
+    @functools.wraps(call)
+    def on_stream(*args, **kw):
+        if kw.get("stream") is None and len(args) <= last:
+            return call(*args, **kw)
+        bound = signature.bind(*args, **kw)
+        bound.apply_defaults()
+        *args, stream = bound.args
+        if stream is None or not _on_device(args[0]):
+            return call(*args, stream)
+        return _call_on(stream, call, *args)
+    return on_stream
+
+
 def _check(status: int, where: str):
     if status != 0:
         raise DGError(status, where)
 
 
+@_takes_stream
 def dg_fp8_gemm_nt(a, sa, b, sb, d=None, stream=None):
     """D[M,N] (bf16) from A[M,K], sA[M,K/128], B[N,K], sB[N/128,K/128]."""
     _codes(a, "a", 2), _codes(b, "b", 2), _scales(sa, "sa", 2), _scales(sb, "sb", 2)
@@ -105,6 +150,7 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(int(nbytes), 0), dtype=torch.uint8, device=device)
 
 
+@_takes_stream
 def dg_fp8_gemm_nt_ws(a, sa, b, sb, workspace, d=None, stream=None):
     """dg_fp8_gemm_nt with a caller workspace (a uint8 device tensor, or None)
     for its split-K path."""
@@ -128,6 +174,7 @@ def dg_fp8_gemm_nt_ws(a, sa, b, sb, workspace, d=None, stream=None):
     return d
 
 
+@_takes_stream
 def dg_fp8_gemm_nt_noalloc(a, sa, b, sb, d, stream=None):
     """dg_fp8_gemm_nt_ws with the library's static scratch array as the
     workspace: allocates nothing (d must be given)."""
@@ -150,6 +197,7 @@ def dg_fp8_gemm_nt_noalloc(a, sa, b, sb, d, stream=None):
 FORMATS = {"e4m3": 0, "e5m2": 1}   # DG_FP8_E4M3, DG_FP8_E5M2
 
 
+@_takes_stream
 def dg_fp8_gemm_nt_fmt(a, sa, b, sb, a_fmt="e4m3", b_fmt="e4m3", d=None, stream=None):
     """dg_fp8_gemm_nt with a per-operand fp8 format ("e4m3" or "e5m2"). Codes
     are uint8 (or the matching torch float8 dtype)."""
@@ -175,6 +223,7 @@ def dg_fp8_gemm_nt_fmt(a, sa, b, sb, a_fmt="e4m3", b_fmt="e4m3", d=None, stream=
     return d
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_contiguous(a, sa, b, sb, expert_ids, d=None, stream=None):
     """Contiguous MoE layout: A[M_total,K], sA[M_total,K/128], B[G,N,K],
     sB[G,N/128,K/128], expert_ids[M_total] int32 -> D[M_total,N]; rows whose
@@ -203,6 +252,7 @@ def dg_fp8_grouped_gemm_contiguous(a, sa, b, sb, expert_ids, d=None, stream=None
     return d
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_contiguous_to_tokens(a, sa, b, sb, expert_ids, token_of_row, T, layout=None, out=None,
                                              stream=None):
     """The contiguous grouped GEMM with row r of the result written to
@@ -232,6 +282,7 @@ def dg_fp8_grouped_gemm_contiguous_to_tokens(a, sa, b, sb, expert_ids, token_of_
     return out
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_contiguous_layout(a, sa, b, sb, expert_ids, layout, d=None, stream=None):
     """The contiguous grouped GEMM with the experts' segment offsets
     (layout [G+1] int32): tiles follow the segments."""
@@ -258,6 +309,7 @@ def dg_fp8_grouped_gemm_contiguous_workspace_bytes(M_total: int, N: int, K: int,
                   "dg_fp8_grouped_gemm_contiguous_workspace_bytes")
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_contiguous_ws(a, sa, b, sb, expert_ids, workspace, token_of_row=None, T=None, layout=None,
                                       d=None, stream=None):
     """The contiguous grouped GEMM with a caller workspace (uint8 device
@@ -295,6 +347,7 @@ def dg_fp8_grouped_gemm_contiguous_ws(a, sa, b, sb, expert_ids, workspace, token
     return d
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_masked(a, sa, b, sb, masked_m, d=None, stream=None):
     """Masked MoE layout: A[G,M_max,K], sA[G,M_max,K/128], B[G,N,K],
     sB[G,N/128,K/128], masked_m[G] int32 -> D[G,M_max,N]; group g writes rows
@@ -328,6 +381,7 @@ def dg_fp8_grouped_gemm_masked(a, sa, b, sb, masked_m, d=None, stream=None):
 DTYPES = {torch.float32: 0, torch.bfloat16: 1}   # DG_DTYPE_F32, DG_DTYPE_BF16
 
 
+@_takes_stream
 def dg_fp8_quantize_1x128(x, q=None, s=None, stream=None):
     """Codes Q[M,K] (uint8 e4m3) and scales S[M,K/128] (fp32) of activations
     x[M,K] (float32 or bfloat16), one scale per 1x128 block. A new S is
@@ -356,6 +410,7 @@ def _dev_or_null(t, name):
     return None if t is None or t.numel() == 0 else _dev(t, name)
 
 
+@_takes_stream
 def dg_fp8_quantize_1x128_gather(x, src_rows, q=None, s=None, stream=None):
     """Quantise rows x[src_rows[r]] into Q[r] (a source index outside
     [0, x.shape[0]) gives a zero row: codes 0, scale 1). Returns (q, s) with
@@ -386,6 +441,7 @@ def dg_moe_contiguous_max_rows(T: int, G: int) -> int:
     return int(_lib.load().dg_moe_contiguous_max_rows(T, G))
 
 
+@_takes_stream
 def dg_moe_route_contiguous(expert_of_token, G, M_cap=None, stream=None):
     """Routing of top-1 tokens into the contiguous layout. Returns
     (row_of_token [T], expert_ids [M_cap], token_of_row [M_cap], layout [G+1]),
@@ -407,6 +463,7 @@ def dg_moe_route_contiguous(expert_of_token, G, M_cap=None, stream=None):
     return row, ids, tok, layout
 
 
+@_takes_stream
 def dg_moe_unpermute(d, row_of_token, out=None, stream=None):
     """out[t] = d[row_of_token[t]] (bf16 rows); out-of-range rows give zeros."""
     if d.dtype != torch.bfloat16 or d.dim() != 2 or d.stride(-1) != 1:
@@ -431,6 +488,7 @@ def _fmt_codes(t, name, ndim):
         raise TypeError("%s must be a %d-D fp8 code tensor with a contiguous last (K) dimension" % (name, ndim))
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_contiguous_fmt(a, sa, b, sb, expert_ids, a_fmt="e4m3", b_fmt="e4m3", d=None, stream=None):
     """dg_fp8_grouped_gemm_contiguous with a per-operand fp8 format ("e4m3" or "e5m2")."""
     _fmt_codes(a, "a", 2), _fmt_codes(b, "b", 3), _scales(sa, "sa", 2), _scales(sb, "sb", 3)
@@ -447,6 +505,7 @@ def dg_fp8_grouped_gemm_contiguous_fmt(a, sa, b, sb, expert_ids, a_fmt="e4m3", b
     return d
 
 
+@_takes_stream
 def dg_fp8_grouped_gemm_masked_fmt(a, sa, b, sb, masked_m, a_fmt="e4m3", b_fmt="e4m3", d=None, stream=None):
     """dg_fp8_grouped_gemm_masked with a per-operand fp8 format ("e4m3" or "e5m2")."""
     _fmt_codes(a, "a", 3), _fmt_codes(b, "b", 3), _scales(sa, "sa", 3), _scales(sb, "sb", 3)
@@ -487,7 +546,7 @@ def _binding():
 
 def _stream_for(stream, t) -> int:
     """The stream's handle for a call on t; what is no device tensor needs none (the binding refuses it)."""
-    return _stream(stream) if stream is not None or getattr(t, "is_cuda", False) else 0
+    return _stream(stream) if stream is not None or _on_device(t) else 0
 
 
 def dg_fp8_rmsnorm_quantize_1x128(x, weight, eps=1e-6, residual=None, residual_out=None, normed=False, y=None,
@@ -498,6 +557,8 @@ def dg_fp8_rmsnorm_quantize_1x128(x, weight, eps=1e-6, residual=None, residual_o
     given; the residual itself updates it in place). normed=True (or a given y)
     also returns the normed rows in bfloat16. A new S is M-major. Returns
     (q, s, residual_out, y), None for what was not asked for."""
+    if stream is not None and _on_device(x):
+        return _call_on(stream, dg_fp8_rmsnorm_quantize_1x128, x, weight, eps, residual, residual_out, normed, y, q, s)
     out = _binding().rmsnorm_quantize(_lib.address("dg_fp8_rmsnorm_quantize_1x128"), x, weight, eps, residual,
                                       residual_out, normed, y, q, s, _stream_for(stream, x))
     if type(out) is int:
@@ -517,6 +578,8 @@ def dg_moe_gate_topk(logits, top_k, score="softmax", renormalize=True, factor=1.
     chosen ones' sum if renormalize; times factor. Returns (ids, weights)."""
     if score not in GATE_SCORES:
         raise ValueError("score must be one of %s" % ", ".join(GATE_SCORES))
+    if stream is not None and _on_device(logits):
+        return _call_on(stream, dg_moe_gate_topk, logits, top_k, score, renormalize, factor, ids, weights)
     out = _binding().gate_topk(_lib.address("dg_moe_gate_topk"), logits, top_k, GATE_SCORES[score], renormalize,
                                factor, ids, weights, _stream_for(stream, logits))
     if type(out) is int:
@@ -536,6 +599,8 @@ def dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, topk_ids, topk_weights, workspace,
     slot skipped), topk_weights[T,top_k] float32 -> out[T,H] bfloat16 =
     sum_j weight_j W2_e (silu(gate) * up). workspace: a device tensor of at
     least dg_fp8_moe_layer_workspace_bytes(T, top_k, H, I) bytes."""
+    if stream is not None and _on_device(x):
+        return _call_on(stream, dg_fp8_moe_layer, x, sx, w13, s13, w2, s2, topk_ids, topk_weights, workspace, out)
     out = _binding().moe_layer(_lib.address("dg_fp8_moe_layer"), x, sx, w13, s13, w2, s2, topk_ids, topk_weights,
                                workspace, out, _stream_for(stream, x))
     if type(out) is int:

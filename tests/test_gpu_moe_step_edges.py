@@ -5,8 +5,9 @@ import numpy as np
 import pytest
 import torch
 
+from fp8_block_scaled_sa_amd import ops
 from tests.gpu_util import bits
-from tests.test_gpu_moe_step import BF16, F8, run_layer
+from tests.test_gpu_moe_step import BF16, F8, make_layer, run_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,61 @@ def test_layer_h_at_the_end_of_bf16(gpu_device, T):
     got = bits(run_layer(a))
     # a zero's sign is that of the sum's order
     assert np.array_equal(np.where(got == 0x8000, 0, got), np.where(bits(ref) == 0x8000, 0, bits(ref)))
+
+
+# ---------------------------------------------------------------- outputs on a stream that is not the current one
+
+def step_calls(side):
+    """Each operator on small inputs with new outputs on stream side, as functions."""
+    a = make_layer(4, 2, 4, 512, 256, 7)
+    x = torch.ones((4, 512), dtype=BF16, device="cuda")
+    w = torch.ones(512, dtype=BF16, device="cuda")
+    logits = torch.zeros((4, 8), device="cuda")
+    ws = ops.workspace(ops.dg_fp8_moe_layer_workspace_bytes(4, 2, 512, 256))
+    return [lambda: ops.dg_fp8_rmsnorm_quantize_1x128(x, w, residual=x, normed=True, stream=side),
+            lambda: ops.dg_moe_gate_topk(logits, 2, stream=side),
+            lambda: ops.dg_fp8_moe_layer(*a, ws, stream=side),
+            lambda: ops.dg_fp8_quantize_1x128(x, stream=side)]
+
+
+def blocks(out):
+    """Size and address of each output."""
+    return [(t.numel() * t.element_size(), t.data_ptr()) for t in (out if isinstance(out, tuple) else (out,))]
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_dropped_while_their_stream_works(gpu_device, which, raw):
+    """Outputs that are dropped before the kernel has run are not handed out to the current stream."""
+    side = torch.cuda.Stream()
+    call = step_calls(side.cuda_stream if raw else side)[which]
+    side.wait_stream(torch.cuda.current_stream())
+    call()                       # memory of both streams' pools is there
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    out = call()
+    held = blocks(out)
+    del out
+    new = [torch.empty(n, dtype=torch.uint8, device="cuda") for n, _ in held for _ in range(4)]
+    assert not {t.data_ptr() for t in new} & {at for _, at in held}
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("which", range(4))
+def test_outputs_dropped_while_the_current_stream_reads(gpu_device, which):
+    """Nor are outputs that the current stream has still to read handed out to their own stream."""
+    side = torch.cuda.Stream()
+    call = step_calls(side)[which]
+    side.wait_stream(torch.cuda.current_stream())
+    call()
+    torch.cuda.synchronize()
+    out = call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(20_000_000)
+    held = blocks(out)
+    del out
+    with torch.cuda.stream(side):
+        new = [torch.empty(n, dtype=torch.uint8, device="cuda") for n, _ in held for _ in range(4)]
+    assert not {t.data_ptr() for t in new} & {at for _, at in held}
+    torch.cuda.synchronize()

@@ -1,4 +1,6 @@
 """The serving step's operators at the borders of their checks, on the host; none of these calls reaches a device."""
+import contextlib
+import inspect
 import threading
 
 import pytest
@@ -49,3 +51,55 @@ def test_host_tensors_are_one_threads_affair(host_tensors):
     t.start()
     t.join()
     assert len(seen) == 3 and all("must be a device tensor" in s for s in seen)
+
+
+class StandIn:
+    """In the place of a device tensor."""
+    is_cuda = True
+
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, stream):
+        self.recorded.append(stream)
+
+
+CALLS = sorted(n for n in vars(ops) if n.startswith("dg_") and "stream" in inspect.signature(getattr(ops, n)).parameters)
+
+
+@pytest.mark.parametrize("name", CALLS)
+@pytest.mark.parametrize("positional", [False, True])
+def test_every_call_with_a_stream_is_made_on_it(monkeypatch, name, positional):
+    routed = []
+    monkeypatch.setattr(ops, "_call_on", lambda stream, call, *args: routed.append((stream, call.__name__, args)))
+    call = getattr(ops, name)
+    parameters = list(inspect.signature(call).parameters.values())
+    assert parameters[-1].name == "stream"
+    args = [StandIn() if p.default is p.empty else p.default for p in parameters[:-1]]
+    call(*args, 7) if positional else call(*args, stream=7)
+    assert routed == [(7, name, tuple(args))]
+
+
+def test_a_call_on_another_stream_allocates_there(monkeypatch):
+    """The stream is torch's current one while the call runs; the one that was current is recorded on what the call
+    returns, but not on what the caller gave it."""
+    current = ["here"]
+
+    @contextlib.contextmanager
+    def enter(stream):
+        current.append(stream)
+        yield
+        current.pop()
+
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: current[-1])
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: "side %d" % handle)
+    made, given = StandIn(), StandIn()
+
+    def call(*args):
+        assert current[-1] == "side 7"
+        return made, args[0], None
+
+    assert ops._call_on(7, call, given, 3) == (made, given, None)
+    assert current == ["here"] and made.recorded == ["here"] and given.recorded == []
+    assert ops._call_on(7, lambda: made) is made and made.recorded == ["here", "here"]
