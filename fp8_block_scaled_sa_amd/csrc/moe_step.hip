@@ -171,7 +171,8 @@ dg_status dg_fp8_rmsnorm_quantize_1x128(const void *X, int x_dtype, int64_t ldx,
     if (!is_float_type(x_dtype) || (R && !is_float_type(r_dtype)) || !is_float_type(w_dtype) || M > kInt32Max ||
         K > kNormMaxK)
         return DG_ERR_UNSUPPORTED;
-    if (!threads_fit(M + 3, norm_row_threads(K)))
+    const int64_t row_threads = norm_row_threads(K), group = std::max<int64_t>(row_threads, 256);
+    if (!threads_fit((M * row_threads + group - 1) / group, group))
         return DG_ERR_UNSUPPORTED;
     if (M == 0)
         return DG_OK;
@@ -238,7 +239,8 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl, int sco
     if (T < 0 || E <= 0 || top_k <= 0 || top_k > E)
         return DG_ERR_BAD_SHAPE;
     if (!is_float_type(l_dtype) || (score != DG_GATE_SOFTMAX && score != DG_GATE_SIGMOID) || E > dgg::kMaxExperts ||
-        top_k > dgg::kMaxTopK || T > kInt32Max || !threads_fit(T + dgg::kTokens, dgg::kThreads / dgg::kTokens))
+        top_k > dgg::kMaxTopK || T > kInt32Max ||
+        !threads_fit((T + dgg::kTokens - 1) / dgg::kTokens, dgg::kThreads))
         return DG_ERR_UNSUPPORTED;
     if (T == 0)
         return DG_OK;

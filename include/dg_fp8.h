@@ -490,8 +490,9 @@ dg_status dg_moe_unpermute(const void *D, int64_t ldd, int64_t d_rows,
  * about 2^63 and more) come out as zeros, and a row of zeros with eps = 0 as
  * NaN. Non-finite inputs give what the formulas give in R_out and Y; the codes
  * and scales of a row that is not finite in Y are unspecified (no fault).
- * Constraints: 0 < K <= 65536, K % 128 == 0, eps >= 0; M below 2^26 for K <=
- * 1024, 2^24 for K <= 8192, 2^22 above (DG_ERR_UNSUPPORTED beyond these);
+ * Constraints: 0 < K <= 65536, K % 128 == 0, eps >= 0; M at most 2^26 - 4 for
+ * K <= 1024, 2^24 - 1 for K <= 8192, 2^22 - 1 above (DG_ERR_UNSUPPORTED beyond
+ * these: a launch takes fewer than 2^32 threads);
  * X, R, R_out, W, Y, Q 16-byte aligned, row strides multiples of 16 bytes; S
  * 4-byte aligned; strides at most 2^28 elements (DG_ERR_UNSUPPORTED above);
  * scale slots distinct as in dg_fp8_quantize_1x128. The outputs lie apart from
@@ -527,9 +528,10 @@ dg_status dg_fp8_rmsnorm_quantize_1x128(const void *X, int x_dtype, int64_t ldx,
  * which dg_fp8_moe_layer skips. A logit of +inf is chosen first, with the
  * weight that the formula gives (NaN for the softmax). fp32 throughout.
  * With top_k = 1 the ids are the expert_of_token of dg_moe_route_contiguous.
- * Constraints: 1 <= top_k <= min(E, 16), E <= 1024, T below 2^28
- * (DG_ERR_UNSUPPORTED beyond 16, 1024 and 2^28), ldl >= E and at most 2^28; pointers aligned to their element;
- * outputs apart from each other and from logits. T = 0 returns DG_OK.
+ * Constraints: 1 <= top_k <= min(E, 16), E <= 1024, T at most 2^28 - 16
+ * (DG_ERR_UNSUPPORTED beyond 16, 1024 and 2^28 - 16), ldl >= E and at most
+ * 2^28; pointers aligned to their element; outputs apart from each other and
+ * from logits. T = 0 returns DG_OK.
  */
 dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
                            int score, int renormalize, float factor,

@@ -7,7 +7,7 @@ import torch
 
 from fp8_block_scaled_sa_amd import ops
 from tests.gpu_util import bits
-from tests.test_gpu_moe_step import BF16, F8, make_layer, run_layer
+from tests.test_gpu_moe_step import BF16, F8, make_layer, normal, run_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -109,3 +109,23 @@ def test_outputs_dropped_while_the_current_stream_reads(gpu_device, which):
         new = [torch.empty(n, dtype=torch.uint8, device="cuda") for n, _ in held for _ in range(4)]
     assert not {t.data_ptr() for t in new} & {at for _, at in held}
     torch.cuda.synchronize()
+
+
+# ---------------------------------------------------------------- the largest launches
+
+def test_norm_most_rows(gpu_device):
+    M, K = 2 ** 26 - 4, 128
+    x = torch.empty((M, K), dtype=BF16, device="cuda")
+    ends = torch.cat([torch.arange(5), torch.arange(M - 5, M)]).cuda()
+    x[ends] = normal((10, K), 7).to(BF16).cuda()
+    w = torch.ones(K, dtype=BF16, device="cuda")
+    q, s, _, _ = ops.dg_fp8_rmsnorm_quantize_1x128(x, w)
+    q2, s2, _, _ = ops.dg_fp8_rmsnorm_quantize_1x128(x[ends], w)
+    assert torch.equal(q[ends], q2) and torch.equal(s[ends], s2)
+
+
+def test_gate_most_tokens(gpu_device):
+    logits = torch.zeros((2 ** 28 - 16, 1), dtype=BF16, device="cuda")
+    ids = torch.full((2 ** 28 - 16, 1), 7, dtype=torch.int32, device="cuda")
+    ops.dg_moe_gate_topk(logits, 1, ids=ids)
+    assert not ids.any()

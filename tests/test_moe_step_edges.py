@@ -7,8 +7,7 @@ import pytest
 import torch
 
 from fp8_block_scaled_sa_amd import DGError, ops
-
-MISALIGNED = 3
+from tests.test_moe_step_abi import IDS, MISALIGNED, S, UNSUPPORTED, gate, norm
 
 
 @pytest.fixture
@@ -103,3 +102,17 @@ def test_a_call_on_another_stream_allocates_there(monkeypatch):
     assert ops._call_on(7, call, given, 3) == (made, given, None)
     assert current == ["here"] and made.recorded == ["here"] and given.recorded == []
     assert ops._call_on(7, lambda: made) is made and made.recorded == ["here", "here"]
+
+
+
+@pytest.mark.parametrize("K,most", [(128, 2 ** 26 - 4), (1024, 2 ** 26 - 4), (1152, 2 ** 24 - 1), (8192, 2 ** 24 - 1),
+                                    (8320, 2 ** 22 - 1), (65536, 2 ** 22 - 1)])
+def test_norm_takes_the_rows_that_a_launch_can_hold(K, most):
+    """The largest M passes the check of sizes (and is refused for its misaligned S), one more does not."""
+    for M, status in ((most, MISALIGNED), (most + 1, UNSUPPORTED)):
+        assert norm(M=M, K=K, ldx=K, ldr=K, ldro=K, ldy=K, ldq=K, s_m=K // 128, s_kb=1, S=S + 2) == status
+
+
+def test_gate_takes_the_tokens_that_a_launch_can_hold():
+    for T, status in ((2 ** 28 - 16, MISALIGNED), (2 ** 28 - 15, UNSUPPORTED)):
+        assert gate(T=T, ids=IDS + 2) == status
