@@ -274,7 +274,7 @@ PyObject *gate_topk(PyObject *, PyObject *const *a, Py_ssize_t n)
 
     const int type = float_type(logits, "logits");
     const int64_t ldl = rows(logits, "logits"), T = logits.size(0), E = logits.size(1);
-    if (top_k < 0)
+    if (top_k < 0 || top_k > E)  // before outputs of that size are made
         return PyLong_FromLong(DG_ERR_BAD_SHAPE);
     if (ids.defined())
         need_slots(ids, "ids", ScalarType::Int, {T, top_k});

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from fp8_block_scaled_sa_amd import DGError, ops
-from tests.test_moe_step_abi import IDS, MISALIGNED, S, UNSUPPORTED, gate, norm
+from tests.test_moe_step_abi import IDS, MISALIGNED, S, SHAPE, UNSUPPORTED, gate, norm
 
 
 @pytest.fixture
@@ -116,3 +116,10 @@ def test_norm_takes_the_rows_that_a_launch_can_hold(K, most):
 def test_gate_takes_the_tokens_that_a_launch_can_hold():
     for T, status in ((2 ** 28 - 16, MISALIGNED), (2 ** 28 - 15, UNSUPPORTED)):
         assert gate(T=T, ids=IDS + 2) == status
+
+
+@pytest.mark.parametrize("top_k", [9, 10 ** 12, 2 ** 62])
+def test_gate_refuses_more_slots_than_experts_before_it_allocates_them(host_tensors, top_k):
+    with pytest.raises(DGError) as e:
+        ops.dg_moe_gate_topk(torch.zeros((2, 8)), top_k)
+    assert e.value.status == SHAPE
