@@ -287,12 +287,13 @@ __device__ __forceinline__ void up_tiles(const LayerParams &p, int e, int n0, co
 // taking the K blocks in turn: for one token and 8 experts of I = 2048 that
 // makes 1024 workgroups, 16 waves a CU, each with D = 2 blocks of 32 rows (8 KB)
 // in flight. D = 3 changed nothing there (38.6 us) and cost a tenth where K is
-// short (19.6 against 22.9 us at H 2048). With up to 64 pairs every wave lists
-// the expert's pairs for itself, in one ballot and without a barrier.
-template <int NT, int D, bool FEW>
+// short (19.6 against 22.9 us at H 2048). One wave lists the expert's pairs:
+// where every wave listed up to 64 of them for itself, without the barrier, 17
+// cases from 1 to 64 tokens kept their time within 1%.
+template <int NT, int D>
 __global__ __launch_bounds__(kUpThreads) void gate_up_kernel(LayerParams p, int by_pair)
 {
-    __shared__ uint16_t list[FEW ? 64 * kUpWaves : kMaxPairs];
+    __shared__ uint16_t list[kMaxPairs];
     __shared__ int count;
     __shared__ v4f red[kUpWaves * NT * 2][64];
     const int tiles = p.I >> 4;
@@ -300,32 +301,24 @@ __global__ __launch_bounds__(kUpThreads) void gate_up_kernel(LayerParams p, int 
     const int e = slot_expert(p, by_pair, slot);
     if (e < 0)
         return;
-    int np;
-    uint16_t *mine = list;
-    if (FEW) {
-        mine = list + 64 * (threadIdx.x >> 6);
-        np = list_pairs(p, e, threadIdx.x & 63, mine);
-    } else {
-        if (threadIdx.x < 64) {
-            const int n = list_pairs(p, e, threadIdx.x, list);
-            if (threadIdx.x == 0)
-                count = n;
-        }
-        __syncthreads();
-        np = count;
+    if (threadIdx.x < 64) {
+        const int n = list_pairs(p, e, threadIdx.x, list);
+        if (threadIdx.x == 0)
+            count = n;
     }
-    np = __builtin_amdgcn_readfirstlane(np);
-    if (np == 0 || (by_pair && mine[0] != slot))
+    __syncthreads();
+    const int np = __builtin_amdgcn_readfirstlane(count);
+    if (np == 0 || (by_pair && list[0] != slot))
         return;
     int base = 0;
     if (NT >= 4)
         for (; np - base > 32; base += 64)
-            up_tiles<NT, D>(p, e, n0, mine, base, np, red);
+            up_tiles<NT, D>(p, e, n0, list, base, np, red);
     if (NT >= 2)
         for (; np - base > 16; base += 32)
-            up_tiles<NT < 2 ? NT : 2, D>(p, e, n0, mine, base, np, red);
+            up_tiles<NT < 2 ? NT : 2, D>(p, e, n0, list, base, np, red);
     for (; base < np; base += 16)
-        up_tiles<1, D>(p, e, n0, mine, base, np, red);
+        up_tiles<1, D>(p, e, n0, list, base, np, red);
 }
 
 // ---------------------------------------------------------------- down
@@ -482,11 +475,11 @@ __device__ __forceinline__ void down_tiles(const LayerParams &p, int e, int n0, 
 // bytes a pair, little beside an expert's weights. 22.7 us for one token against
 // 34.6 with one workgroup per 16 columns that went through all experts and
 // needed no sum after it; for 64 tokens the whole layer went from 481 to 345 us.
-template <int NT, bool FEW>
+template <int NT>
 __global__ __launch_bounds__(kDownThreads, 4) void down_kernel(LayerParams p, int by_pair)
 {
-    __shared__ u32x4 lds[NT >= 2 ? 4096 : 2048];
-    __shared__ uint16_t list[FEW ? 64 * kDownWaves : kMaxPairs];
+    __shared__ u32x4 lds[NT >= 4 ? 4096 : 2048];  // two buffers of the widest pass
+    __shared__ uint16_t list[kMaxPairs];
     __shared__ int count;
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -495,35 +488,27 @@ __global__ __launch_bounds__(kDownThreads, 4) void down_kernel(LayerParams p, in
     const int e = slot_expert(p, by_pair, slot);
     if (e < 0)
         return;
-    int np;
-    uint16_t *mine = list;
-    if (FEW) {
-        mine = list + 64 * wave;
-        np = list_pairs(p, e, tid & 63, mine);
-    } else {
-        if (tid < 64) {
-            const int n = list_pairs(p, e, tid, list);
-            if (tid == 0)
-                count = n;
-        }
-        __syncthreads();
-        np = count;
+    if (tid < 64) {
+        const int n = list_pairs(p, e, tid, list);
+        if (tid == 0)
+            count = n;
     }
-    np = __builtin_amdgcn_readfirstlane(np);
-    if (np == 0 || (by_pair && mine[0] != slot))
+    __syncthreads();
+    const int np = __builtin_amdgcn_readfirstlane(count);
+    if (np == 0 || (by_pair && list[0] != slot))
         return;
     int base = 0;
     if (NT >= 4) {
         for (; np - base > 24; base += 32)
-            down_tiles<4, 2>(p, e, n0, mine, base, np, lds);
+            down_tiles<4, 2>(p, e, n0, list, base, np, lds);
         for (; np - base > 16; base += 24)
-            down_tiles<3, 2>(p, e, n0, mine, base, np, lds);
+            down_tiles<3, 2>(p, e, n0, list, base, np, lds);
     }
     if (NT >= 2)
         for (; np - base > 8; base += 16)
-            down_tiles<2, 2>(p, e, n0, mine, base, np, lds);
+            down_tiles<2, 2>(p, e, n0, list, base, np, lds);
     for (; base < np; base += 8)
-        down_tiles<1, 4>(p, e, n0, mine, base, np, lds);
+        down_tiles<1, 4>(p, e, n0, list, base, np, lds);
 }
 
 // ---------------------------------------------------------------- sum over a token's slots

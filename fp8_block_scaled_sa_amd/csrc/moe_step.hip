@@ -121,35 +121,30 @@ int64_t layer_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I) { return T *
 // more waves (gate_up: 98 registers for 16 tokens, 130 for 32, 140 for 64). For
 // 64 tokens gate_up keeps one block of K in flight: two (208 registers) took
 // 220 instead of 215 us at 16 tokens an expert and 28 instead of 26 on a share
-// of the experts, but 89 instead of 99 where every expert has 64. The lists
-// without barriers for up to 64 pairs came with the whole-line loads and were
-// not timed apart from them.
+// of the experts, but 89 instead of 99 where every expert has 64. The down
+// kernel with tiles of 16 pairs for T of 64 (top-1, 4 experts) read W2 four
+// times: the layer took 70.6 instead of 58.5 us.
 int launch_layer(const dge::LayerParams &p, hipStream_t stream)
 {
     const int pairs = p.T * p.top_k;
     const int by_pair = pairs < p.E;
     const dim3 grid((unsigned)((by_pair ? pairs : p.E) * (p.I / 16))), block(dge::kUpThreads);
-    const bool few = pairs <= 64;
-    if (p.T <= 16 && few)
-        hipLaunchKernelGGL((dge::gate_up_kernel<1, 2, true>), grid, block, 0, stream, p, by_pair);
-    else if (p.T <= 16)
-        hipLaunchKernelGGL((dge::gate_up_kernel<1, 2, false>), grid, block, 0, stream, p, by_pair);
+    if (p.T <= 16)
+        hipLaunchKernelGGL((dge::gate_up_kernel<1, 2>), grid, block, 0, stream, p, by_pair);
     else if (p.T <= 32)
-        hipLaunchKernelGGL((dge::gate_up_kernel<2, 2, false>), grid, block, 0, stream, p, by_pair);
+        hipLaunchKernelGGL((dge::gate_up_kernel<2, 2>), grid, block, 0, stream, p, by_pair);
     else
-        hipLaunchKernelGGL((dge::gate_up_kernel<4, 1, false>), grid, block, 0, stream, p, by_pair);
+        hipLaunchKernelGGL((dge::gate_up_kernel<4, 1>), grid, block, 0, stream, p, by_pair);
     int st = launched();
     if (st != DG_OK)
         return st;
     const dim3 dgrid((unsigned)((by_pair ? pairs : p.E) * (p.H / dge::kDownRows))), threads(dge::kDownThreads);
-    if (p.T <= 8 && few)
-        hipLaunchKernelGGL((dge::down_kernel<1, true>), dgrid, threads, 0, stream, p, by_pair);
-    else if (few)
-        hipLaunchKernelGGL((dge::down_kernel<2, true>), dgrid, threads, 0, stream, p, by_pair);
+    if (p.T <= 8)
+        hipLaunchKernelGGL((dge::down_kernel<1>), dgrid, threads, 0, stream, p, by_pair);
     else if (p.T <= 16)
-        hipLaunchKernelGGL((dge::down_kernel<2, false>), dgrid, threads, 0, stream, p, by_pair);
+        hipLaunchKernelGGL((dge::down_kernel<2>), dgrid, threads, 0, stream, p, by_pair);
     else
-        hipLaunchKernelGGL((dge::down_kernel<4, false>), dgrid, threads, 0, stream, p, by_pair);
+        hipLaunchKernelGGL((dge::down_kernel<4>), dgrid, threads, 0, stream, p, by_pair);
     if ((st = launched()) != DG_OK)
         return st;
     hipLaunchKernelGGL(dge::sum_slots_kernel, dim3((p.H / 4 + dge::kSumThreads - 1) / dge::kSumThreads, p.T),

@@ -561,7 +561,8 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
  * capture, and they may change between replays. A block's products are summed
  * as in the grouped calls; h keeps 16 bits of mantissa; everything else is
  * fp32 up to the one rounding of out. Of each chosen expert W13 is read once
- * per 64 of its tokens, W2 once per 32. Deterministic: fixed orders of summation.
+ * per 64 of its tokens, W2 once per 32 (again where tokens name it more than
+ * once). Deterministic: fixed orders of summation.
  * For more tokens: the contiguous grouped calls.
  * Constraints: H % 128 == 0, I % 128 == 0; T <= 64, 1 <= top_k <= 16,
  * 1 <= E <= 1024, H and I at most 2^18, min(T top_k, E) * I below 2^28

@@ -6,8 +6,9 @@ import pytest
 import torch
 
 from fp8_block_scaled_sa_amd import ops
+from tests.check import assert_close
 from tests.gpu_util import bits
-from tests.test_gpu_moe_step import BF16, F8, make_layer, normal, run_layer
+from tests.test_gpu_moe_step import BF16, F8, layer_reference, make_layer, normal, run_layer, to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -129,3 +130,13 @@ def test_gate_most_tokens(gpu_device):
     ids = torch.full((2 ** 28 - 16, 1), 7, dtype=torch.int32, device="cuda")
     ops.dg_moe_gate_topk(logits, 1, ids=ids)
     assert not ids.any()
+
+
+# ---------------------------------------------------------------- layer: tiles by the number of tokens
+
+@pytest.mark.parametrize("T,k,E,ids", [(8, 16, 24, "distinct"), (7, 16, 5, "repeated"), (8, 9, 3, "one"),
+                                       (9, 7, 9, "one"), (16, 4, 40, "distinct"), (17, 3, 4, "one"),
+                                       (32, 2, 2, "distinct"), (33, 1, 2, "one"), (64, 1, 100, "distinct")])
+def test_layer_tiles(gpu_device, T, k, E, ids):
+    a = make_layer(T, k, E, 256, 384, 300 + T + k, ids)
+    assert_close(bits(run_layer(a)), to_bf16_bits(layer_reference(*a)), "layer")
