@@ -486,9 +486,11 @@ dg_status dg_moe_unpermute(const void *D, int64_t ldd, int64_t d_rows,
  *   W [K] fp32 or bf16 (w_dtype)
  *   Y [M, K] bf16, row stride ldy;  Q [M, K], row stride ldq;
  *   S logical [M, K/128] at S[m*s_stride_m + kb*s_stride_kb]
- * mean(h^2) is formed in fp32: rows whose squares pass its range (values of
- * about 2^63 and more) come out as zeros, and a row of zeros with eps = 0 as
- * NaN. Non-finite inputs give what the formulas give in R_out and Y; the codes
+ * mean(h^2) is formed in fp32: rows whose squares add up to 2^128 or more come
+ * out as zeros, and a row of zeros with eps = 0 as NaN. Squares below 2^-126 lose
+ * bits and below 2^-150 count as 0: without an eps far above that, rows whose
+ * largest value is below 2^-62 come out inexact, below 2^-75 as infinities.
+ * Non-finite inputs give what the formulas give in R_out and Y; the codes
  * and scales of a row that is not finite in Y are unspecified (no fault).
  * Constraints: 0 < K <= 65536, K % 128 == 0, eps >= 0; M at most 2^26 - 4 for
  * K <= 1024, 2^24 - 1 for K <= 8192, 2^22 - 1 above (DG_ERR_UNSUPPORTED beyond
@@ -559,7 +561,9 @@ dg_status dg_moe_gate_topk(const void *logits, int l_dtype, int64_t ldl,
  *       not matter. Calls that use one workspace must be ordered (one stream).
  * The ids and weights are read on the device: no synchronisation, safe to
  * capture, and they may change between replays. A block's products are summed
- * as in the grouped calls; h keeps 16 bits of mantissa; everything else is
+ * as in the grouped calls; h keeps 16 bits of mantissa, and is -0 where g is
+ * below -88.7, from where exp(-g) is infinite in fp32 (|h| is below 2^-121 |u|
+ * there); an infinite h is infinite, not NaN. Everything else is
  * fp32 up to the one rounding of out. Of each chosen expert W13 is read once
  * per 64 of its tokens, W2 once per 32 (again where tokens name it more than
  * once). Deterministic: fixed orders of summation.

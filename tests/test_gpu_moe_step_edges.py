@@ -8,7 +8,8 @@ import torch
 from fp8_block_scaled_sa_amd import ops
 from tests.check import assert_close
 from tests.gpu_util import bits
-from tests.test_gpu_moe_step import BF16, F8, layer_reference, make_layer, normal, run_layer, to_bf16_bits
+from tests.test_gpu_moe_step import (BF16, F8, check_norm, layer_reference, make_layer, normal, run_layer,
+                                     to_bf16_bits)
 
 pytestmark = pytest.mark.gpu
 
@@ -140,3 +141,36 @@ def test_gate_most_tokens(gpu_device):
 def test_layer_tiles(gpu_device, T, k, E, ids):
     a = make_layer(T, k, E, 256, 384, 300 + T + k, ids)
     assert_close(bits(run_layer(a)), to_bf16_bits(layer_reference(*a)), "layer")
+
+
+# ---------------------------------------------------------------- norm: the ends of the range of its squares
+
+@pytest.mark.parametrize("K", [128, 1152, 8320])
+@pytest.mark.parametrize("exponent", [-62, -40, 40, 56])
+def test_norm_small_and_large_rows(gpu_device, K, exponent):
+    """Without an eps, the rows' size falls out of the norm: as exact at both ends of what the header names."""
+    x = normal((5, K), K, False).clamp(-3, 3)
+    x[:, 0] = 1                                      # the largest value is at least that
+    x = x * 2.0 ** exponent
+    w = 1 + 0.1 * normal((K,), 2, False)
+    q, s, _, y = ops.dg_fp8_rmsnorm_quantize_1x128(x.cuda(), w.cuda(), 0.0, normed=True)
+    check_norm(x, w, 0.0, None, q, s, None, y)
+
+
+def test_norm_past_the_ends(gpu_device):
+    x = torch.ones((3, 256))
+    x[0] *= 2.0 ** 64                                # squares add up to more than fp32 holds
+    x[1] *= 2.0 ** -80                               # and to nothing
+    q, s, _, y = ops.dg_fp8_rmsnorm_quantize_1x128(x.cuda(), torch.ones(256, device="cuda"), 0.0, normed=True)
+    assert not q[0].any() and bool((s[0] == 1).all()) and not y[0].any()
+    assert bool((y[1] == math.inf).all()) and bool((y[2] == 1).all())
+
+
+def test_layer_far_negative_gate(gpu_device):
+    """g = -128: exp(-g) is infinite, silu(g) is -0, and so is every product with it: no NaN."""
+    H, I = 128, 128  # noqa: E741
+    code = lambda v, *s: torch.full(s, float(v)).to(F8).view(torch.uint8)  # noqa: E731
+    w13 = torch.cat([code(-1, 1, I, H), code(1, 1, I, H)], 1)
+    a = [t.cuda() for t in (code(1, 2, H), torch.ones((2, 1)), w13, torch.ones((1, 2, 1)), code(1, 1, H, I),
+                            torch.ones((1, 1, 1)), torch.zeros((2, 1), dtype=torch.int32), torch.ones((2, 1)))]
+    assert bool((run_layer(a) == 0).all())
