@@ -29,12 +29,14 @@
 // comes between the products but the last one to bf16. The second product
 // takes them as 8 + 8 columns of one operand and adds the two results.
 //
-// Measured for H 7168, I 2048, in graph replays under the kernel trace:
-//   1 token, 8 of 32 experts:    67 us (first kernel 38.5, second 22.7), 352 MB
-//   8 tokens, 8 of 32:          230 us (first kernel 137), 1268 MB
-//   64 tokens, 8 of 32:         345 us (first kernel 215 to 220), 1410 MB
-// With one tile of tokens the kernels run at 5 to 6 TB/s, near what a kernel
-// that only reads reaches; with more, they fall to 4 to 4.4 TB/s: in the first
+// Measured for H 7168, I 2048, graph replays over three inputs in turn (in
+// brackets the first and the second kernel's median under the kernel trace):
+//   1 token, 8 of 32 experts:    65 us (38.0, 23.7), 352 MB
+//   8 tokens, 8 of 32:          226 us (136, 86), 1268 MB
+//   16 tokens, 8 of 32:         249 us (147, 90), 1396 MB
+//   64 tokens, 8 of 32:         337 us (215, 117), 1411 MB
+// With one tile of tokens the layer runs at 5.4 to 5.6 TB/s, near what a kernel
+// that only reads reaches; with more, it falls to 4.1 or 4.2 TB/s: in the first
 // the waves split K and each reads its own tokens' blocks from L2, two loads a
 // tile beside the four of the weights, in the second the chunks get shorter.
 #pragma once
@@ -472,9 +474,9 @@ __device__ __forceinline__ void down_tiles(const LayerParams &p, int e, int n0, 
 // One workgroup per 128 columns of out and expert, 16 columns a wave: 448
 // workgroups of 8 waves for one token, 8 experts and H = 7168, two a CU (so at
 // most 128 registers). Every pair's product goes to the workspace: fp32, 4 H
-// bytes a pair, little beside an expert's weights. 22.7 us for one token against
-// 34.6 with one workgroup per 16 columns that went through all experts and
-// needed no sum after it; for 64 tokens the whole layer went from 481 to 345 us.
+// bytes a pair, little beside an expert's weights. One workgroup per 16 columns
+// that went through all experts needed no sum after it, but the layer took 74
+// instead of 67 us for one token and 481 instead of 345 for 64.
 template <int NT>
 __global__ __launch_bounds__(kDownThreads, 4) void down_kernel(LayerParams p, int by_pair)
 {

@@ -14,8 +14,10 @@
 // DPP row, four steps and no LDS; a lane holds E / 16 logits in registers. The
 // logits are read once, but the vector instructions of the rounds bound it, not
 // HBM: 8192 tokens x 256 experts, 8 chosen, fp32: 6.8 us with the softmax over
-// all (8.9 MB, 1.3 TB/s), 5.9 us over the chosen; 64 experts 4.1 us, 512
-// experts 10.6 us; one token of 32 experts 3.3 us, a launch.
+// all (8.9 MB, 1.3 TB/s), 6.0 us over the chosen; 64 experts 4.1 us, 512
+// experts 10.6 us; one token of 32 experts 3.2 us, a launch (graph replays over
+// three inputs in turn; 6.2 us instead of 6.8 where the calls are eager, one
+// after the other).
 #pragma once
 
 #include <hip/hip_runtime.h>

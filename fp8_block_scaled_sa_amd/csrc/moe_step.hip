@@ -44,9 +44,14 @@ bool is_float_type(int t) { return t == DG_DTYPE_F32 || t == DG_DTYPE_BF16; }
 // Threads that a row takes (see launch_norm).
 int64_t norm_row_threads(int64_t K) { return K <= 1024 ? 64 : K <= 8192 ? 256 : 1024; }
 
-// Row layouts of the norm kernel: ROW threads per row, NC chunks of 8 a thread:
-// the fewest threads whose registers hold the row, so that short rows share a
-// workgroup (8192 x 1024 runs at 5.4 TB/s, 8192 x 4096 too).
+// Row layouts of the norm kernel: ROW threads per row, NC chunks of 8 a thread.
+// Short rows share a workgroup; past 1024 elements a row has one to itself, of
+// 256 threads while 4 chunks a thread hold it, then of 1024. A layout holds up
+// to twice, the first of 1024 threads up to four times the row that it is used
+// for; the loads past a row's end repeat its last chunk, which the cache holds.
+// bf16, residual and normed rows: 8192 x 1024 runs at 5.2 TB/s, x 4096 at 5.3,
+// x 5120 and x 7168 at 5.0, x 8192 at 4.4, x 8320 at 4.6, x 12288 at 5.2, x
+// 16384 at 5.4, 4096 x 32768 and 2048 x 65536 at 4.9.
 template <bool XBF16, int RES>
 int launch_norm(const dgn::NormParams &p, hipStream_t stream)
 {

@@ -13,8 +13,8 @@
 // HBM bounds it for many rows: x, r and w are read once, the row stays in
 // registers between the sum and the output, and what is written is written in
 // 16-byte stores (codes: 8). 8192 x 7168, bf16 in, residual and normed rows:
-// 106.9 us for 530 MB, 4.96 TB/s, the rate of a 2 GiB copy (4.93 TB/s); 2048
-// rows, which the last-level cache holds in part, 22.4 us. One row: 4.7 us, a
+// 105.5 us for 530 MB, 5.03 TB/s, the rate of a 2 GiB copy (4.93 TB/s); 2048
+// rows 29.7 us (graph replays over three inputs in turn). One row: 4.8 us, a
 // launch and the latency of two dependent reads. 16 lanes hold a 1x128 block
 // (8 elements each), so the block's amax and the row's sum are DPP steps, and
 // the rows are dealt to the XCDs in contiguous ranges, as the quantiser's are,

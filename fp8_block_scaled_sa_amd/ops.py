@@ -4,6 +4,7 @@ Argument marshalling only: every step of the GEMM runs in the HIP library.
 Operands are CUDA (HIP) tensors: e4m3 codes as ``torch.uint8`` or
 ``torch.float8_e4m3fn``, scales ``torch.float32`` (any strides, read through
 the logical index), routing arrays ``torch.int32``, output ``torch.bfloat16``.
+All of a call's tensors are on the current device.
 The call is enqueued on torch's current stream unless ``stream`` is given (a
 torch.cuda.Stream, or a raw handle as an int). Outputs that the call allocates
 belong to the stream that writes them, and may be dropped at any time on either
