@@ -58,6 +58,13 @@ SIGNATURES = {
                                         _p, _i64, _i64, _p, _i64, _i64, _i64, _p, _p, _p, _i64,
                                         _i64, _i64, _i64, _i64, _i64, _p, _i64, _p]),
     "dg_fp8_moe_layer_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64, _i64]),
+    "dg_fp8_rope_cache_write": (ctypes.c_int, [_p, _i64, _i64, _p, _i64, _i64, _i64, _p, _i64, _i64, _p, _i64, _i64,
+                                               ctypes.c_int, _p, _p, _i64, ctypes.c_int, ctypes.c_float, _p, _p, _p,
+                                               _i64, _p]),
+    "dg_fp8_cache_read": (ctypes.c_int, [_p, _p, _p, ctypes.c_int, _i64, _i64, _i64, _p]),
+    "dg_fp8_paged_attention": (ctypes.c_int, [_p, _i64, _i64, _i64, _p, _p, _p, _i64, _i64, _p, _p, _i64, _i64, _i64,
+                                              ctypes.c_float, _i64, _p, _i64, _i64, _p, _i64, _p]),
+    "dg_fp8_paged_attention_workspace_bytes": (ctypes.c_int64, [_i64, _i64, _i64, _i64, _i64, _i64]),
     "dg_moe_route_contiguous": (ctypes.c_int, [_p, _i64, _i64, _p, _p, _p, _p, _i64, _p]),
     "dg_moe_contiguous_max_rows": (ctypes.c_int64, [_i64, _i64]),
     "dg_moe_unpermute": (ctypes.c_int, [_p, _i64, _i64, _p, _i64, _i64, _p, _i64, _p]),

@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = [os.path.join(HERE, "csrc", "library.hip")]
 DEPS = SOURCES + [os.path.join(HERE, "csrc", f) for f in (
-    "dg_fp8.hip", "kernels.hpp", "quant.hpp", "moe.hpp", "moe_step.hip", "norm.hpp", "gate.hpp", "experts.hpp")
+    "dg_fp8.hip", "kernels.hpp", "quant.hpp", "moe.hpp", "moe_step.hip", "norm.hpp", "gate.hpp", "experts.hpp",
+    "attention_step.hip", "cache.hpp", "attend.hpp")
         ] + [os.path.join(ROOT, "include", "dg_fp8.h")]
 LIBRARY = os.path.join(HERE, "libdg_fp8.so")
 DEBUG_LIBRARY = os.path.join(HERE, "libdg_fp8_O1.so")

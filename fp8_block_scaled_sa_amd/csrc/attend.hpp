@@ -1,0 +1,1107 @@
+// attend.hpp -- gfx950 kernels of attention over a paged cache of e4m3 codes.
+//
+// A sequence's new tokens i = 0 .. m - 1 are the last m of its n tokens. Token
+// i, at position pos = n - m + i, sees the keys j <= pos (and j > pos - window):
+//   x_ij = scale sK_j (q_i . K_j)          o_i = sum_j p_ij sV_j V_j / sum_j p_ij,   p_ij = exp(x_ij)
+// with codes K_j, V_j and one fp32 scale for each key and head. The query heads
+// of a group share a key head: their rows (token i, head of the group) stand
+// side by side as columns of the same products, so the cache is read once for
+// all of them.
+//
+// Roundings. The codes are exact in bf16 and fp16, so the products q . K are
+// exact bf16 products summed in fp32; both scales are applied in fp32. The
+// second product takes fp16: its weights p sV, whose rounding to 11 bits is the
+// only one before the output's (bf16 weights, with 8 bits, would add as much
+// error as the output's own rounding). fp16's range is kept by two references:
+// p is exp2(x - m) with a running m that lies at most 8 below the largest x
+// seen, and sV is divided by a power of two e that is at least the largest sV
+// seen; the weights are scaled by 2^7, so they reach up to 2^15, are rounded to
+// 11 bits down to 2^-29 of that and lost below 2^-40. Sums, references and the
+// outputs before their rounding are fp32.
+//
+// Masked keys never count, whatever their rows hold: their weight is set to 0,
+// and codes of V that are NaN there are replaced (0 * NaN would be NaN). A row
+// that sees a NaN code comes out as NaN: in that column, or in all of them where
+// the code lies in a tile that is masked for some rows.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cache.hpp"
+
+namespace dga {
+
+using dgc::Divisor;
+using dgc::quotient;
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kThreads = 256;
+constexpr int kUnit = 128;               // keys that a workgroup of the few-rows kernel takes at once
+constexpr int kFewRows = 64;             // most rows (tokens x heads of a group) of its sequences
+constexpr int kTileRows = 128;           // rows of a workgroup of the many-rows kernel
+constexpr int kTileKeys = 64;            // keys that it takes at once
+constexpr float kNoMax = -1e30f;         // below every x that counts; finite, so that differences are
+constexpr float kSlack = 8.0f;           // how far x may pass its reference
+constexpr int kNoScale = -100;           // exponent below which sV's reference does not go
+
+// One of the two caches: rows of 16-byte multiples, addressed in units of 16 bytes.
+struct Rows {
+    const uint8_t *codes;
+    uint32_t page16, token16;
+    int64_t head;
+    const float *scales;
+    int64_t s_page, s_token, s_head;
+};
+
+struct AttendParams {
+    const uint16_t *Q;                   // bf16 [T, heads * group, D]
+    int64_t q_t, q_h;
+    uint16_t *out;                       // bf16 [T, heads * group, D]
+    int64_t o_t, o_h;
+    Rows k, v;
+    const int32_t *table;                // [B, width]
+    int64_t table_stride;
+    int width, pages;
+    Divisor page;                        // tokens of a page
+    const int32_t *kv_lens, *q_starts;
+    int B, T, heads, max_q_len, window;
+    Divisor group;                       // query heads of a key head
+    float scale_log2;                    // scale / ln 2
+    int few_rows;                        // sequences of up to so many rows are the few-rows kernel's
+    int target, min_units;               // few rows: workgroups aimed at, and units that one takes at least
+    int splits;                          // many rows: workgroups that share a tile's keys
+    int part_rows;                       // rows of a piece's partial result
+    float *part_o;                       // [piece][part_rows][D], sums over p sV V
+    float *part_ml;                      // [piece][part_rows][2], reference and sum of p
+};
+
+// A sequence as the device arrays give it; anything out of range counts as nothing.
+struct Sequence {
+    int start, m, n, low;                // first row of Q, new tokens, tokens, first key that any of them sees
+    int rows;                            // 0: none, or more tokens than max_q_len
+};
+
+__device__ __forceinline__ Sequence sequence(const AttendParams &p, int b)
+{
+    Sequence s;
+    s.start = min(max(p.q_starts[b], 0), p.T);
+    const int end = min(max(p.q_starts[b + 1], s.start), p.T);
+    s.m = end - s.start;
+    s.n = (int)min((int64_t)max(p.kv_lens[b], 0), (int64_t)p.width * p.page.d);
+    s.low = p.window ? max(0, s.n - s.m + 1 - p.window) : 0;
+    s.rows = s.m <= p.max_q_len ? s.m * (int)p.group.d : 0;
+    return s;
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int shifted(int v)
+{
+    return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+
+// Inclusive sums over the 64 lanes: shifts within rows of 16, then the rows' totals onwards.
+__device__ __forceinline__ int scan(int v)
+{
+    v += shifted<0x111, 0xF>(v);
+    v += shifted<0x112, 0xF>(v);
+    v += shifted<0x114, 0xF>(v);
+    v += shifted<0x118, 0xF>(v);
+    v += shifted<0x142, 0xA>(v);
+    return v + shifted<0x143, 0xC>(v);
+}
+
+__device__ __forceinline__ int lane_int(int v, int lane) { return __builtin_amdgcn_readlane(v, lane); }
+
+// Orders a wave's LDS accesses for the compiler; the hardware runs them in order.
+__device__ __forceinline__ void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+__device__ __forceinline__ float max_across(float v)  // over the lanes l, l ^ 16, l ^ 32, l ^ 48
+{
+    v = fmaxf(v, __shfl_xor(v, 16, 64));
+    return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+
+__device__ __forceinline__ float sum_across(float v)
+{
+    v += __shfl_xor(v, 16, 64);
+    return v + __shfl_xor(v, 32, 64);
+}
+
+// Two codes (the low or high half of a dword) as packed bf16 or fp16, exactly.
+template <bool HIGH>
+__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t codes)
+{
+    return __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(codes, 1.0f, HIGH));
+}
+
+template <bool HIGH>
+__device__ __forceinline__ uint32_t codes_to_f16(uint32_t codes)
+{
+    return __builtin_bit_cast(uint32_t, (f16x2)__builtin_amdgcn_cvt_scalef32_pk_f16_fp8(codes, 1.0f, HIGH));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    const f16x2 v = {(_Float16)a, (_Float16)b};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Exponent of the least power of two that is not below s (finite, at least 0): up to 128, for which power_of_2 is infinite.
+__device__ __forceinline__ int exponent_above(float s)
+{
+    const uint32_t bits = __float_as_uint(s);
+    return (int)(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0);
+}
+
+__device__ __forceinline__ bool has_nan_code(uint32_t codes)  // 0x7f or 0xff among four
+{
+    return (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+}
+
+// The codes with NaNs replaced by zeros.
+__device__ __forceinline__ uint32_t without_nan_codes(uint32_t codes)
+{
+    const uint32_t nan = (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+    return codes & ~(nan * 0xffu);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// Where a piece of the few-rows kernel lies.
+struct Piece {
+    Sequence s;
+    int b, head, first, units;           // units [first, first + units) of the sequence's
+    int pieces, index;                   // pieces of each of its heads; this one's number among the launch's
+};
+
+// Units of kUnit keys that a sequence's rows read, counted from the 32 keys that hold the first one.
+__device__ __forceinline__ int units_of(const Sequence &s)
+{
+    return max(0, (s.n - (s.low & ~31) + kUnit - 1) / kUnit);
+}
+
+// The launch's keys are cut into pieces of about the same size, so that uneven
+// sequences fill the CUs evenly: `chunk` units a piece, as many as give
+// p.target pieces in all. Each wave finds its piece by itself from the
+// sequences' lengths (64 at a time, a scan over the lanes), without a planning
+// launch and without the host knowing them. visit(b0, pieces, before) is given
+// the sequences 64 at a time, with each lane's pieces (all heads) and those of
+// the lanes before; it returns whether to stop.
+template <typename Visit>
+__device__ __forceinline__ void for_pieces(const AttendParams &p, Visit visit)
+{
+    const int lane = threadIdx.x & 63;
+    const auto units = [&](int b, Sequence &s) {
+        s.rows = 0;
+        if (b < p.B)
+            s = sequence(p, b);
+        return s.rows > 0 && s.rows <= p.few_rows ? units_of(s) : -1;
+    };
+    Sequence s;
+    int all = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64)
+        all += max(0, units(b0 + lane, s));
+    all = lane_int(scan(all), 63) * p.heads;
+    const int chunk = max(p.min_units, (all + p.target - 1) / p.target);
+    int before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64) {
+        const int u = units(b0 + lane, s);
+        const int pieces = u < 0 ? 0 : max(1, (u + chunk - 1) / chunk);
+        const int upto = scan(pieces * p.heads);
+        if (visit(b0, s, u, pieces, before + upto - pieces * p.heads))
+            return;
+        before += lane_int(upto, 63);
+    }
+}
+
+__device__ __forceinline__ bool find_piece(const AttendParams &p, int index, Piece &w)
+{
+    bool found = false;
+    for_pieces(p, [&](int b0, const Sequence &s, int u, int pieces, int before) {
+        const uint64_t mine = __ballot(index >= before && index < before + pieces * p.heads);
+        if (!mine)
+            return false;
+        const int lane = __builtin_ctzll(mine);
+        w.b = b0 + lane;
+        w.s.start = lane_int(s.start, lane);
+        w.s.m = lane_int(s.m, lane);
+        w.s.n = lane_int(s.n, lane);
+        w.s.low = lane_int(s.low, lane);
+        w.s.rows = lane_int(s.rows, lane);
+        w.pieces = lane_int(pieces, lane);
+        w.index = index;
+        const int at = index - lane_int(before, lane), all = lane_int(u, lane);
+        // Heads next to each other: they read the same pages.
+        const int i = at / p.heads;
+        w.head = at - i * p.heads;
+        w.first = (int)((int64_t)all * i / w.pieces);
+        w.units = (int)((int64_t)all * (i + 1) / w.pieces) - w.first;
+        found = true;
+        return true;
+    });
+    return found;
+}
+
+// Writes D / 16 values of a finished row.
+template <int N>
+__device__ __forceinline__ void store_bf16(uint16_t *to, const float *v)
+{
+    if (N == 8)
+        *(u32x4 *)to = u32x4{dgn::pack_bf16(v[0], v[1]), dgn::pack_bf16(v[2], v[3]), dgn::pack_bf16(v[N - 4], v[N - 3]),
+                             dgn::pack_bf16(v[N - 2], v[N - 1])};
+    else
+        *(u32x2 *)to = u32x2{dgn::pack_bf16(v[0], v[1]), dgn::pack_bf16(v[2], v[3])};
+}
+
+// One piece: up to 16 NT rows of one key head over some units of its keys.
+//
+// Bound by the bytes of the cache. Each wave streams 32 of a unit's 128 keys
+// from HBM straight into the operands' registers, the next unit's loads in
+// flight while it computes one; nothing goes through LDS but addresses and
+// scales. The products are transposed, so that each lane keeps one row's
+// statistics and the first product's output is the second one's operand as it
+// stands: S^T = K Q^T (16x16x32 bf16: lane l holds key l % 16 of K and 32 of
+// its codes, and receives row l % 16, keys 4 (l / 16) + i), O^T = V^T P^T (the
+// order of keys within an operand is free, as long as both have the same: lane
+// group g takes the keys 4 g + i and 16 + 4 g + i; column c of V^T's tile t
+// stands for element (D / 16) c + t, so that a lane reads consecutive codes).
+// K's loads cover whole 128-byte lines, 8 lanes a row, and lanes l and l ^ 8
+// then exchange halves. V's pairs of keys are brought together byte by byte
+// (v_perm) before the conversion, which takes two codes at once.
+template <int D, int NT>
+__global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
+{
+    constexpr int DT = D / 16;           // codes of a key in a lane of V, and tiles of O^T
+    constexpr int KS = D / 32;           // matrix instructions of a tile of S^T
+    constexpr int KL = D / 64;           // 16-byte loads of K in a lane, for 16 keys
+    constexpr int VW = D / 64;           // dwords of V in a lane, for one key
+    constexpr int kPad = D + 4;
+    __shared__ uint32_t offsets[4][64];  // of a wave's 32 keys in K, then in V
+    __shared__ __align__(16) float scales[4][64];
+    __shared__ float refs[4][2][16 * NT];
+    __shared__ __align__(16) float sums[4][16][kPad];
+
+    Piece w;
+    if (!find_piece(p, blockIdx.x, w))
+        return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int c = lane & 15, g = lane >> 4;
+    const int key0 = (w.s.low & ~31) + w.first * kUnit + 32 * wave;    // this wave's first key
+    const int units = w.units;
+    const int32_t *table = p.table + w.b * p.table_stride;
+    const uint8_t *kbase = p.k.codes + w.head * p.k.head, *vbase = p.v.codes + w.head * p.v.head;
+    const bool values = lane >= 32;      // lanes 0..31 look after K's rows, 32..63 after V's
+    const float *sbase = values ? p.v.scales + w.head * p.v.s_head : p.k.scales + w.head * p.k.s_head;
+
+    bf16x8 q[NT][KS];
+    int pos[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = 16 * nt + c;
+        const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+        const bool present = r < w.s.rows;
+        pos[nt] = present ? w.s.n - w.s.m + token : -1;
+        const uint16_t *row = p.Q + (int64_t)(w.s.start + token) * p.q_t + (int64_t)(w.head * (int)p.group.d + h) * p.q_h;
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+            u32x4 v = {0, 0, 0, 0};
+            if (present)
+                v = *(const u32x4 *)(row + (D / 4) * g + 8 * t);
+            q[nt][t] = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+
+    // Steps of the pipeline, by unit: the pages two units ahead, rows and scales one ahead.
+    const auto load_page = [&](int u) {
+        const int j = key0 + u * kUnit + (lane & 31);
+        return u < units && j >= w.s.low && j < w.s.n ? table[quotient(j, p.page)] : -1;
+    };
+    u32x4 kraw[2][KL];
+    uint32_t vraw[8][VW];
+    float scale = 0.0f;
+    bool valid = false;
+    const auto load_rows = [&](int u, int page) {
+        const int j = key0 + u * kUnit + (lane & 31);
+        valid = page >= 0 && page < p.pages;
+        // A key that is not there reads slot 0, and is masked later.
+        const uint32_t pg = valid ? page : 0, token = valid ? j - quotient(j, p.page) * p.page.d : 0;
+        offsets[wave][lane] = values ? pg * p.v.page16 + token * p.v.token16 : pg * p.k.page16 + token * p.k.token16;
+        scale = values ? sbase[pg * p.v.s_page + token * p.v.s_token] : sbase[pg * p.k.s_page + token * p.k.s_token];
+        wave_sync();
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            if (D == 128) {
+#pragma unroll
+                for (int l = 0; l < KL; ++l)
+                    kraw[sub][l] = __builtin_nontemporal_load(
+                        (const u32x4 *)(kbase + 16 * (int64_t)offsets[wave][16 * sub + 8 * l + (lane & 7)] + 32 * g +
+                                        16 * ((lane >> 3) & 1)));
+            } else {
+                kraw[sub][0] = __builtin_nontemporal_load(
+                    (const u32x4 *)(kbase + 16 * (int64_t)offsets[wave][16 * sub + c] + 16 * g));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *at = vbase + 16 * (int64_t)offsets[wave][32 + 16 * sub + 4 * g + i] + DT * c;
+                if (VW == 2) {
+                    const u32x2 v = __builtin_nontemporal_load((const u32x2 *)at);
+                    vraw[4 * sub + i][0] = v[0];
+                    vraw[4 * sub + i][VW - 1] = v[1];
+                } else {
+                    vraw[4 * sub + i][0] = __builtin_nontemporal_load((const uint32_t *)at);
+                }
+            }
+        }
+        wave_sync();
+    };
+
+    f32x4 o[NT][DT];
+    float ref[NT], sum[NT];
+    int exponent = kNoScale;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        ref[nt] = kNoMax;
+        sum[nt] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < DT; ++t)
+            o[nt][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    int page = load_page(0);
+    if (units > 0)
+        load_rows(0, page);
+    page = load_page(1);
+    for (int u = 0; u < units; ++u) {
+        // This unit's operands leave the load registers, then the next unit's loads start.
+        const uint32_t there = (uint32_t)__ballot(valid);
+        const float found = scale;
+        const int first = key0 + u * kUnit;
+        const bool masked = there != 0xffffffffu || first + 31 > w.s.n - w.s.m ||
+                            (p.window && first <= w.s.n - 1 - p.window);
+        u32x4 k[2][KL];
+        uint32_t v[8][VW];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+            for (int l = 0; l < KL; ++l)
+                k[sub][l] = kraw[sub][l];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int l = 0; l < VW; ++l)
+                v[i][l] = vraw[i][l];
+        if (u + 1 < units) {
+            load_rows(u + 1, page);
+            page = load_page(u + 2);
+        }
+
+        // V's reference covers the unit's finite scales.
+        const float size = fabsf(found);
+        const bool counts = values && (there >> (lane & 31) & 1) && size < __builtin_inff();
+        if (__ballot(counts && size > power_of_2(exponent))) {
+            float most = counts ? size : 0.0f;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2)
+                most = fmaxf(most, __shfl_xor(most, d, 64));
+            const int e = max(exponent_above(most), exponent);
+            const float shrink = exponent - e < -126 ? 0.0f : power_of_2(exponent - e);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+                    o[nt][t] *= shrink;
+            exponent = e;
+        }
+        scales[wave][lane] = values ? found * power_of_2(7 - exponent) : found * p.scale_log2;
+        wave_sync();
+        float ks[8], vs[8];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            const f32x4 a = *(const f32x4 *)&scales[wave][16 * sub + 4 * g];
+            const f32x4 b = *(const f32x4 *)&scales[wave][32 + 16 * sub + 4 * g];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ks[4 * sub + i] = a[i];
+                vs[4 * sub + i] = b[i];
+            }
+        }
+        wave_sync();
+
+        if (masked) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const bool here = there >> (16 * (i / 4) + 4 * g + i % 4) & 1;
+                bool nan = false;
+#pragma unroll
+                for (int l = 0; l < VW; ++l) {
+                    nan |= has_nan_code(v[i][l]);
+                    v[i][l] = here ? without_nan_codes(v[i][l]) : 0;
+                }
+                if ((__ballot(nan) >> (16 * g) & 0xffff) != 0)
+                    vs[i] = __builtin_nanf("");
+            }
+        }
+
+        // S^T, 2 x 16 keys.
+        f32x4 s[NT][2];
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            uint32_t row[8];
+            if (D == 128) {
+                // From load order to operand order: lanes 8..15 of each 16 take the first from lane ^ 8's second.
+                const bool upper = lane & 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a = k[sub][0][i], b = k[sub][KL - 1][i];
+                    const uint32_t give = upper ? a : b;
+                    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
+                    row[i] = upper ? got : a;
+                    row[4 + i] = upper ? b : got;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    row[i] = k[sub][0][i];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                s[nt][sub] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int t = 0; t < KS; ++t) {
+                const u32x4 a = {codes_to_bf16<false>(row[2 * t]), codes_to_bf16<true>(row[2 * t]),
+                                 codes_to_bf16<false>(row[2 * t + 1]), codes_to_bf16<true>(row[2 * t + 1])};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    s[nt][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), q[nt][t],
+                                                                         s[nt][sub], 0, 0, 0);
+            }
+        }
+
+        // Weights.
+        f16x8 weights[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            uint32_t seen = 0xff;
+            if (masked) {
+                seen = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = 16 * (i / 4) + 4 * g + i % 4, j = first + at;
+                    const bool sees = (there >> at & 1) && j <= pos[nt] && (!p.window || j > pos[nt] - p.window);
+                    seen |= (uint32_t)sees << i;
+                }
+            }
+            const auto shift = [&](float *x) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = __builtin_fmaf(s[nt][i / 4][i % 4], ks[i], -ref[nt]);
+                    if (masked)
+                        x[i] = seen >> i & 1 ? x[i] : -__builtin_inff();
+                }
+            };
+            float x[8];
+            shift(x);
+            float most = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                most = fmaxf(most, x[i]);
+            if (__ballot(most > kSlack)) {
+                float top = kNoMax;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (seen >> i & 1)
+                        top = fmaxf(top, s[nt][i / 4][i % 4] * ks[i]);
+                top = fmaxf(max_across(top), ref[nt]);
+                const float shrink = __builtin_amdgcn_exp2f(ref[nt] - top);
+                sum[nt] *= shrink;
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+                    o[nt][t] *= shrink;
+                ref[nt] = top;
+                shift(x);
+            }
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float e = __builtin_amdgcn_exp2f(x[i]);
+                sum[nt] += e;
+                y[i] = e * vs[i];
+                if (masked)
+                    y[i] = seen >> i & 1 ? y[i] : 0.0f;
+            }
+            const u32x4 packed = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
+            weights[nt] = __builtin_bit_cast(f16x8, packed);
+        }
+
+        // O^T += V^T P^T
+#pragma unroll
+        for (int l = 0; l < VW; ++l) {
+            uint32_t low[4], high[4];    // elements 0, 1 and 2, 3 of the dword, each for two keys
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                low[i] = __builtin_amdgcn_perm(v[2 * i + 1][l], v[2 * i][l], 0x05010400);
+                high[i] = __builtin_amdgcn_perm(v[2 * i + 1][l], v[2 * i][l], 0x07030602);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                u32x4 a;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t both = d < 2 ? low[i] : high[i];
+                    a[i] = d % 2 ? codes_to_f16<true>(both) : codes_to_f16<false>(both);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    o[nt][4 * l + d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), weights[nt],
+                                                                              o[nt][4 * l + d], 0, 0, 0);
+            }
+        }
+    }
+
+    // The four waves' sums, over their largest reference.
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const float all = sum_across(sum[nt]);
+        if (g == 0) {
+            refs[wave][0][16 * nt + c] = ref[nt];
+            refs[wave][1][16 * nt + c] = all;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        if (16 * nt >= w.s.rows)
+            break;
+        float top = kNoMax;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            top = fmaxf(top, refs[i][0][16 * nt + c]);
+        const float factor = __builtin_amdgcn_exp2f(ref[nt] - top) * power_of_2(exponent - 7);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < DT; t += 4)
+                *(f32x4 *)&sums[wave][c][(4 * g + i) * DT + t] =
+                    f32x4{o[nt][t][i], o[nt][t + 1][i], o[nt][t + 2][i], o[nt][t + 3][i]} * factor;
+        __syncthreads();
+        const int row = threadIdx.x >> 4, r = 16 * nt + row, col = DT * (threadIdx.x & 15);
+        if (r < w.s.rows) {
+            float most = kNoMax, total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                most = fmaxf(most, refs[i][0][r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                total += refs[i][1][r] * __builtin_amdgcn_exp2f(refs[i][0][r] - most);
+            float y[DT];
+#pragma unroll
+            for (int t = 0; t < DT; ++t)
+                y[t] = (sums[0][row][col + t] + sums[1][row][col + t]) + (sums[2][row][col + t] + sums[3][row][col + t]);
+            if (w.pieces == 1) {
+                const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+#pragma unroll
+                for (int t = 0; t < DT; ++t)
+                    y[t] = total == 0.0f ? 0.0f : y[t] / total;
+                store_bf16<DT>(p.out + (int64_t)(w.s.start + token) * p.o_t +
+                                   (int64_t)(w.head * (int)p.group.d + h) * p.o_h + col, y);
+            } else {
+                const int64_t at = (int64_t)w.index * p.part_rows + r;
+#pragma unroll
+                for (int t = 0; t < DT; t += 4)
+                    *(f32x4 *)(p.part_o + at * D + col + t) = f32x4{y[t], y[t + 1], y[t + 2], y[t + 3]};
+                if (col == 0)
+                    *(f32x2 *)(p.part_ml + 2 * at) = f32x2{most, total};
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Joins `count` partial results of a row, the i-th at index(i), and writes it:
+// the four waves of a workgroup take every fourth one each.
+template <int D, typename Index>
+__device__ __forceinline__ void join(const AttendParams &p, int count, Index index, uint16_t *to)
+{
+    constexpr int E = D / 64;
+    __shared__ float part[4][D + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float top = kNoMax;
+    for (int i = lane; i < count; i += 64)
+        top = fmaxf(top, p.part_ml[2 * index(i)]);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        top = fmaxf(top, __shfl_xor(top, d, 64));
+    float total = 0.0f, y[E] = {};
+#pragma unroll 4
+    for (int i = wave; i < count; i += 4) {
+        const int64_t at = index(i);
+        const f32x2 ml = *(const f32x2 *)(p.part_ml + 2 * at);
+        const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
+        total = __builtin_fmaf(ml[1], weight, total);
+        const float *o = p.part_o + at * D + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            y[e] = __builtin_fmaf(o[e], weight, y[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        part[wave][E * lane + e] = y[e];
+    if (lane == 0)
+        part[wave][D] = total;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        total = (part[0][D] + part[1][D]) + (part[2][D] + part[3][D]);
+        float v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int d = 2 * threadIdx.x + e;
+            const float all = (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]);
+            v[e] = total == 0.0f ? 0.0f : all / total;
+        }
+        *(uint32_t *)(to + 2 * threadIdx.x) = dgn::pack_bf16(v[0], v[1]);
+    }
+}
+
+// One row of a sequence (blockIdx.x: sequence and key head, blockIdx.y: row) that several pieces share.
+template <int D>
+__global__ __launch_bounds__(kThreads) void join_few_kernel(AttendParams p)
+{
+    const int r = blockIdx.y, b = blockIdx.x / p.heads, head = blockIdx.x - b * p.heads;
+    int pieces = 0, before = 0, start = 0, rows = 0;
+    for_pieces(p, [&](int b0, const Sequence &s, int, int n, int first) {
+        if (b >= b0 + 64)
+            return false;
+        pieces = lane_int(n, b - b0);
+        before = lane_int(first, b - b0);
+        start = lane_int(s.start, b - b0);
+        rows = lane_int(s.rows, b - b0);
+        return true;
+    });
+    if (pieces < 2 || r >= rows)
+        return;
+    const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+    join<D>(p, pieces, [&](int i) { return (int64_t)(before + i * p.heads + head) * p.part_rows + r; },
+            p.out + (int64_t)(start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h);
+}
+
+// ---------------------------------------------------------------- many rows
+
+// A tile of rows: which sequence's, and the first of its rows.
+struct Tile {
+    Sequence s;
+    int b, first;
+};
+
+// The index-th tile, the last (longest) tiles of a sequence first.
+__device__ __forceinline__ bool find_tile(const AttendParams &p, int index, Tile &w)
+{
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64) {
+        Sequence s;
+        int tiles = 0;
+        s.rows = 0;
+        if (b0 + lane < p.B)
+            s = sequence(p, b0 + lane);
+        if (s.rows > p.few_rows)
+            tiles = (s.rows + kTileRows - 1) / kTileRows;
+        const int upto = before + scan(tiles);
+        const uint64_t mine = __ballot(index >= upto - tiles && index < upto);
+        if (mine) {
+            const int l = __builtin_ctzll(mine);
+            w.b = b0 + l;
+            w.s.start = lane_int(s.start, l);
+            w.s.m = lane_int(s.m, l);
+            w.s.n = lane_int(s.n, l);
+            w.s.low = 0;
+            w.s.rows = lane_int(s.rows, l);
+            w.first = (lane_int(upto, l) - 1 - index) * kTileRows;
+            return true;
+        }
+        before = lane_int(upto, 63);
+    }
+    return false;
+}
+
+// Places of 16-byte chunks in LDS rows. K: rows of D bf16, read by 32 lanes of
+// consecutive keys at one chunk; V: rows (elements) of 64 fp16 keys, read by 32
+// lanes of consecutive elements at one chunk and written by lanes 8 elements
+// apart. Both spread over all the banks of a read.
+template <int D>
+__device__ __forceinline__ int k_place(int key, int chunk)
+{
+    return key * (2 * D) + 16 * (D == 128 ? chunk ^ (key & 15) : chunk ^ ((key >> 1) & 7));
+}
+
+__device__ __forceinline__ int v_place(int element, int chunk)
+{
+    return element * 128 + 16 * (chunk ^ ((element ^ (element >> 3)) & 7));
+}
+
+// One tile of 128 rows of one key head over its keys, or over one of p.splits shares of them.
+//
+// Bound by the matrix instructions and the exponentials between them. The
+// products are transposed as in the few-rows kernel, on 32x32x16 instructions:
+// a wave holds 32 rows (Q^T and O^T in registers), a lane one row with half of
+// the keys. The codes of 64 keys come in with wide loads one tile ahead, are
+// converted once per workgroup and stored to LDS as bf16 K and fp16 V^T, whose
+// keys are in the order in which the first product leaves them.
+template <int D>
+__global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p)
+{
+    constexpr int KS = D / 16;           // matrix instructions of 32 keys of S^T
+    constexpr int DT = D / 32;           // tiles of O^T
+    constexpr int KL = D / 64;           // 16-byte loads of K in a thread
+    constexpr int VW = D / 64;           // dwords of V in a thread, for one key
+    __shared__ __align__(16) uint8_t klds[kTileKeys * 2 * D];
+    __shared__ __align__(16) uint8_t vlds[D * 2 * kTileKeys];
+    __shared__ uint32_t offsets[2][kTileKeys];
+    __shared__ __align__(16) float kscale[kTileKeys], vscale[kTileKeys], poison[kTileKeys];
+    __shared__ uint64_t present[2];
+    __shared__ int reference;
+
+    const int share = blockIdx.x / p.heads, head = blockIdx.x - share * p.heads;
+    const int index = share / p.splits, split = share - index * p.splits;
+    Tile w;
+    if (!find_tile(p, index, w))
+        return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, hf = lane >> 5;
+    const int last = min(w.first + kTileRows, w.s.rows) - 1;
+    const int base = w.s.n - w.s.m;      // position of the first new token
+    const int pos_first = base + (int)quotient(w.first, p.group), pos_last = base + (int)quotient(last, p.group);
+    const int low = p.window ? max(0, pos_first - p.window + 1) : 0;
+    const int start = low & ~(kTileKeys - 1);
+    const int tiles_in_all = max(0, (pos_last - start + kTileKeys) / kTileKeys);
+    const int tile0 = (int)((int64_t)tiles_in_all * split / p.splits);
+    const int tiles = (int)((int64_t)tiles_in_all * (split + 1) / p.splits) - tile0;
+    const int key0 = start + tile0 * kTileKeys;
+
+    // This lane's row.
+    const int r = w.first + 32 * wave + n;
+    const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+    const bool row_present = r < w.s.rows;
+    const int pos = row_present ? base + token : -1;
+    // The wave's rows: the positions between which a tile is masked for some of them.
+    const int r0 = w.first + 32 * wave, r1 = min(r0 + 31, w.s.rows - 1);
+    const bool wave_present = r0 < w.s.rows;
+    const int wave_first = base + (int)quotient(r0, p.group), wave_last = base + (int)quotient(max(r1, 0), p.group);
+    bf16x8 q[KS];
+    {
+        const uint16_t *row = p.Q + (int64_t)(w.s.start + token) * p.q_t +
+                              (int64_t)(head * (int)p.group.d + h) * p.q_h + 8 * hf;
+#pragma unroll
+        for (int t = 0; t < KS; ++t) {
+            u32x4 v = {0, 0, 0, 0};
+            if (row_present)
+                v = *(const u32x4 *)(row + 16 * t);
+            q[t] = __builtin_bit_cast(bf16x8, v);
+        }
+    }
+
+    const int32_t *table = p.table + w.b * p.table_stride;
+    const uint8_t *kbase = p.k.codes + head * p.k.head, *vbase = p.v.codes + head * p.v.head;
+    // Wave 0 looks after the tile's rows of K, wave 1 after those of V, a key a lane.
+    const Rows &mine = wave == 0 ? p.k : p.v;
+    const float *sbase = mine.scales + head * mine.s_head;
+    const auto load_page = [&](int t) {
+        const int j = key0 + t * kTileKeys + lane;
+        return wave < 2 && t < tiles && j >= low && j <= pos_last ? table[quotient(j, p.page)] : -1;
+    };
+    float scale = 0.0f;
+    // The rows' offsets of tile t, and their scales.
+    const auto place_rows = [&](int t, int page) {
+        if (wave < 2) {
+            const int j = key0 + t * kTileKeys + lane;
+            const bool valid = page >= 0 && page < p.pages;
+            const uint32_t pg = valid ? page : 0, in_page = valid ? j - quotient(j, p.page) * p.page.d : 0;
+            offsets[wave][lane] = pg * mine.page16 + in_page * mine.token16;
+            scale = sbase[pg * mine.s_page + in_page * mine.s_token];
+            scale = valid ? scale : 0.0f;
+            const uint64_t all = __ballot(valid);
+            if (wave == 0 && lane == 0)
+                present[t & 1] = all;
+        }
+    };
+    u32x4 kraw[KL];
+    uint32_t vraw[4][VW];
+    constexpr int KC = D / 16;           // threads of a row of K
+    const int krow = threadIdx.x / KC, kcol = threadIdx.x % KC, vgroup = threadIdx.x >> 4, vcol = threadIdx.x & 15;
+    const auto load_rows = [&]() {
+#pragma unroll
+        for (int l = 0; l < KL; ++l)
+            kraw[l] = *(const u32x4 *)(kbase + 16 * (int64_t)offsets[0][krow + l * (kThreads / KC)] + 16 * kcol);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint8_t *at = vbase + 16 * (int64_t)offsets[1][4 * vgroup + i] + (D / 16) * vcol;
+            if (VW == 2) {
+                const u32x2 v = *(const u32x2 *)at;
+                vraw[i][0] = v[0];
+                vraw[i][VW - 1] = v[1];
+            } else {
+                vraw[i][0] = *(const uint32_t *)at;
+            }
+        }
+    };
+    int exponent = kNoScale;             // of V's reference: wave 1's, and as this wave's sums have it
+    int reference_now = kNoScale;
+    const auto store_rows = [&](int t) {
+        const int first = key0 + t * kTileKeys;
+        const uint64_t there = present[t & 1];
+        if (wave == 0)
+            kscale[lane] = scale * p.scale_log2;
+        if (wave == 1) {
+            const float size = fabsf(scale);
+            const bool counts = size < __builtin_inff();
+            if (__ballot(counts && size > power_of_2(reference_now))) {
+                float most = counts ? size : 0.0f;
+#pragma unroll
+                for (int d = 1; d < 64; d *= 2)
+                    most = fmaxf(most, __shfl_xor(most, d, 64));
+                reference_now = max(exponent_above(most), reference_now);
+            }
+            vscale[lane] = scale * power_of_2(7 - reference_now);
+            if (lane == 0)
+                reference = reference_now;
+        }
+#pragma unroll
+        for (int l = 0; l < KL; ++l) {
+            const int key = krow + l * (kThreads / KC);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const u32x4 v = {codes_to_bf16<false>(kraw[l][2 * i]), codes_to_bf16<true>(kraw[l][2 * i]),
+                                 codes_to_bf16<false>(kraw[l][2 * i + 1]), codes_to_bf16<true>(kraw[l][2 * i + 1])};
+                *(u32x4 *)(klds + k_place<D>(key, 2 * kcol + i)) = v;
+            }
+        }
+        if (there != ~(uint64_t)0 || first + kTileKeys - 1 > pos_first || (p.window && first <= pos_last - p.window)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool here = there >> (4 * vgroup + i) & 1;
+                bool nan = false;
+#pragma unroll
+                for (int l = 0; l < VW; ++l) {
+                    nan |= has_nan_code(vraw[i][l]);
+                    vraw[i][l] = here ? without_nan_codes(vraw[i][l]) : 0;
+                }
+                const bool any = (__ballot(nan) >> (lane & 48) & 0xffff) != 0;
+                if (vcol == 0)
+                    poison[4 * vgroup + i] = any ? __builtin_nanf("") : 0.0f;
+            }
+        }
+        // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers.
+        const int chunk = 2 * (vgroup >> 2) + (vgroup & 1), half = vgroup >> 1 & 1;
+#pragma unroll
+        for (int l = 0; l < VW; ++l) {
+            uint32_t both[2][2];         // keys 0, 1 and 2, 3; elements 0, 1 and 2, 3
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                both[i][0] = __builtin_amdgcn_perm(vraw[2 * i + 1][l], vraw[2 * i][l], 0x05010400);
+                both[i][1] = __builtin_amdgcn_perm(vraw[2 * i + 1][l], vraw[2 * i][l], 0x07030602);
+            }
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                u32x2 v;
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    v[i] = d % 2 ? codes_to_f16<true>(both[i][d / 2]) : codes_to_f16<false>(both[i][d / 2]);
+                *(u32x2 *)(vlds + v_place((D / 16) * vcol + 4 * l + d, chunk) + 8 * half) = v;
+            }
+        }
+    };
+
+    f32x16 o[DT];
+    float ref = kNoMax, sum = 0.0f;
+#pragma unroll
+    for (int t = 0; t < DT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[t][i] = 0.0f;
+
+    int page = load_page(0);
+    place_rows(0, page);
+    page = load_page(1);
+    __syncthreads();
+    if (tiles > 0)
+        load_rows();
+    for (int t = 0; t < tiles; ++t) {
+        __syncthreads();                 // the last tile's operands and this one's offsets have been read
+        store_rows(t);
+        if (t + 1 < tiles)
+            place_rows(t + 1, page);
+        __syncthreads();
+        if (t + 1 < tiles) {
+            load_rows();
+            page = load_page(t + 2);
+        }
+        const int first = key0 + t * kTileKeys;
+        if (!wave_present || first > wave_last)
+            continue;
+        const uint64_t there = present[t & 1];
+        const bool masked = there != ~(uint64_t)0 || first + kTileKeys - 1 > wave_first ||
+                            (p.window && first <= wave_last - p.window);
+        if (exponent != reference) {
+            const int e = reference;
+            const float shrink = exponent - e < -126 ? 0.0f : power_of_2(exponent - e);
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                o[d] *= shrink;
+            exponent = e;
+        }
+
+        f32x16 s[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[b][i] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const bf16x8 a = *(const bf16x8 *)(klds + k_place<D>(32 * b + n, 2 * k + hf));
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[k], s[b], 0, 0, 0);
+            }
+        }
+        // Register i of s[b] is key 32 b + 8 (i / 4) + 4 hf + i % 4.
+        uint32_t seen = 0xffffffffu;
+        if (masked) {
+            seen = 0;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const int at = 8 * (i / 4) + 4 * hf + i % 4, j = first + at;
+                const bool sees = (there >> at & 1) && j <= pos && (!p.window || j > pos - p.window);
+                seen |= (uint32_t)sees << i;
+            }
+        }
+        float ks[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const f32x4 v = *(const f32x4 *)&kscale[8 * i + 4 * hf];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                ks[4 * i + e] = v[e];
+        }
+        float x[32];
+        const auto shift = [&]() {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                x[i] = __builtin_fmaf(s[i / 16][i % 16], ks[i], -ref);
+                if (masked)
+                    x[i] = seen >> i & 1 ? x[i] : -__builtin_inff();
+            }
+        };
+        shift();
+        float most = x[0];
+#pragma unroll
+        for (int i = 1; i < 32; ++i)
+            most = fmaxf(most, x[i]);
+        if (__ballot(most > kSlack)) {
+            float top = kNoMax;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (seen >> i & 1)
+                    top = fmaxf(top, s[i / 16][i % 16] * ks[i]);
+            top = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)), ref);
+            const float shrink = __builtin_amdgcn_exp2f(ref - top);
+            sum *= shrink;
+#pragma unroll
+            for (int d = 0; d < DT; ++d)
+                o[d] *= shrink;
+            ref = top;
+            shift();
+        }
+        f16x8 weights[4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            float y[8];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int place = 16 * b + 8 * half + 4 * hf;
+                f32x4 v = *(const f32x4 *)&vscale[place];
+                if (masked)
+                    v += *(const f32x4 *)&poison[place];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int i = 8 * b + 4 * half + e;
+                    const float weight = __builtin_amdgcn_exp2f(x[i]);
+                    sum += weight;
+                    y[4 * half + e] = weight * v[e];
+                    if (masked)
+                        y[4 * half + e] = seen >> i & 1 ? y[4 * half + e] : 0.0f;
+                }
+            }
+            const u32x4 packed = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
+            weights[b] = __builtin_bit_cast(f16x8, packed);
+        }
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                const f16x8 a = *(const f16x8 *)(vlds + v_place(32 * d + n, 2 * b + hf));
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, weights[b], o[d], 0, 0, 0);
+            }
+    }
+
+    sum += __shfl_xor(sum, 32, 64);
+    if (!row_present)
+        return;
+    const float factor = power_of_2(exponent - 7);
+    if (p.splits == 1) {
+        uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h + 4 * hf;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[e] = sum == 0.0f ? 0.0f : o[d][4 * i + e] * factor / sum;
+                store_bf16<4>(to + 32 * d + 8 * i, y);
+            }
+    } else {
+        const int64_t at = (int64_t)blockIdx.x * p.part_rows + r - w.first;
+        float *to = p.part_o + at * D + 4 * hf;
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *(f32x4 *)(to + 32 * d + 8 * i) =
+                    f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * factor;
+        if (hf == 0)
+            *(f32x2 *)(p.part_ml + 2 * at) = f32x2{ref, sum};
+    }
+}
+
+// One row of a tile (blockIdx.x: tile and key head, blockIdx.y: row) whose keys were split.
+template <int D>
+__global__ __launch_bounds__(kThreads) void join_many_kernel(AttendParams p)
+{
+    const int index = blockIdx.x / p.heads, head = blockIdx.x - index * p.heads;
+    Tile w;
+    if (!find_tile(p, index, w))
+        return;
+    const int r = w.first + (int)blockIdx.y;
+    if (r >= w.s.rows)
+        return;
+    const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+    join<D>(p, p.splits,
+            [&](int i) { return (int64_t)((index * p.splits + i) * p.heads + head) * p.part_rows + blockIdx.y; },
+            p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h);
+}
+
+}  // namespace dga

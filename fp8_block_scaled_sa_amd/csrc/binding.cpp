@@ -1,6 +1,7 @@
 // binding.cpp -- the host side of the serving step's calls (residual norm to
-// codes, router top-k, expert layer) between torch tensors and the C ABI of
-// include/dg_fp8.h: checks of types and shapes, the outputs, the call.
+// codes, router top-k, expert layer, the paged cache's write, read and
+// attention) between torch tensors and the C ABI of include/dg_fp8.h: checks of
+// types and shapes, the outputs, the call.
 //
 // These calls are made for single tokens too, where a kernel takes 3 to 5 us
 // and the same steps in Python took 6 (router) to 12 us (norm, layer), against
@@ -18,6 +19,7 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <string>
 
 #include "dg_fp8.h"
@@ -360,6 +362,194 @@ PyObject *moe_layer(PyObject *, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// A cache from its codes [pages, page_size, heads, head_dim] and scales [pages, page_size, heads].
+dg_fp8_cache cache_of(const Tensor &codes, const Tensor &scales, const char *name, const char *scales_name)
+{
+    need_codes(codes, name);
+    if (codes.dim() != 4 || (codes.stride(3) != 1 && codes.size(3) > 1))
+        bad_value(std::string(name) + " must be [pages, page_size, heads, head_dim] with a contiguous last dimension");
+    need_scales(scales, scales_name, codes.sizes().slice(0, 3));
+    return dg_fp8_cache{pointer(codes, name), codes.stride(0), codes.stride(1), codes.stride(2),
+                        (float *)pointer(scales, scales_name), scales.stride(0), scales.stride(1), scales.stride(2),
+                        codes.size(0), codes.size(1), codes.size(2), codes.size(3)};
+}
+
+// [T, heads, D] with contiguous heads.
+void need_heads(const Tensor &t, const char *name)
+{
+    if (t.dim() != 3 || (t.stride(2) != 1 && t.size(2) > 1))
+        bad_value(std::string(name) + " must be [T, heads, head_dim] with a contiguous last dimension");
+}
+
+// A contiguous vector of so many elements.
+void need_vector(const Tensor &t, const char *name, ScalarType type, int64_t size)
+{
+    need_type(t, name, type);
+    if (t.dim() != 1 || t.size(0) != size || (t.stride(0) != 1 && size > 1))
+        bad_value(std::string(name) + " must be a contiguous vector of " + std::to_string(size) + " elements");
+}
+
+// rope_cache_write(entry, k, v, k_cache, k_scales, v_cache, v_scales, slots, positions, freqs, q, interleaved, factor,
+//                  q_out, stream) -> q_out
+PyObject *rope_cache_write(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    need_arguments(n, 15);
+    const auto entry = entry_point<decltype(&dg_fp8_rope_cache_write)>(a[0]);
+    const Tensor k = tensor(a[1], "k"), v = tensor(a[2], "v"), kc = tensor(a[3], "k_cache"), ks = tensor(a[4], "k_scales"),
+                 vc = tensor(a[5], "v_cache"), vs = tensor(a[6], "v_scales"), slots = tensor(a[7], "slots"),
+                 positions = optional(a[8], "positions"), freqs = optional(a[9], "freqs"), q = optional(a[10], "q");
+    const bool interleaved = truth(a[11]);
+    const float factor = real(a[12]);
+    Tensor qo = optional(a[13], "q_out");
+    void *stream = address(a[14]);
+
+    const int type = float_type(k, "k");
+    need_heads(k, "k");
+    need_type(v, "v", k.scalar_type());
+    need_heads(v, "v");
+    need_shape(v, "v", k.sizes());
+    const int64_t T = k.size(0), heads = k.size(1), D = k.size(2);
+    const dg_fp8_cache kcache = cache_of(kc, ks, "k_cache", "k_scales"), vcache = cache_of(vc, vs, "v_cache", "v_scales");
+    need_shape(kc, "k_cache", {kc.size(0), kc.size(1), heads, D});
+    need_shape(vc, "v_cache", kc.sizes());
+    need_vector(slots, "slots", ScalarType::Long, T);
+    int64_t rot = 0;
+    if (freqs.defined()) {
+        if (!positions.defined())
+            bad_value("freqs needs positions");
+        need_type(freqs, "freqs", ScalarType::Double);
+        rot = 2 * freqs.numel();
+        need_vector(freqs, "freqs", ScalarType::Double, rot / 2);
+        need_vector(positions, "positions", ScalarType::Int, T);
+    }
+    int64_t q_heads = 0;
+    if (q.defined()) {
+        need_type(q, "q", k.scalar_type());
+        need_heads(q, "q");
+        q_heads = q.size(1);
+        need_shape(q, "q", {T, q_heads, D});
+        if (q_heads == 0)
+            bad_value("q must have heads");
+        if (qo.defined()) {
+            need_type(qo, "q_out", ScalarType::BFloat16);
+            need_heads(qo, "q_out");
+            need_shape(qo, "q_out", q.sizes());
+        }
+    } else if (qo.defined()) {
+        bad_value("q_out needs q");
+    }
+    const void *kp = pointer(k, "k"), *vp = pointer(v, "v"), *qp = q.defined() ? pointer(q, "q") : nullptr;
+    const int64_t *sp = (const int64_t *)pointer(slots, "slots");
+    const int32_t *pp = rot ? (const int32_t *)pointer(positions, "positions") : nullptr;
+    const double *fp = rot ? (const double *)pointer(freqs, "freqs") : nullptr;
+    if (q.defined() && !qo.defined())
+        qo = make(q, {T, q_heads, D}, {q_heads * D, D, 1}, ScalarType::BFloat16);
+    void *qop = q.defined() ? pointer(qo, "q_out") : nullptr;
+    const int64_t q_t = q.defined() ? q.stride(0) : 0, q_h = q.defined() ? q.stride(1) : 0;
+    const int64_t qo_t = q.defined() ? qo.stride(0) : 0, qo_h = q.defined() ? qo.stride(1) : 0;
+    const dg_status st = without_gil([&] {
+        return entry(qp, q_t, q_h, qop, qo_t, qo_h, q_heads, kp, k.stride(0), k.stride(1), vp, v.stride(0), v.stride(1),
+                     type, pp, fp, rot, interleaved, factor, sp, &kcache, &vcache, T, stream);
+    });
+    if (st != DG_OK)
+        return PyLong_FromLong(st);
+    return result(a[13], qo);
+    END_HANDLE_TH_ERRORS
+}
+
+// cache_read(entry, cache, scales, slots, bf16, out, stream) -> out
+PyObject *cache_read(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    need_arguments(n, 7);
+    const auto entry = entry_point<decltype(&dg_fp8_cache_read)>(a[0]);
+    const Tensor codes = tensor(a[1], "cache"), scales = tensor(a[2], "scales"), slots = tensor(a[3], "slots");
+    const bool bf16 = truth(a[4]);
+    Tensor out = optional(a[5], "out");
+    void *stream = address(a[6]);
+
+    const dg_fp8_cache cache = cache_of(codes, scales, "cache", "scales");
+    if (slots.dim() != 1)
+        bad_value("slots must be a vector");
+    const int64_t T = slots.size(0), heads = cache.heads, D = cache.head_dim;
+    need_vector(slots, "slots", ScalarType::Long, T);
+    if (out.defined()) {
+        need_heads(out, "out");
+        need_shape(out, "out", {T, heads, D});
+    }
+    const int64_t *sp = (const int64_t *)pointer(slots, "slots");
+    if (!out.defined())
+        out = make(codes, {T, heads, D}, {heads * D, D, 1}, bf16 ? ScalarType::BFloat16 : ScalarType::Float);
+    const int type = float_type(out, "out");
+    void *op = pointer(out, "out");
+    const dg_status st =
+        without_gil([&] { return entry(&cache, sp, op, type, out.stride(0), out.stride(1), T, stream); });
+    if (st != DG_OK)
+        return PyLong_FromLong(st);
+    return result(a[5], out);
+    END_HANDLE_TH_ERRORS
+}
+
+// paged_attention(entry, q, k_cache, k_scales, v_cache, v_scales, block_table, kv_lens, q_starts, max_q_len, workspace,
+//                 scale, window, out, stream) -> out
+PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    need_arguments(n, 15);
+    const auto entry = entry_point<decltype(&dg_fp8_paged_attention)>(a[0]);
+    const Tensor q = tensor(a[1], "q"), kc = tensor(a[2], "k_cache"), ks = tensor(a[3], "k_scales"),
+                 vc = tensor(a[4], "v_cache"), vs = tensor(a[5], "v_scales"), table = tensor(a[6], "block_table"),
+                 lens = tensor(a[7], "kv_lens"), starts = tensor(a[8], "q_starts");
+    const int64_t max_q_len = integer(a[9]);
+    const Tensor ws = optional(a[10], "workspace");
+    const int64_t window = integer(a[12]);
+    Tensor out = optional(a[13], "out");
+    void *stream = address(a[14]);
+
+    need_type(q, "q", ScalarType::BFloat16);
+    need_heads(q, "q");
+    const int64_t T = q.size(0), q_heads = q.size(1), D = q.size(2);
+    const float scale = a[11] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : real(a[11]);
+    const dg_fp8_cache kcache = cache_of(kc, ks, "k_cache", "k_scales"), vcache = cache_of(vc, vs, "v_cache", "v_scales");
+    need_shape(kc, "k_cache", {kc.size(0), kc.size(1), kc.size(2), D});
+    need_shape(vc, "v_cache", kc.sizes());
+    need_type(table, "block_table", ScalarType::Int);
+    if (table.dim() != 2 || (table.stride(1) != 1 && table.size(1) > 1))
+        bad_value("block_table must be [B, pages of a sequence] with contiguous rows");
+    const int64_t B = table.size(0), width = table.size(1);
+    need_vector(lens, "kv_lens", ScalarType::Int, B);
+    need_vector(starts, "q_starts", ScalarType::Int, B + 1);
+    if (out.defined()) {
+        need_type(out, "out", ScalarType::BFloat16);
+        need_heads(out, "out");
+        need_shape(out, "out", q.sizes());
+    }
+    const void *qp = pointer(q, "q");
+    const int32_t *tp = (const int32_t *)pointer(table, "block_table"), *lp = (const int32_t *)pointer(lens, "kv_lens"),
+                  *stp = (const int32_t *)pointer(starts, "q_starts");
+    void *wsp = nullptr;
+    int64_t ws_bytes = 0;
+    if (ws.defined() && ws.numel() > 0) {
+        if (!ws.is_contiguous())
+            bad_value("workspace must be a contiguous device tensor");
+        wsp = pointer(ws, "workspace");
+        ws_bytes = ws.numel() * ws.element_size();
+    }
+    if (!out.defined())
+        out = make(q, {T, q_heads, D}, {q_heads * D, D, 1}, ScalarType::BFloat16);
+    void *op = pointer(out, "out");
+    const int64_t table_stride = B > 1 ? table.stride(0) : width;
+    const dg_status st = without_gil([&] {
+        return entry(qp, q.stride(0), q.stride(1), q_heads, &kcache, &vcache, tp, table_stride, width, lp, stp, B, T,
+                     max_q_len, scale, window, op, out.stride(0), out.stride(1), wsp, ws_bytes, stream);
+    });
+    if (st != DG_OK)
+        return PyLong_FromLong(st);
+    return result(a[13], out);
+    END_HANDLE_TH_ERRORS
+}
+
 PyObject *any_device(PyObject *, PyObject *on)
 {
     HANDLE_TH_ERRORS
@@ -378,6 +568,9 @@ PyMethodDef methods[] = {
     {"rmsnorm_quantize", fast<rmsnorm_quantize>(), METH_FASTCALL, nullptr},
     {"gate_topk", fast<gate_topk>(), METH_FASTCALL, nullptr},
     {"moe_layer", fast<moe_layer>(), METH_FASTCALL, nullptr},
+    {"rope_cache_write", fast<rope_cache_write>(), METH_FASTCALL, nullptr},
+    {"cache_read", fast<cache_read>(), METH_FASTCALL, nullptr},
+    {"paged_attention", fast<paged_attention>(), METH_FASTCALL, nullptr},
     {"any_device", any_device, METH_O, "Tests only: this thread's calls take host tensors too."},
     {nullptr, nullptr, 0, nullptr}};
 

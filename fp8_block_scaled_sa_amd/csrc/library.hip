@@ -1,5 +1,7 @@
-// library.hip -- the library as one translation unit: both files of entry
-// points, the second with the first one's host checks and error record.
+// library.hip -- the library as one translation unit: the files of entry
+// points, the later ones with the first one's host checks and error record.
 #include "dg_fp8.hip"
 
 #include "moe_step.hip"
+
+#include "attention_step.hip"

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import functools
 import inspect
+import math
 
 import torch
 
@@ -606,4 +607,104 @@ def dg_fp8_moe_layer(x, sx, w13, s13, w2, s2, topk_ids, topk_weights, workspace,
                                workspace, out, _stream_for(stream, x))
     if type(out) is int:
         raise DGError(out, "dg_fp8_moe_layer")
+    return out
+
+
+# The paged cache's calls, through the same compiled binding.
+
+def dg_rope_frequencies(rot, base=10000.0, scaling=None, stretch=1.0, original=4096, fast=32.0, slow=1.0, device="cuda"):
+    """Radians per position of the rot/2 rotating pairs, float64, and the factor
+    on cosine and sine, as dg_fp8_rope_cache_write takes them: base^(-2i/rot),
+    for contexts `stretch` times longer than the `original` one scaled by
+      "linear"  all divided by stretch (positions interpolated)
+      "base"    base multiplied by stretch^(rot/(rot-2)) (the slowest pair is
+                divided by stretch, the fastest left)
+      "parts"   pairs that turn less than `slow` times over the original context
+                divided by stretch, those that turn more than `fast` times left,
+                linear in the turns between; factor 0.1 ln(stretch) + 1.
+    Returns (freqs, factor)."""
+    if rot <= 0 or rot % 2:
+        raise ValueError("rot must be even and positive")
+    if scaling not in (None, "linear", "base", "parts"):
+        raise ValueError("scaling must be None, linear, base or parts")
+    if not stretch >= 1.0:
+        raise ValueError("stretch must be at least 1")
+    if scaling == "base" and rot > 2:
+        base = base * stretch ** (rot / (rot - 2))
+    freqs = base ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    factor = 1.0
+    if scaling == "linear":
+        freqs = freqs / stretch
+    elif scaling == "parts":
+        if not fast > slow:
+            raise ValueError("fast must be above slow")
+        keep = ((original * freqs / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        freqs = freqs * (keep + (1 - keep) / stretch)
+        factor = 0.1 * math.log(stretch) + 1.0
+    return freqs.to(device), factor
+
+
+def dg_fp8_rope_cache_write(k, v, k_cache, k_scales, v_cache, v_scales, slots, positions=None, freqs=None, q=None,
+                            interleaved=False, factor=1.0, q_out=None, stream=None):
+    """Rotary positions of q[T,q_heads,D] (optional) and k[T,heads,D], and k, v
+    (float32 or bfloat16) into slots[T] (int64, outside the cache: not written)
+    of k_cache, v_cache [pages,page_size,heads,D] (e4m3 codes) and k_scales,
+    v_scales [pages,page_size,heads]. Pair i of the first 2 * len(freqs)
+    elements of a head turns by positions[t] * freqs[i] (int32, float64; no
+    freqs: nothing turns); factor multiplies cosine and sine. Returns q_out
+    (bfloat16, new unless given; q itself turns it in place), None without q."""
+    if stream is not None and _on_device(k):
+        return _call_on(stream, dg_fp8_rope_cache_write, k, v, k_cache, k_scales, v_cache, v_scales, slots, positions,
+                        freqs, q, interleaved, factor, q_out)
+    out = _binding().rope_cache_write(_lib.address("dg_fp8_rope_cache_write"), k, v, k_cache, k_scales, v_cache, v_scales,
+                                      slots, positions, freqs, q, interleaved, factor, q_out, _stream_for(stream, k))
+    if type(out) is int:
+        raise DGError(out, "dg_fp8_rope_cache_write")
+    return out
+
+
+def dg_fp8_cache_read(cache, scales, slots, dtype=torch.bfloat16, out=None, stream=None):
+    """Rows of a cache [pages,page_size,heads,D] (codes) with its scales
+    [pages,page_size,heads] read back: out[T,heads,D] (dtype bfloat16 or
+    float32, or out's) = code * scale of slots[T] (int64); slots outside the
+    cache give zeros."""
+    if dtype not in DTYPES:
+        raise TypeError("dtype must be float32 or bfloat16")
+    if stream is not None and _on_device(cache):
+        return _call_on(stream, dg_fp8_cache_read, cache, scales, slots, dtype, out)
+    out = _binding().cache_read(_lib.address("dg_fp8_cache_read"), cache, scales, slots, dtype == torch.bfloat16, out,
+                                _stream_for(stream, cache))
+    if type(out) is int:
+        raise DGError(out, "dg_fp8_cache_read")
+    return out
+
+
+def dg_fp8_paged_attention_workspace_bytes(T: int, B: int, q_heads: int, kv_heads: int, head_dim: int,
+                                           max_q_len: int) -> int:
+    """Workspace bytes of any dg_fp8_paged_attention call with at most these T, B and max_q_len."""
+    return _query(_lib.load().dg_fp8_paged_attention_workspace_bytes(T, B, q_heads, kv_heads, head_dim, max_q_len),
+                  "dg_fp8_paged_attention_workspace_bytes")
+
+
+def dg_fp8_paged_attention(q, k_cache, k_scales, v_cache, v_scales, block_table, kv_lens, q_starts, max_q_len, workspace,
+                           scale=None, window=0, out=None, stream=None):
+    """Causal attention of a batch's new tokens q[T,q_heads,D] (bfloat16) over a
+    paged cache of e4m3 codes [pages,page_size,heads,D] and scales
+    [pages,page_size,heads]: sequence b's new tokens are rows q_starts[b] to
+    q_starts[b+1] of q, the last of its kv_lens[b] tokens; its tokens' pages
+    are block_table[b] (int32 all three, on the device; a page outside the cache
+    holds no keys). max_q_len: at least the most new tokens of a sequence.
+    scale: default 1/sqrt(D); window > 0: a token sees that many last tokens,
+    itself among them. workspace: a device tensor of at least
+    dg_fp8_paged_attention_workspace_bytes(T, B, q_heads, heads, D, max_q_len)
+    bytes. Returns out[T,q_heads,D] (bfloat16); rows of no sequence are not
+    written."""
+    if stream is not None and _on_device(q):
+        return _call_on(stream, dg_fp8_paged_attention, q, k_cache, k_scales, v_cache, v_scales, block_table, kv_lens,
+                        q_starts, max_q_len, workspace, scale, window, out)
+    out = _binding().paged_attention(_lib.address("dg_fp8_paged_attention"), q, k_cache, k_scales, v_cache, v_scales,
+                                     block_table, kv_lens, q_starts, max_q_len, workspace, scale, window, out,
+                                     _stream_for(stream, q))
+    if type(out) is int:
+        raise DGError(out, "dg_fp8_paged_attention")
     return out

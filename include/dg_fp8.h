@@ -593,6 +593,135 @@ dg_status dg_fp8_moe_layer(const void *X, int64_t ldx,
  * device. */
 int64_t dg_fp8_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t H, int64_t I);
 
+/*
+ * A paged cache of e4m3 codes, as the calls below take it: slot s is token
+ * s % page_size of page s / page_size, and holds for each head a row of
+ * head_dim codes and one fp32 scale: x ~ dec(code) * scale, with scale =
+ * amax/448 of the row's values (1 for a row of zeros), the format of
+ * dg_fp8_quantize_1x128 with one block a row.
+ *   codes   logical [pages, page_size, heads, head_dim] at
+ *           codes[page*stride_page + token*stride_token + head*stride_head + d]
+ *   scales  logical [pages, page_size, heads], likewise with the s_strides
+ * The struct is read during the call; the two arrays are device memory.
+ * Constraints: head_dim 64 or 128; page_size at most 2^20; pages * page_size
+ * below 2^31; heads at most 65536 (DG_ERR_UNSUPPORTED otherwise); codes 16-byte
+ * aligned and its strides multiples of 16, scales 4-byte aligned; strides >= 0
+ * and at most 2^40, codes of a head spanning less than 64 GiB
+ * (DG_ERR_UNSUPPORTED above). Any order of the dimensions is fine (heads before
+ * tokens, keys and values as halves of each page). A cache that is written has
+ * rows and scales that lie apart in some nesting of the strides.
+ */
+typedef struct dg_fp8_cache {
+    void *codes;
+    int64_t stride_page, stride_token, stride_head;
+    float *scales;
+    int64_t s_stride_page, s_stride_token, s_stride_head;
+    int64_t pages, page_size, heads, head_dim;
+} dg_fp8_cache;
+
+/*
+ * Rotary positions of a step's queries and keys, and its keys and values into
+ * the cache. For token t with position pos = positions[t], the first rot
+ * elements of each query and key head turn in pairs i < rot/2:
+ *   a = pos * freqs[i]      (x, y) -> factor * (x cos a - y sin a, x sin a + y cos a)
+ * with (x, y) the elements (i, i + rot/2), or (2i, 2i + 1) when interleaved !=
+ * 0. The other elements stay. Then
+ *   Q_out = the queries, rounded to bf16
+ *   slot slots[t] of k_cache, v_cache = codes and scales of the keys and values
+ * The angle is formed in fp64 (its whole turns dropped), the rest in fp32; the
+ * keys are quantised from their fp32 values. freqs is where a long context's
+ * scaling goes: radians per position, factor what it puts on cosine and sine.
+ *   Q [T, q_heads, D] or NULL (then q_heads 0), Q_out bf16 [T, q_heads, D];
+ *   K, V [T, heads, D]; Q, K, V of x_dtype (DG_DTYPE_F32, DG_DTYPE_BF16), with
+ *   strides of tokens and heads, elements of a head contiguous
+ *   positions [T] int32, freqs [rot/2] fp64 (rot = 0: both NULL, nothing turns)
+ *   slots [T] int64: a token whose slot lies outside [0, pages * page_size)
+ *   (-1: padding) writes no key and value, its query is written
+ * Slots that no token names keep what they hold. A slot is named at most once
+ * in a call, else its rows' contents are unspecified. A row that holds an
+ * infinity or NaN gets the scale NaN and finite codes: it reads back as NaN.
+ * Constraints: rot a multiple of 16, at most head_dim (DG_ERR_BAD_SHAPE); both
+ * caches with the same sizes; bases 16-byte aligned, strides of Q, K, V, Q_out
+ * multiples of 16 bytes and at most 2^28 elements; q_heads at most 65536, T
+ * below 2^24 (DG_ERR_UNSUPPORTED). Q_out may be Q itself (bf16, same address
+ * and strides; then K and V may be other columns of the same tensor), and lies
+ * apart from everything else otherwise; the caches lie apart from the inputs.
+ * Deterministic; T = 0 returns DG_OK.
+ */
+dg_status dg_fp8_rope_cache_write(const void *Q, int64_t q_stride_t, int64_t q_stride_h,
+                                  void *Q_out, int64_t qo_stride_t, int64_t qo_stride_h, int64_t q_heads,
+                                  const void *K, int64_t k_stride_t, int64_t k_stride_h,
+                                  const void *V, int64_t v_stride_t, int64_t v_stride_h, int x_dtype,
+                                  const int32_t *positions, const double *freqs, int64_t rot, int interleaved,
+                                  float factor, const int64_t *slots,
+                                  const dg_fp8_cache *k_cache, const dg_fp8_cache *v_cache,
+                                  int64_t T, void *stream);
+
+/*
+ * Rows of a cache read back: out[t, h, :] = dec(code) * scale of slot slots[t]
+ * and head h, the fp32 product rounded to out_dtype (DG_DTYPE_F32 or
+ * DG_DTYPE_BF16); a slot outside [0, pages * page_size) gives zeros. Slots may
+ * repeat.
+ *   slots [T] int64;  out [T, heads, head_dim], strides of tokens and heads
+ * Constraints: out 16-byte aligned, its strides multiples of 16 bytes and at
+ * most 2^28 elements, its rows apart from each other and from the inputs; T *
+ * heads below 2^31 and T * heads * head_dim below 2^36 (DG_ERR_UNSUPPORTED).
+ * Deterministic; T = 0 returns DG_OK.
+ */
+dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
+                            void *out, int out_dtype, int64_t out_stride_t, int64_t out_stride_h,
+                            int64_t T, void *stream);
+
+/*
+ * Attention of a batch's new tokens over the paged cache, causal: sequence b
+ * has m = q_starts[b+1] - q_starts[b] new tokens, rows q_starts[b] .. of Q, the
+ * last of its n = kv_lens[b] tokens, whose keys and values the cache holds
+ * already (dg_fp8_rope_cache_write). Its key j lies in page block_table[b, j /
+ * page_size]. New token i, at position p = n - m + i, with query head h of the
+ * q_heads / heads that share key head h / (q_heads / heads):
+ *   x_j = scale * q . k_j     for the keys j <= p, and j > p - window if window > 0
+ *   out = bf16( sum_j exp(x_j) v_j / sum_j exp(x_j) )
+ * A row that sees no key (p < 0, or no page) is 0. Keys in pages outside [0,
+ * pages), and past the table's width, are not seen: pages that every window has
+ * left may be given back, with -1 in the table. What a row does not see never
+ * counts, whatever the cache holds there; a NaN code in a value that it sees
+ * makes it NaN in that column, or in all of them.
+ *   Q, out  bf16 [T, q_heads, head_dim], strides of tokens and heads
+ *   block_table [B, table_width] int32, row stride table_stride
+ *   kv_lens [B], q_starts [B + 1] int32, ascending (all three device memory: no
+ *   synchronisation, safe to capture, they may change between replays)
+ *   max_q_len: at least every sequence's m; the rows of a sequence with more
+ *   are not written, nor are rows of no sequence
+ *   workspace  of dg_fp8_paged_attention_workspace_bytes bytes or more for
+ *   these sizes or larger ones (DG_ERR_SCRATCH below what the call needs),
+ *   16-byte aligned, contents arbitrary; calls that share one must be ordered
+ * Values out of range in kv_lens and q_starts are clamped to what the table and
+ * Q hold (no fault). The products are exact bf16 products with fp32 sums; the
+ * weights of the second one are rounded to 11 bits; everything else is fp32 up
+ * to the rounding of out. Deterministic: the split of the keys follows from the
+ * lengths, and partial results are added in a fixed order.
+ * Constraints: q_heads % heads == 0, both caches with the same sizes, window >=
+ * 0, scale finite (DG_ERR_BAD_SHAPE); table_width * page_size at most 2^30, T *
+ * q_heads below 2^31, B * heads * (table_width * page_size / 128 + 2) below
+ * 2^31, launches below 2^32 threads (DG_ERR_UNSUPPORTED); Q and out 16-byte
+ * aligned, strides multiples of 8 and at most 2^28; out's rows lie apart from
+ * each other; out and workspace apart from each other and from the inputs.
+ * T = 0 or B = 0 returns DG_OK.
+ */
+dg_status dg_fp8_paged_attention(const void *Q, int64_t q_stride_t, int64_t q_stride_h, int64_t q_heads,
+                                 const dg_fp8_cache *k_cache, const dg_fp8_cache *v_cache,
+                                 const int32_t *block_table, int64_t table_stride, int64_t table_width,
+                                 const int32_t *kv_lens, const int32_t *q_starts,
+                                 int64_t B, int64_t T, int64_t max_q_len, float scale, int64_t window,
+                                 void *out, int64_t out_stride_t, int64_t out_stride_h,
+                                 void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Workspace bytes that every call of dg_fp8_paged_attention with at most these
+ * T, B and max_q_len takes; a negative value is -dg_status (bad or unsupported
+ * sizes). Needs no device. */
+int64_t dg_fp8_paged_attention_workspace_bytes(int64_t T, int64_t B, int64_t q_heads, int64_t kv_heads,
+                                               int64_t head_dim, int64_t max_q_len);
+
 #ifdef __cplusplus
 }
 #endif

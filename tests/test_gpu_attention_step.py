@@ -1,0 +1,404 @@
+"""The operators over a paged cache of e4m3 codes on the GPU against plain 64-bit forms: rotary positions and the
+cache's write, its read, and attention of new tokens.
+
+Tolerances. A value rounded once is off by half a step of its type (torch.finfo(t).eps / 2, relative); before it:
+  write      cosine and sine of an fp32 angle in half turns: the angle's rounding moves them by pi 2^-24, the functions
+             by 2 ulp, their product with factor by half one: together under 2^-21 of the factor; the two products and
+             the sum add 2^-23: an element is within 2^-20 factor (|x| + |y|) of the formula's; scales likewise, and a
+             code stands within half a step of what it should (2^-4 of the value, 2^-10 below the normal codes) plus that;
+  read       the fp32 product's rounding (2^-24) and the type's;
+  attention  x is a sum of D exact products in fp32: off by at most (D + 4) 2^-24 sum_d |q_d k_d| scale =: e. A weight
+             exp(x) is then off by 2 e (relative, e < 1/2) plus 2^-20 of the exponential and the scales, and by the
+             2^-11 of its rounding to fp16; a sum over n keys adds n 2^-24, numerator and denominator each. With A =
+             sum p |v| / sum p an output is within (2^-11 + 4 e + 2^-19 + n 2^-23) A of the formula's before its
+             rounding to bf16. Weights of less than 2^-29 of the largest |scale x code weight| are rounded more
+             coarsely, to 2^-40 of it at worst: n 2^-40 448 max |sV|, far below 2^-11 A in these tests.
+"""
+import math
+
+import pytest
+import torch
+
+from fp8_block_scaled_sa_amd import ops
+from tests.gpu_util import guards_intact, sentinel_bf16
+
+pytestmark = pytest.mark.gpu
+
+F8 = torch.float8_e4m3fn
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+
+
+def normal(shape, seed, outliers=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(shape, generator=g, device="cuda")
+    if outliers:
+        x[torch.rand(shape, generator=g, device="cuda") < 1e-3] *= 20
+    return x
+
+
+def half(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def same(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+# ---------------------------------------------------------------- a cache
+
+def quantized(x):
+    """Codes (uint8) and scales of rows [..., D]. (Divided by a tensor: by a number, torch multiplies with its
+    reciprocal on the device, which is off by an ulp.)"""
+    amax = x.abs().amax(-1)
+    s = torch.where(amax == 0, torch.ones_like(amax), amax / torch.full_like(amax, 448))
+    return (x / s[..., None]).clamp(-448, 448).to(F8).view(torch.uint8), s
+
+
+def make_cache(pages, page, heads, D, seed, layout="tokens"):
+    """Codes [pages, page, heads, D] and scales [pages, page, heads] of normal rows; layout: the order in memory."""
+    codes, s = quantized(normal((pages, page, heads, D), seed))
+    if layout == "heads":               # [pages, heads, page, D]
+        codes = codes.transpose(1, 2).contiguous().transpose(1, 2)
+        s = s.transpose(1, 2).contiguous().transpose(1, 2)
+    elif layout == "padded":
+        buf = torch.full((pages, page + 1, heads, D + 16), 0x7F, dtype=torch.uint8, device="cuda")
+        buf[:, :page, :, :D] = codes
+        codes = buf[:, :page, :, :D]
+        sbuf = torch.full((heads, pages, page + 2), math.nan, device="cuda")
+        sbuf[:, :, :page] = s.permute(2, 0, 1)
+        s = sbuf[:, :, :page].permute(1, 2, 0)
+    return codes, s
+
+
+def values(codes, s):
+    return codes.contiguous().view(F8).double() * s.double()[..., None]
+
+
+# ---------------------------------------------------------------- write
+
+def rotated(x, positions, freqs, factor, interleaved):
+    """The formula in 64 bits, and the sum of magnitudes that the tolerance refers to."""
+    y, size = x.double().clone(), x.double().abs()
+    n = 0 if freqs is None else len(freqs)
+    if n:
+        a = positions.double()[:, None] * freqs
+        co, si = (factor * a.cos())[:, None], (factor * a.sin())[:, None]
+        first = slice(0, 2 * n, 2) if interleaved else slice(0, n)
+        second = slice(1, 2 * n, 2) if interleaved else slice(n, 2 * n)
+        u, v = x.double()[..., first], x.double()[..., second]
+        y[..., first], y[..., second] = u * co - v * si, u * si + v * co
+        size[..., first] = size[..., second] = factor * (u.abs() + v.abs())
+    return y, size
+
+
+def check_codes(codes, s, ref, size):
+    """Codes [T, heads, D] and scales against rows ref, which an fp32 computation has within 2^-20 size."""
+    off = 2.0 ** -20 * size
+    amax = ref.abs().amax(-1)
+    want = torch.where(amax > 0, amax / 448, torch.ones_like(amax))
+    assert bool(((s.double() - want).abs() <= 2.0 ** -23 * want + off.amax(-1) / 448).all())
+    t = ref / s.double()[..., None]
+    got = codes.view(F8).double()
+    slack = off / s.double()[..., None] + 2.0 ** -22 * t.abs()
+    assert bool(((got - t).abs() <= torch.clamp((t.abs() + slack) * half(F8), min=2.0 ** -10) + slack).all())
+    assert bool((got.abs().amax(-1) == torch.where(amax > 0, 448.0, 0.0)).all())
+
+
+WRITES = [  # T, q_heads, heads, D, rot, page, dtype, interleaved
+    (1, 32, 8, 128, 128, 64, BF16, False), (1, 1, 1, 64, 64, 1, BF16, True), (2, 3, 1, 128, 64, 16, F32, False),
+    (61, 24, 4, 64, 32, 16, F32, True), (37, 5, 5, 128, 16, 7, BF16, False), (300, 8, 2, 64, 64, 48, BF16, False),
+    (5, 70, 3, 128, 128, 5, BF16, True), (9, 0, 2, 128, 96, 32, F32, False), (33, 4, 1, 128, 0, 16, BF16, False),
+    (1025, 8, 1, 128, 128, 128, F32, False), (700, 1, 1, 64, 48, 33, BF16, True)]
+
+
+@pytest.mark.parametrize("layout", ["tokens", "heads", "padded"])
+@pytest.mark.parametrize("T,q_heads,heads,D,rot,page,dtype,interleaved", WRITES)
+def test_write(gpu_device, T, q_heads, heads, D, rot, page, dtype, interleaved, layout):
+    pages = T // page + 3
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    slots = torch.randperm(pages * page, generator=g, device="cuda")[:T].contiguous()
+    slots[::5] = -1
+    if T > 3:
+        slots[1], slots[2] = pages * page, -(1 << 40)
+    qkv = normal((T, q_heads + 2 * heads, D), T + 1).to(dtype)
+    q, k, v = qkv.split([q_heads, heads, heads], 1)
+    positions = torch.randint(0, 1 << 20, (T,), generator=g, device="cuda", dtype=torch.int32)
+    freqs, factor = ops.dg_rope_frequencies(rot, scaling="parts", stretch=4.0) if rot else (None, 1.0)
+    kc, ks = make_cache(pages, page, heads, D, 5, layout)
+    vc, vs = make_cache(pages, page, heads, D, 6, layout)
+    before = [t.clone() for t in (kc, ks, vc, vs)]
+    whole = [torch.empty(0, dtype=t.dtype, device="cuda").set_(t.untyped_storage()) for t in (kc, ks, vc, vs)]
+    image = [t.clone() for t in whole]
+    out = ops.dg_fp8_rope_cache_write(k, v, kc, ks, vc, vs, slots, positions=positions if rot else None, freqs=freqs,
+                                      q=q if q_heads else None, interleaved=interleaved, factor=factor)
+    torch.cuda.synchronize()
+    if q_heads:
+        ref, size = rotated(q, positions, freqs, factor, interleaved)
+        assert out.dtype == BF16
+        assert bool(((out.double() - ref).abs() <= half(BF16) * ref.abs() + 2.0 ** -19 * size).all())
+    else:
+        assert out is None
+    kept = (slots >= 0) & (slots < pages * page)
+    at = slots[kept]
+    for codes, s, old, x, turns in ((kc, ks, before[:2], k, freqs), (vc, vs, before[2:], v, None)):
+        ref, size = rotated(x, positions, turns, factor, interleaved)
+        p, t = at // page, at % page
+        check_codes(codes[p, t], s[p, t], ref[kept], size[kept])
+        # the other slots, and what lies between the rows, are as they were
+        codes[p, t], s[p, t] = old[0][p, t], old[1][p, t]
+    assert all(same(a, b) for a, b in zip(whole, image))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_write_without_rotation_is_the_quantizer(gpu_device, dtype):
+    """Rows of 128: the same codes and scales as dg_fp8_quantize_1x128, bit for bit, tiny and zero rows among them."""
+    T, heads = 200, 3
+    x = normal((T, heads, 128), 3)
+    x[5] *= 1e-30
+    x[6] *= 1e-38
+    x[7] = 0
+    x[8] *= 1e30
+    x = x.to(dtype)
+    kc, ks = make_cache(4, 64, heads, 128, 1)
+    vc, vs = make_cache(4, 64, heads, 128, 2)
+    slots = torch.arange(T, device="cuda")
+    ops.dg_fp8_rope_cache_write(x, x.flip(0).contiguous(), kc, ks, vc, vs, slots)
+    q, s = ops.dg_fp8_quantize_1x128(x.reshape(T, heads * 128))
+    assert torch.equal(kc.view(-1, heads * 128)[:T], q) and torch.equal(ks.view(-1, heads)[:T], s)
+    assert torch.equal(vc.view(-1, heads * 128)[:T], q.flip(0)) and torch.equal(vs.view(-1, heads)[:T], s.flip(0))
+
+
+def test_write_far_positions(gpu_device):
+    """Positions up to 2^31 - 1 and negative ones: the angle's whole turns cost nothing."""
+    positions = torch.tensor([0, 1, -1, 2 ** 24 + 1, 2 ** 31 - 1, -2 ** 31, 123456789], dtype=torch.int32, device="cuda")
+    T = len(positions)
+    freqs, _ = ops.dg_rope_frequencies(64)
+    x = normal((T, 1, 64), 9)
+    kc, ks = make_cache(1, 16, 1, 64, 1)
+    vc, vs = make_cache(1, 16, 1, 64, 2)
+    q = ops.dg_fp8_rope_cache_write(x, x, kc, ks, vc, vs, torch.arange(T, device="cuda"), positions, freqs, q=x)
+    ref, size = rotated(x, positions, freqs, 1.0, False)
+    # 2^31 radians in fp64 are off by 2^-22, on either side
+    assert bool(((q.double() - ref).abs() <= half(BF16) * ref.abs() + (2.0 ** -19 + 2.0 ** -20) * size).all())
+
+
+def test_write_in_place(gpu_device):
+    """Queries turned in place in a fused tensor that keys and values are columns of."""
+    T, Hq, H, D = 77, 12, 2, 128
+    qkv = normal((T, Hq + 2 * H, D), 4).to(BF16)
+    freqs, _ = ops.dg_rope_frequencies(D)
+    positions = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda")
+
+    def go(qkv, in_place):
+        q, k, v = qkv.split([Hq, H, H], 1)
+        c = [*make_cache(5, 16, H, D, 1), *make_cache(5, 16, H, D, 2)]
+        out = ops.dg_fp8_rope_cache_write(k, v, *c, slots, positions, freqs, q=q, q_out=q if in_place else None)
+        return [out, *c]
+    want = go(qkv, False)
+    mine = qkv.clone()
+    got = go(mine, True)
+    assert all(same(a, b) for a, b in zip(want, got))
+    assert torch.equal(mine[:, Hq:], qkv[:, Hq:])
+
+
+def test_write_keys_and_values_of_one_tensor(gpu_device):
+    """K and V as halves of each page of one tensor."""
+    T, H, D = 40, 2, 64
+    k, v = normal((T, H, D), 1), normal((T, H, D), 2)
+    both = torch.zeros((4, 2, 16, H, D), dtype=torch.uint8, device="cuda")
+    s = torch.zeros((4, 2, 16, H), device="cuda")
+    slots = torch.randperm(64, device="cuda")[:T]
+    ops.dg_fp8_rope_cache_write(k, v, both[:, 0], s[:, 0], both[:, 1], s[:, 1], slots)
+    for i, x in ((0, k), (1, v)):
+        want = quantized(x.cpu())
+        assert torch.equal(both[:, i].reshape(64, H, D)[slots].cpu(), want[0])
+        assert torch.equal(s[:, i].reshape(64, H)[slots].cpu(), want[1])
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_write_of_what_is_not_finite(gpu_device, bad):
+    """The row reads back as NaN, its codes are finite, its neighbours are untouched."""
+    T, H, D = 9, 2, 128
+    x = normal((T, H, D), 1)
+    y = x.clone()
+    y[4, 1, 77] = bad
+    slots = torch.arange(T, device="cuda")
+    freqs, _ = ops.dg_rope_frequencies(D)
+    positions = slots.int()
+    got = []
+    for z in (x, y):
+        c = [*make_cache(1, 16, H, D, 1), *make_cache(1, 16, H, D, 2)]
+        ops.dg_fp8_rope_cache_write(z, z, *c, slots, positions, freqs)
+        got.append([ops.dg_fp8_cache_read(c[0], c[1], slots, dtype=F32), ops.dg_fp8_cache_read(c[2], c[3], slots, dtype=F32)])
+        assert not bool(((c[0] & 0x7F) == 0x7F).any()) and not bool(((c[2] & 0x7F) == 0x7F).any())
+    for a, b in zip(*got):
+        assert bool(b[4, 1].isnan().all())
+        b[4, 1] = a[4, 1]
+        assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- read
+
+@pytest.mark.parametrize("layout", ["tokens", "heads", "padded"])
+@pytest.mark.parametrize("T,heads,D,page", [(1, 1, 64, 1), (1, 8, 128, 64), (333, 4, 64, 16), (57, 3, 128, 5),
+                                            (2000, 5, 128, 48)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_read(gpu_device, T, heads, D, page, dtype, layout):
+    pages = max(2, T // page // 2)
+    codes, s = make_cache(pages, page, heads, D, T, layout)
+    g = torch.Generator(device="cuda").manual_seed(T)
+    slots = torch.randint(0, pages * page, (T,), generator=g, device="cuda")     # repeats among them
+    slots[::7] = torch.tensor([-1, pages * page, -(1 << 50), 1 << 50], device="cuda").repeat(T)[:len(slots[::7])]
+    out = torch.full((T, heads + 1, D + 16), 7.0, dtype=dtype, device="cuda")
+    got = ops.dg_fp8_cache_read(codes, s, slots, out=out[:, :heads, :D])
+    there = (slots >= 0) & (slots < pages * page)
+    ref = torch.zeros((T, heads, D), dtype=F64, device="cuda")
+    at = slots[there]
+    ref[there] = values(codes[at // page, at % page], s[at // page, at % page])
+    assert bool(((got.double() - ref).abs() <= (half(dtype) + 2.0 ** -24) * ref.abs()).all())
+    out[:, :heads, :D] = 7.0
+    assert bool((out == 7.0).all())
+    new = ops.dg_fp8_cache_read(codes, s, slots, dtype=dtype)
+    assert new.dtype == dtype and tuple(new.shape) == (T, heads, D)
+    assert bool(((new.double() - ref).abs() <= (half(dtype) + 2.0 ** -24) * ref.abs()).all())
+
+
+# ---------------------------------------------------------------- attention
+
+class Batch:
+    """Sequences of (new tokens, tokens) on random pages, with everything that a call takes."""
+
+    def __init__(self, lengths, heads, kv_heads, D, page, seed=0, layout="tokens", gap=0, spare=2, width=None):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lengths, self.page, self.D = lengths, page, D
+        need = [-(-n // page) for _, n in lengths]
+        pages = sum(need) + spare
+        order = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)
+        self.width = max(need + [1]) if width is None else width
+        self.table = torch.full((len(lengths), self.width), -1, dtype=torch.int32, device="cuda")
+        used = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = order[used:used + n]
+            used += n
+        starts = [gap]
+        for m, _ in lengths:
+            starts.append(starts[-1] + m)
+        self.starts = starts
+        T = starts[-1] + gap
+        self.q = 2 * torch.randn((T, heads, D), generator=g, device="cuda")
+        self.q = self.q.to(BF16)
+        self.k = make_cache(pages, page, kv_heads, D, seed + 1, layout)
+        self.v = make_cache(pages, page, kv_heads, D, seed + 2, layout)
+        self.kv_lens = torch.tensor([n for _, n in lengths], dtype=torch.int32, device="cuda")
+        self.q_starts = torch.tensor(starts, dtype=torch.int32, device="cuda")
+        self.longest = max([m for m, _ in lengths] + [1])
+        self.ws = ops.workspace(ops.dg_fp8_paged_attention_workspace_bytes(T, len(lengths), heads, kv_heads, D, self.longest))
+        self.ws.fill_(0xFF)
+
+    def call(self, out=None, **kw):
+        longest = kw.pop("longest", self.longest)
+        ws = kw.pop("ws", self.ws)
+        return ops.dg_fp8_paged_attention(self.q, *self.k, *self.v, self.table, self.kv_lens, self.q_starts, longest, ws,
+                                          out=out, **kw)
+
+    def reference(self, scale=None, window=0):
+        """Outputs in 64 bits and how far they may be off, sequence by sequence: rows of no sequence are NaN."""
+        q, D, page = self.q.double(), self.D, self.page
+        scale = D ** -0.5 if scale is None else scale
+        T, Hq, _ = q.shape
+        H = self.k[0].shape[2]
+        pages = self.k[0].shape[0]
+        out = torch.full(q.shape, math.nan, dtype=F64, device="cuda")
+        tol = torch.zeros_like(out)
+        for b, (m, n) in enumerate(self.lengths):
+            n = min(n, self.width * page)
+            if m == 0:
+                continue
+            j = torch.arange(n, device="cuda")
+            held = self.table[b].long()[j // page]
+            there = (held >= 0) & (held < pages)
+            held = torch.where(there, held, 0)
+            k, v = (values(c[held, j % page], s[held, j % page]) for c, s in (self.k, self.v))   # [n, H, D]
+            pos = torch.arange(n - m, n, device="cuda")[:, None]
+            seen = (j <= pos) & there
+            if window:
+                seen &= j > pos - window
+            for h in range(Hq):
+                kh, vh = k[:, h // (Hq // H)], v[:, h // (Hq // H)]
+                rows = slice(self.starts[b], self.starts[b] + m)
+                # what is not seen holds anything, NaN too
+                used = seen.any(0)[:, None]
+                kh, vh = torch.where(used, kh, 0.0), torch.where(used, vh, 0.0)
+                x = torch.where(seen, scale * (q[rows, h] @ kh.t()), -math.inf)
+                e = (D + 4) * 2.0 ** -24 * abs(scale) * (q[rows, h].abs() @ kh.abs().t())
+                top = torch.where(seen.any(1, keepdim=True), x.amax(1, keepdim=True) if n else x, 0.0)
+                p = torch.exp(x - top)
+                total = p.sum(1, keepdim=True)
+                some = total > 0
+                o = torch.where(some, p @ vh / torch.where(some, total, 1.0), 0.0)
+                a = torch.where(some, p @ vh.abs() / torch.where(some, total, 1.0), 0.0)
+                worst = torch.where(seen, e, 0.0).amax(1, keepdim=True) if n else torch.zeros_like(total)
+                out[rows, h] = o
+                tol[rows, h] = half(BF16) * o.abs() + (2.0 ** -11 + 4 * worst + 2.0 ** -19 + n * 2.0 ** -23) * a
+        return out, tol
+
+    def check(self, got, **kw):
+        ref, tol = self.reference(**kw)
+        rows = slice(self.starts[0], self.starts[-1])
+        off = (got.double() - ref)[rows].abs()
+        worst = (off - tol[rows]).amax() if off.numel() else torch.zeros(())
+        assert bool((off <= tol[rows]).all()), "off by %.3g more than allowed" % float(worst)
+
+
+SINGLES = [  # lengths, heads, kv_heads, D, page
+    ([(1, 1)], 1, 1, 64, 1), ([(1, 1)], 8, 1, 128, 64), ([(1, 31)], 16, 1, 64, 16), ([(1, 32)], 32, 8, 128, 64),
+    ([(1, 33)], 4, 4, 128, 16), ([(1, 127), (1, 128), (1, 129), (1, 255), (1, 5)], 8, 2, 128, 16),
+    ([(1, 4000)], 32, 8, 128, 64), ([(1, 200 + 37 * i) for i in range(70)], 4, 2, 64, 48),
+    ([(1, 1000), (1, 3), (1, 2777)], 28, 4, 128, 7), ([(1, 700), (1, 999)], 40, 1, 128, 32),
+    ([(1, 3000)], 64, 1, 64, 16)]
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", SINGLES)
+@pytest.mark.parametrize("layout", ["tokens", "heads", "padded"])
+def test_attention_of_single_tokens(gpu_device, lengths, heads, kv_heads, D, page, layout):
+    b = Batch(lengths, heads, kv_heads, D, page, 3, layout)
+    b.check(b.call())
+
+
+FEW = [([(2, 2)], 8, 1, 128, 16), ([(4, 100), (4, 4), (4, 257)], 32, 8, 128, 32), ([(5, 1000), (1, 10), (3, 3)], 8, 2, 64, 48),
+       ([(8, 300)], 64, 8, 128, 64), ([(16, 16), (16, 2000)], 4, 1, 128, 16), ([(64, 129), (0, 50), (1, 64)], 1, 1, 64, 16)]
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", FEW)
+def test_attention_of_few_tokens(gpu_device, lengths, heads, kv_heads, D, page):
+    b = Batch(lengths, heads, kv_heads, D, page, 4)
+    b.check(b.call())
+
+
+CHUNKS = [([(65, 65)], 1, 1, 64, 16), ([(128, 128)], 2, 1, 128, 64), ([(129, 1000)], 8, 8, 128, 48),
+          ([(100, 100), (100, 777), (1, 500), (0, 9), (17, 64)], 28, 4, 128, 16), ([(512, 3000)], 8, 2, 128, 64),
+          ([(1000, 1000), (1, 1)], 16, 2, 64, 32), ([(300, 5000)], 4, 1, 128, 7), ([(1, 400)] * 20 + [(200, 900)], 8, 1, 64, 16),
+          ([(40, 90)], 96, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", CHUNKS)
+def test_attention_of_chunks(gpu_device, lengths, heads, kv_heads, D, page):
+    b = Batch(lengths, heads, kv_heads, D, page, 5)
+    b.check(b.call())
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 64, 100, 1000, 5000])
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", [
+    ([(1, 1500), (1, 3), (1, 64)], 8, 2, 128, 16), ([(4, 300), (7, 7)], 8, 2, 64, 48),
+    ([(200, 1500), (1, 77), (150, 150)], 8, 2, 128, 32)])
+def test_attention_window(gpu_device, lengths, heads, kv_heads, D, page, window):
+    """With the pages before every window given back, and NaN where they were."""
+    b = Batch(lengths, heads, kv_heads, D, page, 6)
+    for i, (m, n) in enumerate(lengths):
+        gone = max(0, n - m + 1 - window) // page
+        for c, s in (b.k, b.v):
+            c[b.table[i, :gone].long()] = 0x7F
+            s[b.table[i, :gone].long()] = math.nan
+        b.table[i, :gone] = -1
+    b.check(b.call(window=window), window=window)
