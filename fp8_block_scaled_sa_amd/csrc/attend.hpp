@@ -50,7 +50,7 @@ constexpr int kUnit = 128;               // keys that a workgroup of the few-row
 constexpr int kFewRows = 64;             // most rows (tokens x heads of a group) of its sequences
 constexpr int kTileRows = 128;           // rows of a workgroup of the many-rows kernel
 constexpr int kTileKeys = 64;            // keys that it takes at once
-constexpr float kNoMax = -1e30f;         // below every x that counts; finite, so that differences are
+constexpr float kNoMax = -1e30f;         // reference of a row that has seen nothing; finite, so that differences are
 constexpr float kSlack = 8.0f;           // how far x may pass its reference
 constexpr int kNoScale = -100;           // exponent below which sV's reference does not go
 
@@ -372,12 +372,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
     };
 
     f32x4 o[NT][DT];
-    float ref[NT], sum[NT];
+    float ref[NT], limit[NT], sum[NT];
     int exponent = kNoScale;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        ref[nt] = kNoMax;
-        sum[nt] = 0.0f;
+        ref[nt] = sum[nt] = 0.0f;
+        limit[nt] = -__builtin_inff();
 #pragma unroll
         for (int t = 0; t < DT; ++t)
             o[nt][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -443,18 +443,23 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
         }
         wave_sync();
 
+        // This lane's keys whose values are not finite: codes and scales are replaced by zeros, and a row that sees one
+        // becomes NaN.
+        uint32_t bad = 0;
         if (masked) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool here = there >> (16 * (i / 4) + 4 * g + i % 4) & 1;
+                const bool here = there >> (4 * g) >> (16 * (i / 4) + i % 4) & 1;
                 bool nan = false;
 #pragma unroll
                 for (int l = 0; l < VW; ++l) {
                     nan |= has_nan_code(v[i][l]);
                     v[i][l] = here ? without_nan_codes(v[i][l]) : 0;
                 }
-                if ((__ballot(nan) >> (16 * g) & 0xffff) != 0)
-                    vs[i] = __builtin_nanf("");
+                const bool finite = fabsf(vs[i]) < __builtin_inff();
+                vs[i] = finite ? vs[i] : 0.0f;
+                if (!finite || (__ballot(nan) >> (16 * g) & 0xffff) != 0)
+                    bad |= 1u << i;
             }
         }
 
@@ -497,44 +502,40 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
         f16x8 weights[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            uint32_t seen = 0xff;
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x[i] = __builtin_fmaf(s[nt][i / 4][i % 4], ks[i], -ref[nt]);
             if (masked) {
-                seen = 0;
+                // From this lane's first key on: keys [from, to] are seen, where they are there.
+                const int to = pos[nt] - first - 4 * g, from = p.window ? to - p.window + 1 : -kUnit;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int at = 16 * (i / 4) + 4 * g + i % 4, j = first + at;
-                    const bool sees = (there >> at & 1) && j <= pos[nt] && (!p.window || j > pos[nt] - p.window);
-                    seen |= (uint32_t)sees << i;
+                    const int at = 16 * (i / 4) + i % 4;
+                    const bool sees = (there >> (4 * g) >> at & 1) && at <= to && at >= from;
+                    x[i] = sees ? x[i] : -__builtin_inff();
+                    if (sees && (bad >> i & 1))
+                        sum[nt] = __builtin_nanf("");
                 }
             }
-            const auto shift = [&](float *x) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = __builtin_fmaf(s[nt][i / 4][i % 4], ks[i], -ref[nt]);
-                    if (masked)
-                        x[i] = seen >> i & 1 ? x[i] : -__builtin_inff();
-                }
-            };
-            float x[8];
-            shift(x);
             float most = x[0];
 #pragma unroll
             for (int i = 1; i < 8; ++i)
                 most = fmaxf(most, x[i]);
-            if (__ballot(most > kSlack)) {
-                float top = kNoMax;
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (seen >> i & 1)
-                        top = fmaxf(top, s[nt][i / 4][i % 4] * ks[i]);
-                top = fmaxf(max_across(top), ref[nt]);
-                const float shrink = __builtin_amdgcn_exp2f(ref[nt] - top);
+            if (__ballot(most > limit[nt])) {
+                const float top = max_across(most);
+                const bool moves = top > limit[nt];
+                const float by = moves ? top : 0.0f;
+                const float shrink = limit[nt] == kSlack ? __builtin_amdgcn_exp2f(-by) : 1.0f;
                 sum[nt] *= shrink;
 #pragma unroll
                 for (int t = 0; t < DT; ++t)
                     o[nt][t] *= shrink;
-                ref[nt] = top;
-                shift(x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] -= by;
+                ref[nt] += by;
+                limit[nt] = moves ? kSlack : limit[nt];
             }
             float y[8];
 #pragma unroll
@@ -542,8 +543,6 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 const float e = __builtin_amdgcn_exp2f(x[i]);
                 sum[nt] += e;
                 y[i] = e * vs[i];
-                if (masked)
-                    y[i] = seen >> i & 1 ? y[i] : 0.0f;
             }
             const u32x4 packed = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
             weights[nt] = __builtin_bit_cast(f16x8, packed);
@@ -578,6 +577,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const float all = sum_across(sum[nt]);
+        ref[nt] = limit[nt] == kSlack ? ref[nt] : kNoMax;
         if (g == 0) {
             refs[wave][0][16 * nt + c] = ref[nt];
             refs[wave][1][16 * nt + c] = all;
@@ -772,8 +772,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
     __shared__ __align__(16) uint8_t klds[kTileKeys * 2 * D];
     __shared__ __align__(16) uint8_t vlds[D * 2 * kTileKeys];
     __shared__ uint32_t offsets[2][kTileKeys];
-    __shared__ __align__(16) float kscale[kTileKeys], vscale[kTileKeys], poison[kTileKeys];
+    __shared__ __align__(16) float kscale[kTileKeys], vscale[kTileKeys];
     __shared__ uint64_t present[2];
+    __shared__ uint8_t poison[kTileKeys], nan_codes[kThreads];
     __shared__ int reference;
 
     const int share = blockIdx.x / p.heads, head = blockIdx.x - share * p.heads;
@@ -864,6 +865,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
     const auto store_rows = [&](int t) {
         const int first = key0 + t * kTileKeys;
         const uint64_t there = present[t & 1];
+        const bool masked = there != ~(uint64_t)0 || first + kTileKeys - 1 > pos_first ||
+                            (p.window && first <= pos_last - p.window);
         if (wave == 0)
             kscale[lane] = scale * p.scale_log2;
         if (wave == 1) {
@@ -876,7 +879,9 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
                     most = fmaxf(most, __shfl_xor(most, d, 64));
                 reference_now = max(exponent_above(most), reference_now);
             }
-            vscale[lane] = scale * power_of_2(7 - reference_now);
+            vscale[lane] = masked && !counts ? 0.0f : scale * power_of_2(7 - reference_now);
+            if (masked)
+                poison[lane] = !counts;
             if (lane == 0)
                 reference = reference_now;
         }
@@ -890,20 +895,18 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
                 *(u32x4 *)(klds + k_place<D>(key, 2 * kcol + i)) = v;
             }
         }
-        if (there != ~(uint64_t)0 || first + kTileKeys - 1 > pos_first || (p.window && first <= pos_last - p.window)) {
+        if (masked) {
+            uint32_t nans = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const bool here = there >> (4 * vgroup + i) & 1;
-                bool nan = false;
 #pragma unroll
                 for (int l = 0; l < VW; ++l) {
-                    nan |= has_nan_code(vraw[i][l]);
+                    nans |= (uint32_t)has_nan_code(vraw[i][l]) << i;
                     vraw[i][l] = here ? without_nan_codes(vraw[i][l]) : 0;
                 }
-                const bool any = (__ballot(nan) >> (lane & 48) & 0xffff) != 0;
-                if (vcol == 0)
-                    poison[4 * vgroup + i] = any ? __builtin_nanf("") : 0.0f;
             }
+            nan_codes[threadIdx.x] = nans;
         }
         // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers.
         const int chunk = 2 * (vgroup >> 2) + (vgroup & 1), half = vgroup >> 1 & 1;
@@ -927,7 +930,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
     };
 
     f32x16 o[DT];
-    float ref = kNoMax, sum = 0.0f;
+    float ref = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
 #pragma unroll
     for (int t = 0; t < DT; ++t)
 #pragma unroll
@@ -965,96 +968,90 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
             exponent = e;
         }
 
-        f32x16 s[2];
+        f32x16 x[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                s[b][i] = 0.0f;
+                x[b][i] = 0.0f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
                 const bf16x8 a = *(const bf16x8 *)(klds + k_place<D>(32 * b + n, 2 * k + hf));
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[k], s[b], 0, 0, 0);
+                x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[k], x[b], 0, 0, 0);
             }
         }
-        // Register i of s[b] is key 32 b + 8 (i / 4) + 4 hf + i % 4.
-        uint32_t seen = 0xffffffffu;
-        if (masked) {
-            seen = 0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int at = 8 * (i / 4) + 4 * hf + i % 4, j = first + at;
-                const bool sees = (there >> at & 1) && j <= pos && (!p.window || j > pos - p.window);
-                seen |= (uint32_t)sees << i;
-            }
-        }
-        float ks[32];
+        // Register i of x[b] is key 32 b + 8 (i / 4) + 4 hf + i % 4.
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const f32x4 v = *(const f32x4 *)&kscale[8 * i + 4 * hf];
+            const f32x4 ks = *(const f32x4 *)&kscale[8 * i + 4 * hf];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                ks[4 * i + e] = v[e];
+                x[i / 4][4 * (i % 4) + e] = __builtin_fmaf(x[i / 4][4 * (i % 4) + e], ks[e], -ref);
         }
-        float x[32];
-        const auto shift = [&]() {
+        if (masked) {
+            // This lane's keys whose values are not finite (their codes or scales were replaced by zeros): a row that
+            // sees one becomes NaN.
+            uint64_t bad = 0;
+            {
+                uint32_t nans = 0;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    nans |= nan_codes[16 * (lane >> 2) + c];
+                bad = __ballot(poison[lane] || (nans >> (lane & 3) & 1));
+            }
+            // From this lane's first key on: keys [from, to] are seen, where they are there.
+            const uint64_t mine = there >> (4 * hf), bads = bad >> (4 * hf);
+            const int to = pos - first - 4 * hf, from = p.window ? to - p.window + 1 : -kTileKeys;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-                x[i] = __builtin_fmaf(s[i / 16][i % 16], ks[i], -ref);
-                if (masked)
-                    x[i] = seen >> i & 1 ? x[i] : -__builtin_inff();
+                const int at = 8 * (i / 4) + i % 4;
+                const bool sees = (mine >> at & 1) && at <= to && at >= from;
+                x[i / 16][i % 16] = sees ? x[i / 16][i % 16] : -__builtin_inff();
+                if (sees && (bads >> at & 1))
+                    sum = __builtin_nanf("");
             }
-        };
-        shift();
-        float most = x[0];
+        }
+        float most = x[0][0];
 #pragma unroll
         for (int i = 1; i < 32; ++i)
-            most = fmaxf(most, x[i]);
-        if (__ballot(most > kSlack)) {
-            float top = kNoMax;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (seen >> i & 1)
-                    top = fmaxf(top, s[i / 16][i % 16] * ks[i]);
-            top = fmaxf(fmaxf(top, __shfl_xor(top, 32, 64)), ref);
-            const float shrink = __builtin_amdgcn_exp2f(ref - top);
+            most = fmaxf(most, x[i / 16][i % 16]);
+        if (__ballot(most > limit)) {
+            const float top = fmaxf(most, __shfl_xor(most, 32, 64));
+            const bool moves = top > limit;
+            const float by = moves ? top : 0.0f;
+            const float shrink = limit == kSlack ? __builtin_amdgcn_exp2f(-by) : 1.0f;
             sum *= shrink;
 #pragma unroll
             for (int d = 0; d < DT; ++d)
                 o[d] *= shrink;
-            ref = top;
-            shift();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                x[i / 16][i % 16] -= by;
+            ref += by;
+            limit = moves ? kSlack : limit;
         }
-        f16x8 weights[4];
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             float y[8];
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
                 const int place = 16 * b + 8 * half + 4 * hf;
-                f32x4 v = *(const f32x4 *)&vscale[place];
-                if (masked)
-                    v += *(const f32x4 *)&poison[place];
+                const f32x4 v = *(const f32x4 *)&vscale[place];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int i = 8 * b + 4 * half + e;
-                    const float weight = __builtin_amdgcn_exp2f(x[i]);
+                    const float weight = __builtin_amdgcn_exp2f(x[i / 16][i % 16]);
                     sum += weight;
                     y[4 * half + e] = weight * v[e];
-                    if (masked)
-                        y[4 * half + e] = seen >> i & 1 ? y[4 * half + e] : 0.0f;
                 }
             }
-            const u32x4 packed = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
-            weights[b] = __builtin_bit_cast(f16x8, packed);
-        }
+            const u32x4 weights = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            for (int d = 0; d < DT; ++d) {
                 const f16x8 a = *(const f16x8 *)(vlds + v_place(32 * d + n, 2 * b + hf));
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, weights[b], o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(f16x8, weights), o[d], 0, 0, 0);
             }
+        }
     }
 
     sum += __shfl_xor(sum, 32, 64);
@@ -1083,7 +1080,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
                 *(f32x4 *)(to + 32 * d + 8 * i) =
                     f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * factor;
         if (hf == 0)
-            *(f32x2 *)(p.part_ml + 2 * at) = f32x2{ref, sum};
+            *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kSlack ? ref : kNoMax, sum};
     }
 }
 
