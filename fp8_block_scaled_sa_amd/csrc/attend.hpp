@@ -739,20 +739,12 @@ __device__ __forceinline__ bool find_tile(const AttendParams &p, int index, Tile
     return false;
 }
 
-// Places of 16-byte chunks in LDS rows. K: rows of D bf16, read by 32 lanes of
-// consecutive keys at one chunk; V: rows (elements) of 64 fp16 keys, read by 32
-// lanes of consecutive elements at one chunk and written by lanes 8 elements
-// apart. Both spread over all the banks of a read.
+// LDS rows: K by key, D bf16; V^T by element, 64 fp16 keys. The padding spreads the lanes of a read (consecutive rows,
+// one 16-byte chunk) over all banks, and lets every place be one address and a constant. Element (D / 16) c + i of V
+// has row 16 i + c, so that the lanes that write one i write consecutive rows.
 template <int D>
-__device__ __forceinline__ int k_place(int key, int chunk)
-{
-    return key * (2 * D) + 16 * (D == 128 ? chunk ^ (key & 15) : chunk ^ ((key >> 1) & 7));
-}
-
-__device__ __forceinline__ int v_place(int element, int chunk)
-{
-    return element * 128 + 16 * (chunk ^ ((element ^ (element >> 3)) & 7));
-}
+constexpr int kRowBytes = 2 * D + 16;
+constexpr int kColumnBytes = 2 * kTileKeys + 16;
 
 // One tile of 128 rows of one key head over its keys, or over one of p.splits shares of them.
 //
@@ -769,8 +761,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
     constexpr int DT = D / 32;           // tiles of O^T
     constexpr int KL = D / 64;           // 16-byte loads of K in a thread
     constexpr int VW = D / 64;           // dwords of V in a thread, for one key
-    __shared__ __align__(16) uint8_t klds[kTileKeys * 2 * D];
-    __shared__ __align__(16) uint8_t vlds[D * 2 * kTileKeys];
+    __shared__ __align__(16) uint8_t klds[kTileKeys * kRowBytes<D>];
+    __shared__ __align__(16) uint8_t vlds[D * kColumnBytes];
     __shared__ uint32_t offsets[2][kTileKeys];
     __shared__ __align__(16) float kscale[kTileKeys], vscale[kTileKeys];
     __shared__ uint64_t present[2];
@@ -834,7 +826,6 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
             const uint32_t pg = valid ? page : 0, in_page = valid ? j - quotient(j, p.page) * p.page.d : 0;
             offsets[wave][lane] = pg * mine.page16 + in_page * mine.token16;
             scale = sbase[pg * mine.s_page + in_page * mine.s_token];
-            scale = valid ? scale : 0.0f;
             const uint64_t all = __ballot(valid);
             if (wave == 0 && lane == 0)
                 present[t & 1] = all;
@@ -870,6 +861,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
         if (wave == 0)
             kscale[lane] = scale * p.scale_log2;
         if (wave == 1) {
+            scale = there >> lane & 1 ? scale : 0.0f;
             const float size = fabsf(scale);
             const bool counts = size < __builtin_inff();
             if (__ballot(counts && size > power_of_2(reference_now))) {
@@ -892,7 +884,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
             for (int i = 0; i < 2; ++i) {
                 const u32x4 v = {codes_to_bf16<false>(kraw[l][2 * i]), codes_to_bf16<true>(kraw[l][2 * i]),
                                  codes_to_bf16<false>(kraw[l][2 * i + 1]), codes_to_bf16<true>(kraw[l][2 * i + 1])};
-                *(u32x4 *)(klds + k_place<D>(key, 2 * kcol + i)) = v;
+                *(u32x4 *)(klds + key * kRowBytes<D> + 32 * kcol + 16 * i) = v;
             }
         }
         if (masked) {
@@ -924,7 +916,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     v[i] = d % 2 ? codes_to_f16<true>(both[i][d / 2]) : codes_to_f16<false>(both[i][d / 2]);
-                *(u32x2 *)(vlds + v_place((D / 16) * vcol + 4 * l + d, chunk) + 8 * half) = v;
+                *(u32x2 *)(vlds + (16 * (4 * l + d) + vcol) * kColumnBytes + 16 * chunk + 8 * half) = v;
             }
         }
     };
@@ -970,16 +962,17 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
 
         f32x16 x[2];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 x[b][i] = 0.0f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const bf16x8 a = *(const bf16x8 *)(klds + k_place<D>(32 * b + n, 2 * k + hf));
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const bf16x8 a = *(const bf16x8 *)(klds + (32 * b + n) * kRowBytes<D> + 16 * hf + 32 * k);
                 x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[k], x[b], 0, 0, 0);
             }
-        }
         // Register i of x[b] is key 32 b + 8 (i / 4) + 4 hf + i % 4.
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -1048,7 +1041,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
             const u32x4 weights = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                const f16x8 a = *(const f16x8 *)(vlds + v_place(32 * d + n, 2 * b + hf));
+                const f16x8 a = *(const f16x8 *)(vlds + (32 * d + n) * kColumnBytes + 16 * hf + 32 * b);
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(f16x8, weights), o[d], 0, 0, 0);
             }
         }
@@ -1058,30 +1051,32 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
     if (!row_present)
         return;
     const float factor = power_of_2(exponent - 7);
-    if (p.splits == 1) {
-        uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h + 4 * hf;
+    // Registers i % 8 of all tiles hold consecutive elements.
+    constexpr int E = 2 * DT;
+    uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h;
+    const int64_t at = (int64_t)blockIdx.x * p.part_rows + r - w.first;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int element = E * (8 * (i / 4) + 4 * hf + i % 4);
+        float y[E];
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[4];
+            for (int e = 0; e < 2; ++e)
+                y[2 * d + e] = o[d][i + 8 * e] * factor;
+        if (p.splits == 1) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    y[e] = sum == 0.0f ? 0.0f : o[d][4 * i + e] * factor / sum;
-                store_bf16<4>(to + 32 * d + 8 * i, y);
-            }
-    } else {
-        const int64_t at = (int64_t)blockIdx.x * p.part_rows + r - w.first;
-        float *to = p.part_o + at * D + 4 * hf;
+            for (int e = 0; e < E; ++e)
+                y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
+            store_bf16<E>(to + element, y);
+        } else {
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *(f32x4 *)(to + 32 * d + 8 * i) =
-                    f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * factor;
-        if (hf == 0)
-            *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kSlack ? ref : kNoMax, sum};
+            for (int e = 0; e < E; e += 4)
+                *(f32x4 *)(p.part_o + at * D + element + e) = f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
+        }
     }
+    if (p.splits > 1 && hf == 0)
+        *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kSlack ? ref : kNoMax, sum};
 }
 
 // One row of a tile (blockIdx.x: tile and key head, blockIdx.y: row) whose keys were split.
