@@ -43,15 +43,18 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kUnit = 128;               // keys that a workgroup of the few-rows kernel takes at once
 constexpr int kFewRows = 64;             // most rows (tokens x heads of a group) of its sequences
-constexpr int kTileRows = 128;           // rows of a workgroup of the many-rows kernel
-constexpr int kTileKeys = 64;            // keys that it takes at once
+constexpr int kTileRows = 256;           // rows of a workgroup of the many-rows kernel
+constexpr int kTileKeys = 64;            // keys that a workgroup of the many-rows kernel takes at once
 constexpr float kNoMax = -1e30f;         // reference of a row that has seen nothing; finite, so that differences are
 constexpr float kSlack = 8.0f;           // how far x may pass its reference
+constexpr float kMostWeight = 0x1p15f;   // how far the sum of a lane's weights of a tile may go (fp16 ends at 65504)
+constexpr float kUnset = -1.0f;          // limit of a row whose reference has not been set
 constexpr int kNoScale = -100;           // exponent below which sV's reference does not go
 
 // One of the two caches: rows of 16-byte multiples, addressed in units of 16 bytes.
@@ -158,6 +161,11 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
 {
     const f16x2 v = {(_Float16)a, (_Float16)b};
     return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ uint32_t times(uint32_t two, f16x2 by)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, two) * by);
 }
 
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -709,7 +717,7 @@ struct Tile {
 };
 
 // The index-th tile, the last (longest) tiles of a sequence first.
-__device__ __forceinline__ bool find_tile(const AttendParams &p, int index, Tile &w)
+__device__ __forceinline__ bool find_tile(const AttendParams &p, int index, int tile_rows, Tile &w)
 {
     const int lane = threadIdx.x & 63;
     int before = 0;
@@ -720,7 +728,7 @@ __device__ __forceinline__ bool find_tile(const AttendParams &p, int index, Tile
         if (b0 + lane < p.B)
             s = sequence(p, b0 + lane);
         if (s.rows > p.few_rows)
-            tiles = (s.rows + kTileRows - 1) / kTileRows;
+            tiles = (s.rows + tile_rows - 1) / tile_rows;
         const int upto = before + scan(tiles);
         const uint64_t mine = __ballot(index >= upto - tiles && index < upto);
         if (mine) {
@@ -731,7 +739,7 @@ __device__ __forceinline__ bool find_tile(const AttendParams &p, int index, Tile
             w.s.n = lane_int(s.n, l);
             w.s.low = 0;
             w.s.rows = lane_int(s.rows, l);
-            w.first = (lane_int(upto, l) - 1 - index) * kTileRows;
+            w.first = (lane_int(upto, l) - 1 - index) * tile_rows;
             return true;
         }
         before = lane_int(upto, 63);
@@ -746,55 +754,306 @@ template <int D>
 constexpr int kRowBytes = 2 * D + 16;
 constexpr int kColumnBytes = 2 * kTileKeys + 16;
 
-// One tile of 128 rows of one key head over its keys, or over one of p.splits shares of them.
-//
-// Bound by the matrix instructions and the exponentials between them. The
-// products are transposed as in the few-rows kernel, on 32x32x16 instructions:
-// a wave holds 32 rows (Q^T and O^T in registers), a lane one row with half of
-// the keys. The codes of 64 keys come in with wide loads one tile ahead, are
-// converted once per workgroup and stored to LDS as bf16 K and fp16 V^T, whose
-// keys are in the order in which the first product leaves them.
+constexpr int kComputeWaves = kTileRows / 32;
+constexpr int kManyThreads = 64 * (kComputeWaves + 4);  // two waves bring in K, two bring in V
+constexpr int kHalf = kTileKeys / 2;                    // keys of a tile that a wave brings in
+
+// What the many-rows kernel's waves share: two buffers, one computed while the other is filled, with what goes for each
+// half of a tile.
 template <int D>
-__global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p)
+struct ManyLds {
+    __align__(16) uint8_t k[2][kTileKeys * kRowBytes<D>];
+    __align__(16) uint8_t v[2][D * kColumnBytes];
+    __align__(16) float kscales[2][kTileKeys];
+    struct {
+        uint32_t present[2];             // bits of the keys that are there
+        int references[2];               // exponent of V's reference
+        uint32_t bad[2];                 // bits of keys whose values are not finite, where some row does not see every key
+        uint32_t unused[2];
+    } __align__(16) about[2];
+    __align__(16) uint32_t offsets[4][kHalf];            // of the rows that a wave loads next
+    __align__(16) _Float16 vscales[2][kHalf];            // in units of the reference's 2^-6
+};
+
+// The keys of a workgroup.
+struct Keys {
+    int key0, tiles, low, last;          // first key of the first tile, tiles, first and last key that count
+    int pos_first, pos_last;             // positions of the first and the last row
+};
+
+// Whether some row between two positions does not see every one of the kHalf keys from `first` on.
+__device__ __forceinline__ bool masked(int first, uint32_t there, int pos_first, int pos_last, int window)
+{
+    return there != ~0u || first + kHalf - 1 > pos_first || (window && first <= pos_last - window);
+}
+
+// Pages, rows and scales of a half tile of one of the caches, a key a lane (twice).
+struct Rider {
+    const Rows &rows;
+    const int32_t *table;
+    const float *scales;
+    const AttendParams &p;
+    const Keys &k;
+    int part, lane;
+
+    __device__ __forceinline__ int first(int t) const { return k.key0 + t * kTileKeys + kHalf * part; }
+    __device__ __forceinline__ int page(int t) const
+    {
+        return table[quotient(min(first(t) + (lane & 31), k.last), p.page)];
+    }
+    // Offset and scale of this lane's key, and which of the keys are there. What is not there reads slot 0, and is
+    // masked.
+    __device__ __forceinline__ uint32_t place(int t, int page, uint32_t &offset, float &scale) const
+    {
+        const int j = first(t) + (lane & 31);
+        const bool valid = j >= k.low && j <= k.last && page >= 0 && page < p.pages;
+        const uint32_t pg = valid ? page : 0, token = valid ? j - quotient(j, p.page) * p.page.d : 0;
+        offset = pg * rows.page16 + token * rows.token16;
+        scale = scales[pg * rows.s_page + token * rows.s_token];
+        return (uint32_t)__ballot(valid);
+    }
+};
+
+// The loop of a wave that brings in a cache: tile t + 1 is stored while the others compute tile t, and tile t + 3
+// loaded, so that a tile's loads have more than a round to arrive.
+template <typename Load, typename Store, typename Raw>
+__device__ __forceinline__ void bring(int tiles, const Rider &rider, Load load, Store store, Raw &even, Raw &odd)
+{
+    even.page = rider.page(0);
+    odd.page = rider.page(1);
+    load(0, even);
+    load(1, odd);
+    store(0, even);
+    load(2, even);
+    __syncthreads();
+    for (int t = 0;; t += 2) {
+        store(t + 1, odd);
+        load(t + 3, odd);
+        __syncthreads();
+        if (t + 1 >= tiles)
+            break;
+        store(t + 2, even);
+        load(t + 4, even);
+        __syncthreads();
+        if (t + 2 >= tiles)
+            break;
+    }
+}
+
+// K: codes to bf16.
+template <int D>
+__device__ __forceinline__ void bring_k(const AttendParams &p, const Keys &k, const int32_t *table, int head, int part,
+                                        ManyLds<D> &lds)
+{
+    constexpr int L = D / 16;            // lanes of a row
+    constexpr int N = kHalf * L / 64;    // 16-byte loads of a lane
+    const int lane = threadIdx.x & 63, row = lane / L, col = lane % L;
+    const Rider rider = {p.k, table, p.k.scales + head * p.k.s_head, p, k, part, lane};
+    const uint8_t *base = p.k.codes + head * p.k.head + 16 * col;
+    uint32_t *offsets = lds.offsets[part];
+    struct Raw {
+        u32x4 codes[N];
+        float scale;
+        uint32_t there;
+        int page;                        // of the tile after the next
+    } even, odd;
+    const auto load = [&](int t, Raw &raw) {
+        uint32_t offset;
+        raw.there = rider.place(t, raw.page, offset, raw.scale);
+        raw.page = rider.page(t + 2);
+        offsets[lane & 31] = offset;
+        wave_sync();
+#pragma unroll
+        for (int l = 0; l < N; ++l)
+            raw.codes[l] = *(const u32x4 *)(base + 16 * (int64_t)offsets[row + l * (64 / L)]);
+        wave_sync();
+    };
+    const auto store = [&](int t, const Raw &raw) {
+        uint8_t *to = lds.k[t & 1] + (kHalf * part + row) * kRowBytes<D> + 32 * col;
+#pragma unroll
+        for (int l = 0; l < N; ++l)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t low = raw.codes[l][2 * i], high = raw.codes[l][2 * i + 1];
+                *(u32x4 *)(to + l * (64 / L) * kRowBytes<D> + 16 * i) =
+                    u32x4{codes_to_bf16<false>(low), codes_to_bf16<true>(low), codes_to_bf16<false>(high),
+                          codes_to_bf16<true>(high)};
+            }
+        if (lane < kHalf)
+            lds.kscales[t & 1][kHalf * part + lane] = raw.scale * p.scale_log2;
+        if (lane == 0)
+            lds.about[t & 1].present[part] = raw.there;
+    };
+    bring(k.tiles, rider, load, store, even, odd);
+}
+
+// V: codes times their scale to fp16, transposed.
+template <int D>
+__device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, const int32_t *table, int head, int part,
+                                        ManyLds<D> &lds)
+{
+    constexpr int VW = D / 64;           // dwords of a lane, for one key
+    const int lane = threadIdx.x & 63, group = lane >> 4, col = lane & 15;
+    const Rider rider = {p.v, table, p.v.scales + head * p.v.s_head, p, k, part, lane};
+    const uint8_t *base = p.v.codes + head * p.v.head + (D / 16) * col;
+    uint32_t *offsets = lds.offsets[2 + part];
+    struct Raw {
+        uint32_t codes[8][VW];           // keys 16 (i / 4) + 4 group + i % 4
+        float scale;
+        uint32_t there;
+        int page;                        // of the tile after the next
+    } even, odd;
+    int reference = kNoScale;
+    const auto load = [&](int t, Raw &raw) {
+        uint32_t offset;
+        raw.there = rider.place(t, raw.page, offset, raw.scale);
+        raw.page = rider.page(t + 2);
+        offsets[lane & 31] = offset;
+        wave_sync();
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const u32x4 rows = *(const u32x4 *)&offsets[16 * r + 4 * group];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint8_t *at = base + 16 * (int64_t)rows[i];
+                if (VW == 2) {
+                    const u32x2 v = *(const u32x2 *)at;
+                    raw.codes[4 * r + i][0] = v[0];
+                    raw.codes[4 * r + i][VW - 1] = v[1];
+                } else {
+                    raw.codes[4 * r + i][0] = *(const uint32_t *)at;
+                }
+            }
+        }
+        wave_sync();
+    };
+    const auto store = [&](int t, Raw &raw) {
+        const uint32_t there = raw.there;
+        const float found = there >> (lane & 31) & 1 ? raw.scale : 0.0f, size = fabsf(found);
+        const bool finite = size < __builtin_inff();
+        // The other V wave's reference as of the tile before, or the two would differ for good.
+        reference = max(reference, t ? __builtin_amdgcn_readfirstlane(lds.about[(t + 1) & 1].references[1 - part]) : kNoScale);
+        if (__ballot(finite && size > power_of_2(reference))) {
+            float most = finite ? size : 0.0f;
+#pragma unroll
+            for (int d = 1; d < 64; d *= 2)
+                most = fmaxf(most, __shfl_xor(most, d, 64));
+            reference = max(__builtin_amdgcn_readfirstlane(exponent_above(most)), reference);
+        }
+        uint32_t bad = 0;
+        float factor = power_of_2(6 - reference);
+        if (masked(rider.first(t), there, k.pos_first, k.pos_last, p.window)) {
+            // What is not there becomes zeros (0 * NaN would be NaN), and so do NaN codes and scales that are not
+            // finite, whose keys are noted.
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int key = 16 * (i / 4) + i % 4;    // of group 0
+                const bool here = there >> (4 * group) >> key & 1;
+                bool nan = false;
+#pragma unroll
+                for (int l = 0; l < VW; ++l) {
+                    nan |= has_nan_code(raw.codes[i][l]);
+                    raw.codes[i][l] = here ? without_nan_codes(raw.codes[i][l]) : 0;
+                }
+                const uint64_t some = __ballot(nan);
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    bad |= (uint32_t)((some >> (16 * g) & 0xffff) != 0) << (key + 4 * g);
+            }
+            bad |= (uint32_t)__ballot(!finite);
+            factor = finite ? factor : 0.0f;
+        }
+        if (lane < kHalf)
+            lds.vscales[part][lane] = (_Float16)(factor == 0.0f ? 0.0f : found * factor);
+        if (lane == 0) {
+            lds.about[t & 1].bad[part] = bad;
+            lds.about[t & 1].references[part] = reference;
+        }
+        wave_sync();
+        // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers. Element (D / 16) col + i
+        // has row 16 i + col, so that lanes write consecutive rows.
+        uint8_t *to = lds.v[t & 1] + col * kColumnBytes + 2 * kHalf * part + 16 * (group & 1) + 8 * (group >> 1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const f16x4 vs = *(const f16x4 *)&lds.vscales[part][16 * r + 4 * group];
+#pragma unroll
+            for (int l = 0; l < VW; ++l) {
+                uint32_t both[2][2];     // keys 0, 1 and 2, 3; elements 0, 1 and 2, 3
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t one = raw.codes[4 * r + 2 * i][l], two = raw.codes[4 * r + 2 * i + 1][l];
+                    both[i][0] = __builtin_amdgcn_perm(two, one, 0x05010400);
+                    both[i][1] = __builtin_amdgcn_perm(two, one, 0x07030602);
+                }
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    u32x2 v;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        v[i] = times(d % 2 ? codes_to_f16<true>(both[i][d / 2]) : codes_to_f16<false>(both[i][d / 2]),
+                                     f16x2{vs[2 * i], vs[2 * i + 1]});
+                    *(u32x2 *)(to + 16 * (4 * l + d) * kColumnBytes + 32 * r) = v;
+                }
+            }
+        }
+        wave_sync();
+    };
+    bring(k.tiles, rider, load, store, even, odd);
+}
+
+// One tile of 256 rows of one key head over its keys, or over one of p.splits shares of them.
+//
+// The products are transposed as in the few-rows kernel, on 32x32x16
+// instructions: each of eight waves holds 32 rows (Q^T and O^T in registers), a
+// lane a row with half of the keys. Four more waves bring in K and V, 64 keys at
+// a time: they look up the pages, load the codes two tiles ahead, convert them
+// (K to bf16, V times its scale to fp16) and store them to LDS while the other
+// waves compute the tile before; V transposed, its keys in the order in which
+// the first product leaves them. One barrier a tile.
+template <int D>
+__global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendParams p)
 {
     constexpr int KS = D / 16;           // matrix instructions of 32 keys of S^T
     constexpr int DT = D / 32;           // tiles of O^T
-    constexpr int KL = D / 64;           // 16-byte loads of K in a thread
-    constexpr int VW = D / 64;           // dwords of V in a thread, for one key
-    __shared__ __align__(16) uint8_t klds[kTileKeys * kRowBytes<D>];
-    __shared__ __align__(16) uint8_t vlds[D * kColumnBytes];
-    __shared__ uint32_t offsets[2][kTileKeys];
-    __shared__ __align__(16) float kscale[kTileKeys], vscale[kTileKeys];
-    __shared__ uint64_t present[2];
-    __shared__ uint8_t poison[kTileKeys], nan_codes[kThreads];
-    __shared__ int reference;
+    __shared__ ManyLds<D> lds;
 
     const int share = blockIdx.x / p.heads, head = blockIdx.x - share * p.heads;
     const int index = share / p.splits, split = share - index * p.splits;
     Tile w;
-    if (!find_tile(p, index, w))
+    if (!find_tile(p, index, kTileRows, w))
         return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n = lane & 31, hf = lane >> 5;
     const int last = min(w.first + kTileRows, w.s.rows) - 1;
     const int base = w.s.n - w.s.m;      // position of the first new token
-    const int pos_first = base + (int)quotient(w.first, p.group), pos_last = base + (int)quotient(last, p.group);
-    const int low = p.window ? max(0, pos_first - p.window + 1) : 0;
-    const int start = low & ~(kTileKeys - 1);
-    const int tiles_in_all = max(0, (pos_last - start + kTileKeys) / kTileKeys);
+    Keys k;
+    k.pos_first = base + (int)quotient(w.first, p.group);
+    k.pos_last = base + (int)quotient(last, p.group);
+    k.low = p.window ? max(0, k.pos_first - p.window + 1) : 0;
+    const int start = k.low & ~(kTileKeys - 1);
+    const int tiles_in_all = max(0, (k.pos_last - start + kTileKeys) / kTileKeys);
     const int tile0 = (int)((int64_t)tiles_in_all * split / p.splits);
-    const int tiles = (int)((int64_t)tiles_in_all * (split + 1) / p.splits) - tile0;
-    const int key0 = start + tile0 * kTileKeys;
+    k.tiles = (int)((int64_t)tiles_in_all * (split + 1) / p.splits) - tile0;
+    k.key0 = start + tile0 * kTileKeys;
+    k.last = min(k.pos_last, k.key0 + k.tiles * kTileKeys - 1);           // of this share
+
+    if (wave >= kComputeWaves) {
+        if (k.tiles == 0)
+            return;
+        const int32_t *table = p.table + w.b * p.table_stride;
+        const int part = wave & 1;
+        if (wave < kComputeWaves + 2)
+            bring_k<D>(p, k, table, head, part, lds);
+        else
+            bring_v<D>(p, k, table, head, part, lds);
+        return;
+    }
 
     // This lane's row.
+    const int n = lane & 31, hf = lane >> 5;
     const int r = w.first + 32 * wave + n;
     const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
     const bool row_present = r < w.s.rows;
     const int pos = row_present ? base + token : -1;
-    // The wave's rows: the positions between which a tile is masked for some of them.
-    const int r0 = w.first + 32 * wave, r1 = min(r0 + 31, w.s.rows - 1);
-    const bool wave_present = r0 < w.s.rows;
-    const int wave_first = base + (int)quotient(r0, p.group), wave_last = base + (int)quotient(max(r1, 0), p.group);
     bf16x8 q[KS];
     {
         const uint16_t *row = p.Q + (int64_t)(w.s.start + token) * p.q_t +
@@ -807,250 +1066,132 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
             q[t] = __builtin_bit_cast(bf16x8, v);
         }
     }
-
-    const int32_t *table = p.table + w.b * p.table_stride;
-    const uint8_t *kbase = p.k.codes + head * p.k.head, *vbase = p.v.codes + head * p.v.head;
-    // Wave 0 looks after the tile's rows of K, wave 1 after those of V, a key a lane.
-    const Rows &mine = wave == 0 ? p.k : p.v;
-    const float *sbase = mine.scales + head * mine.s_head;
-    const auto load_page = [&](int t) {
-        const int j = key0 + t * kTileKeys + lane;
-        return wave < 2 && t < tiles && j >= low && j <= pos_last ? table[quotient(j, p.page)] : -1;
-    };
-    float scale = 0.0f;
-    // The rows' offsets of tile t, and their scales.
-    const auto place_rows = [&](int t, int page) {
-        if (wave < 2) {
-            const int j = key0 + t * kTileKeys + lane;
-            const bool valid = page >= 0 && page < p.pages;
-            const uint32_t pg = valid ? page : 0, in_page = valid ? j - quotient(j, p.page) * p.page.d : 0;
-            offsets[wave][lane] = pg * mine.page16 + in_page * mine.token16;
-            scale = sbase[pg * mine.s_page + in_page * mine.s_token];
-            const uint64_t all = __ballot(valid);
-            if (wave == 0 && lane == 0)
-                present[t & 1] = all;
-        }
-    };
-    u32x4 kraw[KL];
-    uint32_t vraw[4][VW];
-    constexpr int KC = D / 16;           // threads of a row of K
-    const int krow = threadIdx.x / KC, kcol = threadIdx.x % KC, vgroup = threadIdx.x >> 4, vcol = threadIdx.x & 15;
-    const auto load_rows = [&]() {
-#pragma unroll
-        for (int l = 0; l < KL; ++l)
-            kraw[l] = *(const u32x4 *)(kbase + 16 * (int64_t)offsets[0][krow + l * (kThreads / KC)] + 16 * kcol);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint8_t *at = vbase + 16 * (int64_t)offsets[1][4 * vgroup + i] + (D / 16) * vcol;
-            if (VW == 2) {
-                const u32x2 v = *(const u32x2 *)at;
-                vraw[i][0] = v[0];
-                vraw[i][VW - 1] = v[1];
-            } else {
-                vraw[i][0] = *(const uint32_t *)at;
-            }
-        }
-    };
-    int exponent = kNoScale;             // of V's reference: wave 1's, and as this wave's sums have it
-    int reference_now = kNoScale;
-    const auto store_rows = [&](int t) {
-        const int first = key0 + t * kTileKeys;
-        const uint64_t there = present[t & 1];
-        const bool masked = there != ~(uint64_t)0 || first + kTileKeys - 1 > pos_first ||
-                            (p.window && first <= pos_last - p.window);
-        if (wave == 0)
-            kscale[lane] = scale * p.scale_log2;
-        if (wave == 1) {
-            scale = there >> lane & 1 ? scale : 0.0f;
-            const float size = fabsf(scale);
-            const bool counts = size < __builtin_inff();
-            if (__ballot(counts && size > power_of_2(reference_now))) {
-                float most = counts ? size : 0.0f;
-#pragma unroll
-                for (int d = 1; d < 64; d *= 2)
-                    most = fmaxf(most, __shfl_xor(most, d, 64));
-                reference_now = max(exponent_above(most), reference_now);
-            }
-            vscale[lane] = masked && !counts ? 0.0f : scale * power_of_2(7 - reference_now);
-            if (masked)
-                poison[lane] = !counts;
-            if (lane == 0)
-                reference = reference_now;
-        }
-#pragma unroll
-        for (int l = 0; l < KL; ++l) {
-            const int key = krow + l * (kThreads / KC);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const u32x4 v = {codes_to_bf16<false>(kraw[l][2 * i]), codes_to_bf16<true>(kraw[l][2 * i]),
-                                 codes_to_bf16<false>(kraw[l][2 * i + 1]), codes_to_bf16<true>(kraw[l][2 * i + 1])};
-                *(u32x4 *)(klds + key * kRowBytes<D> + 32 * kcol + 16 * i) = v;
-            }
-        }
-        if (masked) {
-            uint32_t nans = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool here = there >> (4 * vgroup + i) & 1;
-#pragma unroll
-                for (int l = 0; l < VW; ++l) {
-                    nans |= (uint32_t)has_nan_code(vraw[i][l]) << i;
-                    vraw[i][l] = here ? without_nan_codes(vraw[i][l]) : 0;
-                }
-            }
-            nan_codes[threadIdx.x] = nans;
-        }
-        // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers.
-        const int chunk = 2 * (vgroup >> 2) + (vgroup & 1), half = vgroup >> 1 & 1;
-#pragma unroll
-        for (int l = 0; l < VW; ++l) {
-            uint32_t both[2][2];         // keys 0, 1 and 2, 3; elements 0, 1 and 2, 3
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                both[i][0] = __builtin_amdgcn_perm(vraw[2 * i + 1][l], vraw[2 * i][l], 0x05010400);
-                both[i][1] = __builtin_amdgcn_perm(vraw[2 * i + 1][l], vraw[2 * i][l], 0x07030602);
-            }
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                u32x2 v;
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    v[i] = d % 2 ? codes_to_f16<true>(both[i][d / 2]) : codes_to_f16<false>(both[i][d / 2]);
-                *(u32x2 *)(vlds + (16 * (4 * l + d) + vcol) * kColumnBytes + 16 * chunk + 8 * half) = v;
-            }
-        }
-    };
+    // The positions of the wave's rows, between which a tile is masked for some of them (a wave without rows: all are).
+    const int r0 = w.first + 32 * wave;
+    const int wave_first = r0 < w.s.rows ? base + (int)quotient(r0, p.group) : -1;
+    const int wave_last = r0 < w.s.rows ? base + (int)quotient(min(r0 + 32, w.s.rows) - 1, p.group) : -1;
 
     f32x16 o[DT];
-    float ref = 0.0f, limit = -__builtin_inff(), sum = 0.0f;
+    // Weights are exp2(x - ref), 2^7 where ref was set; past `limit` for the sum of a lane's weights of 32 keys it moves.
+    float ref = 0.0f, limit = pos >= 0 ? kUnset : kMostWeight, sum = 0.0f;
+    int exponent = kNoScale;             // of V's reference in o
 #pragma unroll
-    for (int t = 0; t < DT; ++t)
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            o[t][i] = 0.0f;
-
-    int page = load_page(0);
-    place_rows(0, page);
-    page = load_page(1);
-    __syncthreads();
-    if (tiles > 0)
-        load_rows();
-    for (int t = 0; t < tiles; ++t) {
-        __syncthreads();                 // the last tile's operands and this one's offsets have been read
-        store_rows(t);
-        if (t + 1 < tiles)
-            place_rows(t + 1, page);
-        __syncthreads();
-        if (t + 1 < tiles) {
-            load_rows();
-            page = load_page(t + 2);
-        }
-        const int first = key0 + t * kTileKeys;
-        if (!wave_present || first > wave_last)
-            continue;
-        const uint64_t there = present[t & 1];
-        const bool masked = there != ~(uint64_t)0 || first + kTileKeys - 1 > wave_first ||
-                            (p.window && first <= wave_last - p.window);
-        if (exponent != reference) {
-            const int e = reference;
-            const float shrink = exponent - e < -126 ? 0.0f : power_of_2(exponent - e);
+            o[d][i] = 0.0f;
+    // The queries are there before the loop, or its first use of them would wait for every load in each round.
 #pragma unroll
-            for (int d = 0; d < DT; ++d)
-                o[d] *= shrink;
-            exponent = e;
-        }
-
+    for (int i = 0; i < KS; ++i)
+        asm volatile("" : "+v"(q[i]));
+    if (k.tiles > 0)
+        __syncthreads();
+    for (int t = 0; t < k.tiles; ++t) {
+        const int first = k.key0 + t * kTileKeys;
+        const uint8_t *kfrom = lds.k[t & 1] + n * kRowBytes<D> + 16 * hf;
+        const uint8_t *vfrom = lds.v[t & 1] + n * kColumnBytes + 16 * hf;
         f32x16 x[2];
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 x[b][i] = 0.0f;
+        const u32x4 about = *(const u32x4 *)&lds.about[t & 1];
+        const auto multiply_k = [&](int b) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                const bf16x8 a = *(const bf16x8 *)(klds + (32 * b + n) * kRowBytes<D> + 16 * hf + 32 * k);
-                x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[k], x[b], 0, 0, 0);
+            for (int i = 0; i < KS; ++i) {
+                const bf16x8 a = *(const bf16x8 *)(kfrom + 32 * b * kRowBytes<D> + 32 * i);
+                x[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[i], x[b], 0, 0, 0);
             }
-        // Register i of x[b] is key 32 b + 8 (i / 4) + 4 hf + i % 4.
+        };
+        multiply_k(0);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const f32x4 ks = *(const f32x4 *)&kscale[8 * i + 4 * hf];
+        for (int b = 0; b < 2; ++b) {
+            // Register i of x[b] is key 32 b + 8 (i / 4) + 4 hf + i % 4.
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                x[i / 4][4 * (i % 4) + e] = __builtin_fmaf(x[i / 4][4 * (i % 4) + e], ks[e], -ref);
-        }
-        if (masked) {
-            // This lane's keys whose values are not finite (their codes or scales were replaced by zeros): a row that
-            // sees one becomes NaN.
-            uint64_t bad = 0;
-            {
-                uint32_t nans = 0;
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 ks = *(const f32x4 *)&lds.kscales[t & 1][32 * b + 8 * i + 4 * hf];
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    nans |= nan_codes[16 * (lane >> 2) + c];
-                bad = __ballot(poison[lane] || (nans >> (lane & 3) & 1));
+                for (int c = 0; c < 4; ++c)
+                    x[b][4 * i + c] = __builtin_fmaf(x[b][4 * i + c], ks[c], -ref);
             }
-            // From this lane's first key on: keys [from, to] are seen, where they are there.
-            const uint64_t mine = there >> (4 * hf), bads = bad >> (4 * hf);
-            const int to = pos - first - 4 * hf, from = p.window ? to - p.window + 1 : -kTileKeys;
+            const uint32_t there = (uint32_t)__builtin_amdgcn_readfirstlane((int)about[b]);
+            if (masked(first + 32 * b, there, wave_first, wave_last, p.window)) {
+                // A row that sees a key whose values are not finite (they are zeros now) becomes NaN. From this lane's
+                // first key on, keys [from, to] are seen, where they are there.
+                const uint32_t mine = there >> (4 * hf), bad = lds.about[t & 1].bad[b] >> (4 * hf);
+                const int to = pos - (first + 32 * b) - 4 * hf, from = p.window ? to - p.window + 1 : -kTileKeys;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const int at = 8 * (i / 4) + i % 4;
-                const bool sees = (mine >> at & 1) && at <= to && at >= from;
-                x[i / 16][i % 16] = sees ? x[i / 16][i % 16] : -__builtin_inff();
-                if (sees && (bads >> at & 1))
-                    sum = __builtin_nanf("");
-            }
-        }
-        float most = x[0][0];
-#pragma unroll
-        for (int i = 1; i < 32; ++i)
-            most = fmaxf(most, x[i / 16][i % 16]);
-        if (__ballot(most > limit)) {
-            const float top = fmaxf(most, __shfl_xor(most, 32, 64));
-            const bool moves = top > limit;
-            const float by = moves ? top : 0.0f;
-            const float shrink = limit == kSlack ? __builtin_amdgcn_exp2f(-by) : 1.0f;
-            sum *= shrink;
-#pragma unroll
-            for (int d = 0; d < DT; ++d)
-                o[d] *= shrink;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                x[i / 16][i % 16] -= by;
-            ref += by;
-            limit = moves ? kSlack : limit;
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            float y[8];
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int place = 16 * b + 8 * half + 4 * hf;
-                const f32x4 v = *(const f32x4 *)&vscale[place];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 8 * b + 4 * half + e;
-                    const float weight = __builtin_amdgcn_exp2f(x[i / 16][i % 16]);
-                    sum += weight;
-                    y[4 * half + e] = weight * v[e];
+                for (int i = 0; i < 16; ++i) {
+                    const int at = 8 * (i / 4) + i % 4;
+                    const bool sees = (mine >> at & 1) && at <= to && at >= from;
+                    x[b][i] = sees ? x[b][i] : -__builtin_inff();
+                    if (sees && (bad >> at & 1))
+                        sum = __builtin_nanf("");
                 }
             }
-            const u32x4 weights = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
+            // The next half's scores, while this one's weights are formed.
+            if (b == 0)
+                multiply_k(1);
+            // The weights in fp16, as the second product takes them, and their sum.
+            u32x4 weights[2];
+            float part;
+            const auto weigh = [&]() {
+                float parts[2] = {0.0f, 0.0f};
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const f16x8 a = *(const f16x8 *)(vlds + (32 * d + n) * kColumnBytes + 16 * hf + 32 * b);
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(f16x8, weights), o[d], 0, 0, 0);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t two =
+                        pack_f16(__builtin_amdgcn_exp2f(x[b][2 * i]), __builtin_amdgcn_exp2f(x[b][2 * i + 1]));
+                    weights[i / 4][i % 4] = two;
+                    parts[i % 2] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, two),
+                                                          f16x2{(_Float16)1.0f, (_Float16)1.0f}, parts[i % 2], false);
+                }
+                part = parts[0] + parts[1];
+            };
+            weigh();
+            const int e = __builtin_amdgcn_readfirstlane((int)about[2 + b]);
+            if (__ballot(part > limit) || e != exponent) {
+                // A larger reference of V shrinks the sums to it; a smaller one (of the half tiles that two waves bring
+                // in) lets them grow again.
+                const float change = exponent - e < -126 ? 0.0f : power_of_2(min(exponent - e, 127));
+                exponent = e;
+                float top = x[b][0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i)
+                    top = fmaxf(top, x[b][i]);
+                top = fmaxf(top, __shfl_xor(top, 32, 64));
+                const int over = part > limit, other = __shfl_xor(over, 32, 64);    // of the row's other half
+                const bool moves = (over | other) != 0 && top > -__builtin_inff();
+                const float by = moves ? top - 7.0f : 0.0f;
+                float shrink = limit == kUnset ? 1.0f : __builtin_amdgcn_exp2f(-by);
+                sum *= shrink;
+                shrink *= change;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    o[d] *= shrink;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    x[b][i] -= by;
+                ref += by;
+                limit = moves ? kMostWeight : limit;
+                weigh();
             }
+            sum += part;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const f16x8 a = *(const f16x8 *)(vfrom + 32 * d * kColumnBytes + 64 * b + 32 * c);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, __builtin_bit_cast(f16x8, weights[c]), o[d], 0, 0, 0);
+                }
         }
+        __syncthreads();
     }
 
     sum += __shfl_xor(sum, 32, 64);
     if (!row_present)
         return;
-    const float factor = power_of_2(exponent - 7);
+    const float factor = power_of_2(exponent - 6);
     // Registers i % 8 of all tiles hold consecutive elements.
     constexpr int E = 2 * DT;
     uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h;
@@ -1076,7 +1217,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_many_kernel(AttendParams p
         }
     }
     if (p.splits > 1 && hf == 0)
-        *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kSlack ? ref : kNoMax, sum};
+        *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kUnset ? kNoMax : ref, sum};
 }
 
 // One row of a tile (blockIdx.x: tile and key head, blockIdx.y: row) whose keys were split.
@@ -1085,7 +1226,7 @@ __global__ __launch_bounds__(kThreads) void join_many_kernel(AttendParams p)
 {
     const int index = blockIdx.x / p.heads, head = blockIdx.x - index * p.heads;
     Tile w;
-    if (!find_tile(p, index, w))
+    if (!find_tile(p, index, p.part_rows, w))
         return;
     const int r = w.first + (int)blockIdx.y;
     if (r >= w.s.rows)

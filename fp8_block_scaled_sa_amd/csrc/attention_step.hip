@@ -166,7 +166,7 @@ struct AttendPlan {
     int few_rows;          // rows up to which a sequence is its
     int64_t pieces;        // its workgroups at most, which is what its partial results take
     int64_t part_rows;
-    bool many;             // whether there can be sequences of more rows
+    int tile_rows;         // of the many-rows kernel (0: there cannot be sequences of more rows)
     int64_t many_tiles;    // their tiles at most
     int splits;            // workgroups that share a tile's keys
     int64_t many_pieces;
@@ -176,30 +176,31 @@ struct AttendPlan {
 
 constexpr int kFewTarget = 1024;
 constexpr int kFewMinUnits = 1;
-constexpr int kManyTarget = 512;
+constexpr int kManyTarget = 256;
 constexpr int kMaxSplits = 16;
 
 AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64_t D, int64_t max_q_len)
 {
     AttendPlan a = {};
     const int64_t longest = std::min(max_q_len, T), rows = longest * group;
-    a.many = rows > dga::kFewRows;
+    const bool many = rows > dga::kFewRows;
     // Beside chunks, the few-rows kernel is for the sequences with a single token; one sequence alone takes one kernel.
-    const int64_t few = !a.many ? rows : B > 1 && group <= dga::kFewRows ? group : 0;
+    const int64_t few = !many ? rows : B > 1 && group <= dga::kFewRows ? group : 0;
     a.tiles = few == 0 ? 0 : few <= 16 ? 1 : few <= 32 ? 2 : 4;
     a.few_rows = 16 * a.tiles;
     if (a.tiles) {
         a.pieces = kFewTarget + B * heads;
-        a.part_rows = a.many ? a.few_rows : rows;
+        a.part_rows = many ? a.few_rows : rows;
         a.bytes = a.pieces * a.part_rows * (D + 2) * 4;
     }
     a.most_bytes = (kFewTarget + B * heads) * std::min<int64_t>(dga::kFewRows, rows) * (D + 2) * 4;
-    if (a.many) {
-        a.many_tiles = (T * group + std::min(B, T) * (dga::kTileRows - 1)) / dga::kTileRows;
+    if (many) {
+        a.tile_rows = dga::kTileRows;
+        a.many_tiles = (T * group + std::min(B, T) * (a.tile_rows - 1)) / a.tile_rows;
         a.splits = (int)std::min<int64_t>(std::max<int64_t>(kManyTarget / (a.many_tiles * heads), 1), kMaxSplits);
         a.many_pieces = a.many_tiles * heads * a.splits;
         if (a.splits > 1)
-            a.bytes = std::max(a.bytes, a.many_pieces * dga::kTileRows * (D + 2) * 4);
+            a.bytes = std::max(a.bytes, a.many_pieces * a.tile_rows * (D + 2) * 4);
         // With more than one share, a launch has at most kManyTarget workgroups.
         a.most_bytes = std::max<int64_t>(a.most_bytes, (int64_t)kManyTarget * dga::kTileRows * (D + 2) * 4);
     }
@@ -220,7 +221,7 @@ int check_attend_sizes(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int
         return DG_OK;
     const AttendPlan a = plan_attend(T, B, heads, q_heads / heads, D, max_q_len);
     if (a.pieces > kMaxPieces || a.many_pieces > kMaxPieces || B * heads * a.part_rows > kMaxPieces ||
-        (a.splits > 1 && a.many_tiles * heads * dga::kTileRows > kMaxPieces))
+        (a.splits > 1 && a.many_tiles * heads * a.tile_rows > kMaxPieces))
         return DG_ERR_UNSUPPORTED;
     return DG_OK;
 }
@@ -253,16 +254,17 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
                 return st;
         }
     }
-    if (a.many) {
+    if (a.tile_rows) {
         p.splits = a.splits;
-        p.part_rows = dga::kTileRows;
-        p.part_ml = p.part_o + a.many_pieces * dga::kTileRows * D;
-        hipLaunchKernelGGL((dga::attend_many_kernel<D>), dim3((unsigned)a.many_pieces), threads, 0, stream, p);
+        p.part_rows = a.tile_rows;
+        p.part_ml = p.part_o + a.many_pieces * a.tile_rows * D;
+        const dim3 grid((unsigned)a.many_pieces);
+        hipLaunchKernelGGL((dga::attend_many_kernel<D>), grid, dim3(dga::kManyThreads), 0, stream, p);
         int st = launched();
         if (st != DG_OK)
             return st;
         if (a.splits > 1) {
-            hipLaunchKernelGGL((dga::join_many_kernel<D>), dim3((unsigned)(a.many_tiles * p.heads), dga::kTileRows),
+            hipLaunchKernelGGL((dga::join_many_kernel<D>), dim3((unsigned)(a.many_tiles * p.heads), (unsigned)a.tile_rows),
                                threads, 0, stream, p);
             return launched();
         }

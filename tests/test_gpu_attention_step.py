@@ -8,11 +8,13 @@ Tolerances. A value rounded once is off by half a step of its type (torch.finfo(
              code stands within half a step of what it should (2^-4 of the value, 2^-10 below the normal codes) plus that;
   read       the fp32 product's rounding (2^-24) and the type's;
   attention  x is a sum of D exact products in fp32: off by at most (D + 4) 2^-24 sum_d |q_d k_d| scale =: e. A weight
-             exp(x) is then off by 2 e (relative, e < 1/2) plus 2^-20 of the exponential and the scales, and by the
-             2^-11 of its rounding to fp16; a sum over n keys adds n 2^-24, numerator and denominator each. With A =
-             sum p |v| / sum p an output is within (2^-11 + 4 e + 2^-19 + n 2^-23) A of the formula's before its
-             rounding to bf16. Weights of less than 2^-29 of the largest |scale x code weight| are rounded more
-             coarsely, to 2^-40 of it at worst: n 2^-40 448 max |sV|, far below 2^-11 A in these tests.
+             exp(x) is then off by 2 e (relative, e < 1/2) plus 2^-20 of the exponential and the scales; a sum over n
+             keys adds n 2^-24, numerator and denominator each. fp16 takes the weights, by 2^-11 off, in the numerator
+             or (many rows) in both, which counts twice; there it also takes sV and sV V, 2^-11 each: 2^-9 in all. With
+             A = sum p |v| / sum p an output is within (2^-9 + 4 e + 2^-19 + n 2^-23) A of the formula's before its
+             rounding to bf16. What fp16 rounds more coarsely, weights below 2^-21 of a row's largest and values whose
+             scale is below 2^-20 of the largest, is off by 2^-31 and 2^-35 of the largest at worst: n 2^-30 448 max
+             |sV|, far below 2^-9 A in these tests.
 """
 import math
 
@@ -340,7 +342,7 @@ class Batch:
                 a = torch.where(some, p @ vh.abs() / torch.where(some, total, 1.0), 0.0)
                 worst = torch.where(seen, e, 0.0).amax(1, keepdim=True) if n else torch.zeros_like(total)
                 out[rows, h] = o
-                tol[rows, h] = half(BF16) * o.abs() + (2.0 ** -11 + 4 * worst + 2.0 ** -19 + n * 2.0 ** -23) * a
+                tol[rows, h] = half(BF16) * o.abs() + (2.0 ** -9 + 4 * worst + 2.0 ** -19 + n * 2.0 ** -23) * a
         return out, tol
 
     def check(self, got, **kw):
