@@ -191,7 +191,7 @@ __device__ __forceinline__ uint32_t without_nan_codes(uint32_t codes)
 
 // ---------------------------------------------------------------- few rows
 
-// Where a piece of the few-rows kernel lies.
+// Where a piece of the few-rows kernel lies: its units of a sequence's keys, for one head.
 struct Piece {
     Sequence s;
     int b, head, first, units;           // units [first, first + units) of the sequence's
@@ -208,62 +208,83 @@ __device__ __forceinline__ int units_of(const Sequence &s)
 // sequences fill the CUs evenly: `chunk` units a piece, as many as give
 // p.target pieces in all. Each wave finds its piece by itself from the
 // sequences' lengths (64 at a time, a scan over the lanes), without a planning
-// launch and without the host knowing them. visit(b0, pieces, before) is given
-// the sequences 64 at a time, with each lane's pieces (all heads) and those of
-// the lanes before; it returns whether to stop.
-template <typename Visit>
-__device__ __forceinline__ void for_pieces(const AttendParams &p, Visit visit)
+// launch and without the host knowing them.
+struct Cut {
+    Sequence s;                          // of this lane, of 64
+    int units, pieces, before;           // pieces of each of its heads; pieces of the lanes (and sequences) before
+};
+
+__device__ __forceinline__ int lane_units(const AttendParams &p, int b, Sequence &s)
 {
-    const int lane = threadIdx.x & 63;
-    const auto units = [&](int b, Sequence &s) {
-        s.rows = 0;
-        if (b < p.B)
-            s = sequence(p, b);
-        return s.rows > 0 && s.rows <= p.few_rows ? units_of(s) : -1;
-    };
-    Sequence s;
-    int all = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 64)
-        all += max(0, units(b0 + lane, s));
-    all = lane_int(scan(all), 63) * p.heads;
-    const int chunk = max(p.min_units, (all + p.target - 1) / p.target);
-    int before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 64) {
-        const int u = units(b0 + lane, s);
-        const int pieces = u < 0 ? 0 : max(1, (u + chunk - 1) / chunk);
-        const int upto = scan(pieces * p.heads);
-        if (visit(b0, s, u, pieces, before + upto - pieces * p.heads))
-            return;
-        before += lane_int(upto, 63);
-    }
+    s.rows = 0;
+    if (b < p.B)
+        s = sequence(p, b);
+    return s.rows > 0 && s.rows <= p.few_rows ? units_of(s) : -1;
 }
 
-__device__ __forceinline__ bool find_piece(const AttendParams &p, int index, Piece &w)
+// Units of a piece. c: the first 64 sequences' cut is begun.
+__device__ __forceinline__ int chunk_of(const AttendParams &p, Cut &c)
 {
-    bool found = false;
-    for_pieces(p, [&](int b0, const Sequence &s, int u, int pieces, int before) {
-        const uint64_t mine = __ballot(index >= before && index < before + pieces * p.heads);
-        if (!mine)
-            return false;
-        const int lane = __builtin_ctzll(mine);
-        w.b = b0 + lane;
-        w.s.start = lane_int(s.start, lane);
-        w.s.m = lane_int(s.m, lane);
-        w.s.n = lane_int(s.n, lane);
-        w.s.low = lane_int(s.low, lane);
-        w.s.rows = lane_int(s.rows, lane);
-        w.pieces = lane_int(pieces, lane);
-        w.index = index;
-        const int at = index - lane_int(before, lane), all = lane_int(u, lane);
-        // Heads next to each other: they read the same pages.
-        const int i = at / p.heads;
-        w.head = at - i * p.heads;
-        w.first = (int)((int64_t)all * i / w.pieces);
-        w.units = (int)((int64_t)all * (i + 1) / w.pieces) - w.first;
-        found = true;
-        return true;
-    });
-    return found;
+    const int lane = threadIdx.x & 63;
+    c.units = lane_units(p, lane, c.s);
+    int all = max(0, c.units);
+    for (int b0 = 64; b0 < p.B; b0 += 64) {
+        Sequence s;
+        all += max(0, lane_units(p, b0 + lane, s));
+    }
+    all = lane_int(scan(all), 63) * p.heads;
+    return max(p.min_units, (all + p.target - 1) / p.target);
+}
+
+// Cuts the sequences from b0 on; returns the pieces up to and with them.
+__device__ __forceinline__ int cut(const AttendParams &p, int b0, int chunk, int before, Cut &c)
+{
+    if (b0)
+        c.units = lane_units(p, b0 + (threadIdx.x & 63), c.s);
+    c.pieces = c.units < 0 ? 0 : max(1, (c.units + chunk - 1) / chunk);
+    const int upto = scan(c.pieces * p.heads);
+    c.before = before + upto - c.pieces * p.heads;
+    return before + lane_int(upto, 63);
+}
+
+__device__ __forceinline__ bool find_piece(const AttendParams &p, int block, Piece &w)
+{
+    Cut c;
+    const int chunk = chunk_of(p, c);
+    int total = cut(p, 0, chunk, 0, c);
+    for (int b0 = 64; b0 < p.B; b0 += 64)
+        total = cut(p, b0, chunk, total, c);
+    // Workgroups are dealt to the 8 XCDs in turn. Renumbered, each XCD takes a contiguous range of pieces, so that the
+    // heads of a page, whose rows lie side by side, are read by the same one at the same time (64 sequences up to 16384
+    // tokens: 259 -> 232 us).
+    const int xcd = block % 8, per = total / 8, extra = total % 8, turn = block / 8;
+    if (turn >= per + (xcd < extra))
+        return false;
+    const int index = xcd * per + min(xcd, extra) + turn;
+    int b0 = 0;
+    if (p.B > 64) {
+        c.units = lane_units(p, threadIdx.x & 63, c.s);
+        for (int upto = cut(p, 0, chunk, 0, c); upto <= index; ) {
+            b0 += 64;
+            upto = cut(p, b0, chunk, upto, c);
+        }
+    }
+    const int lane = __builtin_ctzll(__ballot(index >= c.before && index < c.before + c.pieces * p.heads));
+    w.b = b0 + lane;
+    w.s.start = lane_int(c.s.start, lane);
+    w.s.m = lane_int(c.s.m, lane);
+    w.s.n = lane_int(c.s.n, lane);
+    w.s.low = lane_int(c.s.low, lane);
+    w.s.rows = lane_int(c.s.rows, lane);
+    w.pieces = lane_int(c.pieces, lane);
+    w.index = index;
+    const int at = index - lane_int(c.before, lane), all = lane_int(c.units, lane);
+    // Heads next to each other: they read the same pages.
+    const int i = at / p.heads;
+    w.head = at - i * p.heads;
+    w.first = (int)((int64_t)all * i / w.pieces);
+    w.units = (int)((int64_t)all * (i + 1) / w.pieces) - w.first;
+    return true;
 }
 
 // Writes D / 16 values of a finished row.
@@ -335,33 +356,39 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
         }
     }
 
-    // Steps of the pipeline, by unit: the pages two units ahead, rows and scales one ahead.
+    // What a unit brings: its codes, the scale of this lane's key, which keys are there, and the page of this lane's key
+    // in the unit after the next.
+    struct Raw {
+        u32x4 k[2][KL];
+        uint32_t v[8][VW];
+        float scale;
+        uint32_t there;
+        int page;
+    } even, odd;
+    // Without a branch around it, so that nothing waits for it before its use; units are at most the sequence's.
     const auto load_page = [&](int u) {
-        const int j = key0 + u * kUnit + (lane & 31);
-        return u < units && j >= w.s.low && j < w.s.n ? table[quotient(j, p.page)] : -1;
+        return table[quotient(min(key0 + u * kUnit + (lane & 31), w.s.n - 1), p.page)];
     };
-    u32x4 kraw[2][KL];
-    uint32_t vraw[8][VW];
-    float scale = 0.0f;
-    bool valid = false;
-    const auto load_rows = [&](int u, int page) {
+    const auto load = [&](int u, Raw &raw) {
         const int j = key0 + u * kUnit + (lane & 31);
-        valid = page >= 0 && page < p.pages;
+        const bool valid = u < units && j >= w.s.low && j < w.s.n && raw.page >= 0 && raw.page < p.pages;
         // A key that is not there reads slot 0, and is masked later.
-        const uint32_t pg = valid ? page : 0, token = valid ? j - quotient(j, p.page) * p.page.d : 0;
+        const uint32_t pg = valid ? raw.page : 0, token = valid ? j - quotient(j, p.page) * p.page.d : 0;
+        raw.there = (uint32_t)__ballot(valid);
+        raw.page = load_page(u + 2);
         offsets[wave][lane] = values ? pg * p.v.page16 + token * p.v.token16 : pg * p.k.page16 + token * p.k.token16;
-        scale = values ? sbase[pg * p.v.s_page + token * p.v.s_token] : sbase[pg * p.k.s_page + token * p.k.s_token];
+        raw.scale = values ? sbase[pg * p.v.s_page + token * p.v.s_token] : sbase[pg * p.k.s_page + token * p.k.s_token];
         wave_sync();
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
             if (D == 128) {
 #pragma unroll
                 for (int l = 0; l < KL; ++l)
-                    kraw[sub][l] = __builtin_nontemporal_load(
+                    raw.k[sub][l] = __builtin_nontemporal_load(
                         (const u32x4 *)(kbase + 16 * (int64_t)offsets[wave][16 * sub + 8 * l + (lane & 7)] + 32 * g +
                                         16 * ((lane >> 3) & 1)));
             } else {
-                kraw[sub][0] = __builtin_nontemporal_load(
+                raw.k[sub][0] = __builtin_nontemporal_load(
                     (const u32x4 *)(kbase + 16 * (int64_t)offsets[wave][16 * sub + c] + 16 * g));
             }
 #pragma unroll
@@ -369,10 +396,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 const uint8_t *at = vbase + 16 * (int64_t)offsets[wave][32 + 16 * sub + 4 * g + i] + DT * c;
                 if (VW == 2) {
                     const u32x2 v = __builtin_nontemporal_load((const u32x2 *)at);
-                    vraw[4 * sub + i][0] = v[0];
-                    vraw[4 * sub + i][VW - 1] = v[1];
+                    raw.v[4 * sub + i][0] = v[0];
+                    raw.v[4 * sub + i][VW - 1] = v[1];
                 } else {
-                    vraw[4 * sub + i][0] = __builtin_nontemporal_load((const uint32_t *)at);
+                    raw.v[4 * sub + i][0] = __builtin_nontemporal_load((const uint32_t *)at);
                 }
             }
         }
@@ -391,33 +418,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
             o[nt][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    int page = load_page(0);
-    if (units > 0)
-        load_rows(0, page);
-    page = load_page(1);
-    for (int u = 0; u < units; ++u) {
-        // This unit's operands leave the load registers, then the next unit's loads start.
-        const uint32_t there = (uint32_t)__ballot(valid);
-        const float found = scale;
+    const auto attend = [&](int u, Raw &raw) {
+        const uint32_t there = raw.there;
+        const float found = raw.scale;
         const int first = key0 + u * kUnit;
         const bool masked = there != 0xffffffffu || first + 31 > w.s.n - w.s.m ||
                             (p.window && first <= w.s.n - 1 - p.window);
-        u32x4 k[2][KL];
-        uint32_t v[8][VW];
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-            for (int l = 0; l < KL; ++l)
-                k[sub][l] = kraw[sub][l];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int l = 0; l < VW; ++l)
-                v[i][l] = vraw[i][l];
-        if (u + 1 < units) {
-            load_rows(u + 1, page);
-            page = load_page(u + 2);
-        }
 
         // V's reference covers the unit's finite scales.
         const float size = fabsf(found);
@@ -461,8 +467,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 bool nan = false;
 #pragma unroll
                 for (int l = 0; l < VW; ++l) {
-                    nan |= has_nan_code(v[i][l]);
-                    v[i][l] = here ? without_nan_codes(v[i][l]) : 0;
+                    nan |= has_nan_code(raw.v[i][l]);
+                    raw.v[i][l] = here ? without_nan_codes(raw.v[i][l]) : 0;
                 }
                 const bool finite = fabsf(vs[i]) < __builtin_inff();
                 vs[i] = finite ? vs[i] : 0.0f;
@@ -481,7 +487,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 const bool upper = lane & 8;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t a = k[sub][0][i], b = k[sub][KL - 1][i];
+                    const uint32_t a = raw.k[sub][0][i], b = raw.k[sub][KL - 1][i];
                     const uint32_t give = upper ? a : b;
                     const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, false);
                     row[i] = upper ? got : a;
@@ -490,7 +496,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    row[i] = k[sub][0][i];
+                    row[i] = raw.k[sub][0][i];
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -562,8 +568,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
             uint32_t low[4], high[4];    // elements 0, 1 and 2, 3 of the dword, each for two keys
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                low[i] = __builtin_amdgcn_perm(v[2 * i + 1][l], v[2 * i][l], 0x05010400);
-                high[i] = __builtin_amdgcn_perm(v[2 * i + 1][l], v[2 * i][l], 0x07030602);
+                low[i] = __builtin_amdgcn_perm(raw.v[2 * i + 1][l], raw.v[2 * i][l], 0x05010400);
+                high[i] = __builtin_amdgcn_perm(raw.v[2 * i + 1][l], raw.v[2 * i][l], 0x07030602);
             }
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
@@ -579,6 +585,29 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                                                                               o[nt][4 * l + d], 0, 0, 0);
             }
         }
+    };
+
+    // Each wave loads two units ahead: while it computes one, the next is on its way. The queries are there before the
+    // loop, or its first use of them would wait for every load in each round.
+    if (units > 0) {
+        even.page = load_page(0);
+        odd.page = load_page(1);
+        load(0, even);
+        load(1, odd);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int t = 0; t < KS; ++t)
+                asm volatile("" : "+v"(q[nt][t]));
+        // (No way out in the middle: where two ways join, loads are waited for as on the shorter one.)
+        for (int u = 0; u + 1 < units; u += 2) {
+            attend(u, even);
+            load(u + 2, even);
+            attend(u + 1, odd);
+            load(u + 3, odd);
+        }
+        if (units & 1)
+            attend(units - 1, even);
     }
 
     // The four waves' sums, over their largest reference.
@@ -691,16 +720,13 @@ template <int D>
 __global__ __launch_bounds__(kThreads) void join_few_kernel(AttendParams p)
 {
     const int r = blockIdx.y, b = blockIdx.x / p.heads, head = blockIdx.x - b * p.heads;
-    int pieces = 0, before = 0, start = 0, rows = 0;
-    for_pieces(p, [&](int b0, const Sequence &s, int, int n, int first) {
-        if (b >= b0 + 64)
-            return false;
-        pieces = lane_int(n, b - b0);
-        before = lane_int(first, b - b0);
-        start = lane_int(s.start, b - b0);
-        rows = lane_int(s.rows, b - b0);
-        return true;
-    });
+    Cut c;
+    const int chunk = chunk_of(p, c);
+    int upto = 0;
+    for (int b0 = 0; b0 <= b; b0 += 64)
+        upto = cut(p, b0, chunk, upto, c);
+    const int pieces = lane_int(c.pieces, b % 64), before = lane_int(c.before, b % 64);
+    const int start = lane_int(c.s.start, b % 64), rows = lane_int(c.s.rows, b % 64);
     if (pieces < 2 || r >= rows)
         return;
     const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
@@ -826,18 +852,17 @@ __device__ __forceinline__ void bring(int tiles, const Rider &rider, Load load, 
     store(0, even);
     load(2, even);
     __syncthreads();
-    for (int t = 0;; t += 2) {
+    // (No way out in the middle: where two ways join, loads are waited for as on the shorter one.)
+    for (int t = 0; t + 1 < tiles; t += 2) {
         store(t + 1, odd);
         load(t + 3, odd);
         __syncthreads();
-        if (t + 1 >= tiles)
-            break;
         store(t + 2, even);
         load(t + 4, even);
         __syncthreads();
-        if (t + 2 >= tiles)
-            break;
     }
+    if (tiles & 1)                       // there is nothing to bring in any more
+        __syncthreads();
 }
 
 // K: codes to bf16.
