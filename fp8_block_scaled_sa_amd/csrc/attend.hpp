@@ -48,8 +48,9 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kUnit = 128;               // keys that a workgroup of the few-rows kernel takes at once
-constexpr int kFewRows = 64;             // most rows (tokens x heads of a group) of its sequences
+constexpr int kFewRows = 32;             // most rows (tokens x heads of a group) of its sequences
 constexpr int kTileRows = 256;           // rows of a workgroup of the many-rows kernel
+constexpr int kJoinRows = 16;            // of a cut tile, that a workgroup joins
 constexpr int kTileKeys = 64;            // keys that a workgroup of the many-rows kernel takes at once
 constexpr float kNoMax = -1e30f;         // reference of a row that has seen nothing; finite, so that differences are
 constexpr float kSlack = 8.0f;           // how far x may pass its reference
@@ -82,7 +83,7 @@ struct AttendParams {
     float scale_log2;                    // scale / ln 2
     int few_rows;                        // sequences of up to so many rows are the few-rows kernel's
     int target, min_units;               // few rows: workgroups aimed at, and units that one takes at least
-    int splits;                          // many rows: workgroups that share a tile's keys
+    int most_pieces;                     // many rows: workgroups up to which tiles may be cut (0: not at all)
     int part_rows;                       // rows of a piece's partial result
     float *part_o;                       // [piece][part_rows][D], sums over p sV V
     float *part_ml;                      // [piece][part_rows][2], reference and sum of p
@@ -736,39 +737,159 @@ __global__ __launch_bounds__(kThreads) void join_few_kernel(AttendParams p)
 
 // ---------------------------------------------------------------- many rows
 
-// A tile of rows: which sequence's, and the first of its rows.
+// A tile of rows of one key head, and the piece of its keys that a workgroup takes.
 struct Tile {
     Sequence s;
-    int b, first;
+    int b, first, head;                  // sequence, first row
+    int pieces, piece, slot;             // pieces of its keys; this one's number; the place of its partial result
 };
 
-// The index-th tile, the last (longest) tiles of a sequence first.
-__device__ __forceinline__ bool find_tile(const AttendParams &p, int index, int tile_rows, Tile &w)
+// How the tiles of 64 sequences are cut, this lane's one.
+struct Cuts {
+    Sequence s;
+    int tiles, keys;                     // tiles of rows; tiles of keys that the longest of them reads
+    int pieces;                          // of each tile's keys
+};
+
+__device__ __forceinline__ void lane_tiles(const AttendParams &p, int b, Cuts &c)
+{
+    c.s.rows = 0;
+    if (b < p.B)
+        c.s = sequence(p, b);
+    c.tiles = c.s.rows > p.few_rows ? (c.s.rows + kTileRows - 1) / kTileRows : 0;
+    c.keys = c.tiles ? max(1, (c.s.n - (c.s.low & ~(kTileKeys - 1)) + kTileKeys - 1) / kTileKeys) : 0;
+}
+
+// Pieces of a tile of this lane's sequence, of about 1 / rate tiles of keys each.
+__device__ __forceinline__ int pieces_of(const Cuts &c, float rate) { return max(1, (int)((float)c.keys * rate + 0.5f)); }
+
+// How tiles are cut: the reciprocal of the tiles of keys of a piece, 0 for not at
+// all. Every workgroup comes to the same estimate from the lengths, in units of
+// the time that a workgroup takes for one tile of keys (1.8 us): pieces that fill
+// the 256 CUs at most once take as long as the longest; one sequence's, equal
+// ones, as many rounds as they fill; uneven ones their average and a part of the
+// longest. Cutting costs the joining launch's work (2), and for each piece its
+// partial result's way out and back. (16 sequences of 16 tokens, 8 heads of 8, up
+// to 8192 tokens: 370 us uncut, MEASURED us cut.)
+__device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
 {
     const int lane = threadIdx.x & 63;
+    float total = 0.0f;
+    int most = 0, pieces = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64) {
+        Cuts c;
+        lane_tiles(p, b0 + lane, c);
+        if (b0 == 0)
+            first = c;
+        total += (float)c.tiles * (float)c.keys;
+        pieces += c.tiles;
+        most = max(most, c.keys);
+    }
+    if (p.most_pieces == 0)
+        return 0.0f;
+    const float cost = 0.03f * (float)p.part_rows / kTileRows, heads = (float)p.heads;
+    float best = 0.0f;
+    if (p.B == 1) {
+        const float tiles = (float)lane_int(pieces, 0) * heads, keys = (float)lane_int(most, 0);
+        float least = keys * __builtin_ceilf(tiles / 256.0f);
+#pragma unroll
+        for (int rounds = 1; rounds <= 3; ++rounds) {
+            const float parts = fminf(__builtin_floorf(256.0f * (float)rounds / tiles), keys);
+            const float time = (float)rounds * keys / parts + 2.0f + cost * tiles * parts;
+            if (parts >= 2.0f && time < least) {
+                least = time;
+                best = parts / keys;
+            }
+        }
+        return best;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        total += __shfl_xor(total, d, 64);
+        most = max(most, __shfl_xor(most, d, 64));
+    }
+    total *= heads / 256.0f;
+    pieces = lane_int(scan(pieces), 63) * p.heads;
+    const auto estimate = [&](float longest) { return pieces <= 256 ? longest : fmaxf(longest, 1.1f * total + 0.3f * longest); };
+    float least = estimate((float)most);
+    for (int parts = 2; parts <= 16 && parts <= most && least > total + 2.0f; parts *= 2) {
+        const float rate = (float)parts / (float)most;
+        pieces = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 64) {
+            Cuts c = first;
+            if (b0)
+                lane_tiles(p, b0 + lane, c);
+            pieces += c.tiles * pieces_of(c, rate);
+        }
+        pieces = lane_int(scan(pieces), 63) * p.heads;
+        const float time = estimate((float)most / (float)parts) + 2.0f + cost * (float)pieces;
+        if (pieces > p.most_pieces || time >= least)
+            break;
+        least = time;
+        best = rate;
+    }
+    return best;
+}
+
+// The block's piece: of a sequence, the last (longest) tiles first, heads next to each other.
+__device__ __forceinline__ bool find_tile(const AttendParams &p, int block, Tile &w)
+{
+    Cuts c;
+    const float rate = cut_tiles(p, c);
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 64) {
-        Sequence s;
-        int tiles = 0;
-        s.rows = 0;
-        if (b0 + lane < p.B)
-            s = sequence(p, b0 + lane);
-        if (s.rows > p.few_rows)
-            tiles = (s.rows + tile_rows - 1) / tile_rows;
-        const int upto = before + scan(tiles);
-        const uint64_t mine = __ballot(index >= upto - tiles && index < upto);
+        if (b0)
+            lane_tiles(p, b0 + (threadIdx.x & 63), c);
+        c.pieces = pieces_of(c, rate);
+        const int all = c.tiles * c.pieces * p.heads, upto = before + scan(all);
+        const uint64_t mine = __ballot(block >= upto - all && block < upto);
         if (mine) {
             const int l = __builtin_ctzll(mine);
             w.b = b0 + l;
-            w.s.start = lane_int(s.start, l);
-            w.s.m = lane_int(s.m, l);
-            w.s.n = lane_int(s.n, l);
+            w.s.start = lane_int(c.s.start, l);
+            w.s.m = lane_int(c.s.m, l);
+            w.s.n = lane_int(c.s.n, l);
             w.s.low = 0;
-            w.s.rows = lane_int(s.rows, l);
-            w.first = (lane_int(upto, l) - 1 - index) * tile_rows;
+            w.s.rows = lane_int(c.s.rows, l);
+            w.pieces = lane_int(c.pieces, l);
+            const int at = block - lane_int(upto - all, l), share = at / p.heads, tile = share / w.pieces;
+            w.head = at - share * p.heads;
+            w.piece = share - tile * w.pieces;
+            w.first = (lane_int(c.tiles, l) - 1 - tile) * kTileRows;
+            w.slot = block;
             return true;
         }
         before = lane_int(upto, 63);
+    }
+    return false;
+}
+
+// The index-th cut tile (of all key heads), with the place of its first piece's partial result.
+__device__ __forceinline__ bool find_cut_tile(const AttendParams &p, int index, Tile &w)
+{
+    Cuts c;
+    const float rate = cut_tiles(p, c);
+    int tiles_before = 0, pieces_before = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64) {
+        if (b0)
+            lane_tiles(p, b0 + (threadIdx.x & 63), c);
+        c.pieces = pieces_of(c, rate);
+        const int tiles = c.pieces > 1 ? c.tiles * p.heads : 0, all = c.tiles * c.pieces * p.heads;
+        const int tiles_upto = tiles_before + scan(tiles), upto = pieces_before + scan(all);
+        const uint64_t mine = __ballot(index >= tiles_upto - tiles && index < tiles_upto);
+        if (mine) {
+            const int l = __builtin_ctzll(mine);
+            w.s.start = lane_int(c.s.start, l);
+            w.s.rows = lane_int(c.s.rows, l);
+            w.pieces = lane_int(c.pieces, l);
+            const int at = index - lane_int(tiles_upto - tiles, l), tile = at / p.heads;
+            w.head = at - tile * p.heads;
+            w.first = (lane_int(c.tiles, l) - 1 - tile) * kTileRows;
+            w.slot = lane_int(upto - all, l) + tile * w.pieces * p.heads + w.head;
+            return true;
+        }
+        tiles_before = lane_int(tiles_upto, 63);
+        pieces_before = lane_int(upto, 63);
     }
     return false;
 }
@@ -1026,7 +1147,7 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
     bring(k.tiles, rider, load, store, even, odd);
 }
 
-// One tile of 256 rows of one key head over its keys, or over one of p.splits shares of them.
+// One tile of 256 rows of one key head over its keys, or over a piece of them.
 //
 // The products are transposed as in the few-rows kernel, on 32x32x16
 // instructions: each of eight waves holds 32 rows (Q^T and O^T in registers), a
@@ -1042,11 +1163,10 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
     constexpr int DT = D / 32;           // tiles of O^T
     __shared__ ManyLds<D> lds;
 
-    const int share = blockIdx.x / p.heads, head = blockIdx.x - share * p.heads;
-    const int index = share / p.splits, split = share - index * p.splits;
     Tile w;
-    if (!find_tile(p, index, kTileRows, w))
+    if (!find_tile(p, blockIdx.x, w))
         return;
+    const int head = w.head;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int last = min(w.first + kTileRows, w.s.rows) - 1;
     const int base = w.s.n - w.s.m;      // position of the first new token
@@ -1056,10 +1176,10 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
     k.low = p.window ? max(0, k.pos_first - p.window + 1) : 0;
     const int start = k.low & ~(kTileKeys - 1);
     const int tiles_in_all = max(0, (k.pos_last - start + kTileKeys) / kTileKeys);
-    const int tile0 = (int)((int64_t)tiles_in_all * split / p.splits);
-    k.tiles = (int)((int64_t)tiles_in_all * (split + 1) / p.splits) - tile0;
+    const int tile0 = (int)((int64_t)tiles_in_all * w.piece / w.pieces);
+    k.tiles = (int)((int64_t)tiles_in_all * (w.piece + 1) / w.pieces) - tile0;
     k.key0 = start + tile0 * kTileKeys;
-    k.last = min(k.pos_last, k.key0 + k.tiles * kTileKeys - 1);           // of this share
+    k.last = min(k.pos_last, k.key0 + k.tiles * kTileKeys - 1);           // of this piece
 
     if (wave >= kComputeWaves) {
         if (k.tiles == 0)
@@ -1176,10 +1296,11 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
             weigh();
             const int e = __builtin_amdgcn_readfirstlane((int)about[2 + b]);
             if (__ballot(part > limit) || e != exponent) {
-                // A larger reference of V shrinks the sums to it; a smaller one (of the half tiles that two waves bring
-                // in) lets them grow again.
-                const float change = exponent - e < -126 ? 0.0f : power_of_2(min(exponent - e, 127));
-                exponent = e;
+                // The sums shrink to a larger reference of V; for a smaller one (two waves bring in V, with a reference
+                // each) the weights do.
+                const float change = exponent - e < -126 ? 0.0f : power_of_2(min(exponent - e, 0));
+                const _Float16 lower = (_Float16)(e - exponent < -126 ? 0.0f : power_of_2(min(e - exponent, 0)));
+                exponent = max(exponent, e);
                 float top = x[b][0];
 #pragma unroll
                 for (int i = 1; i < 16; ++i)
@@ -1200,6 +1321,10 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                 ref += by;
                 limit = moves ? kMostWeight : limit;
                 weigh();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    weights[i / 4][i % 4] = __builtin_bit_cast(
+                        uint32_t, __builtin_bit_cast(f16x2, (uint32_t)weights[i / 4][i % 4]) * f16x2{lower, lower});
             }
             sum += part;
 #pragma unroll
@@ -1220,7 +1345,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
     // Registers i % 8 of all tiles hold consecutive elements.
     constexpr int E = 2 * DT;
     uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h;
-    const int64_t at = (int64_t)blockIdx.x * p.part_rows + r - w.first;
+    const int64_t at = (int64_t)w.slot * p.part_rows + r - w.first;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int element = E * (8 * (i / 4) + 4 * hf + i % 4);
@@ -1230,7 +1355,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
 #pragma unroll
             for (int e = 0; e < 2; ++e)
                 y[2 * d + e] = o[d][i + 8 * e] * factor;
-        if (p.splits == 1) {
+        if (w.pieces == 1) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
@@ -1241,25 +1366,46 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                 *(f32x4 *)(p.part_o + at * D + element + e) = f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
         }
     }
-    if (p.splits > 1 && hf == 0)
+    if (w.pieces > 1 && hf == 0)
         *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kUnset ? kNoMax : ref, sum};
 }
 
-// One row of a tile (blockIdx.x: tile and key head, blockIdx.y: row) whose keys were split.
+// Rows of a cut tile (blockIdx.x: tile and key head, blockIdx.y: kJoinRows of them), a wave a row at a time.
 template <int D>
 __global__ __launch_bounds__(kThreads) void join_many_kernel(AttendParams p)
 {
-    const int index = blockIdx.x / p.heads, head = blockIdx.x - index * p.heads;
+    constexpr int E = D / 64;
     Tile w;
-    if (!find_tile(p, index, p.part_rows, w))
+    if (!find_cut_tile(p, blockIdx.x, w))
         return;
-    const int r = w.first + (int)blockIdx.y;
-    if (r >= w.s.rows)
-        return;
-    const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
-    join<D>(p, p.splits,
-            [&](int i) { return (int64_t)((index * p.splits + i) * p.heads + head) * p.part_rows + blockIdx.y; },
-            p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    for (int i = kJoinRows * blockIdx.y + wave; i < kJoinRows * ((int)blockIdx.y + 1) && w.first + i < w.s.rows; i += 4) {
+        const auto index = [&](int piece) { return (int64_t)(w.slot + piece * p.heads) * p.part_rows + i; };
+        float top = kNoMax;
+        for (int piece = 0; piece < w.pieces; ++piece)
+            top = fmaxf(top, p.part_ml[2 * index(piece)]);
+        float total = 0.0f, y[E] = {};
+#pragma unroll 4
+        for (int piece = 0; piece < w.pieces; ++piece) {
+            const int64_t at = index(piece);
+            const f32x2 ml = *(const f32x2 *)(p.part_ml + 2 * at);
+            const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
+            total = __builtin_fmaf(ml[1], weight, total);
+            const float *o = p.part_o + at * D + E * lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                y[e] = __builtin_fmaf(o[e], weight, y[e]);
+        }
+        const int r = w.first + i, token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+        uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(w.head * (int)p.group.d + h) * p.o_h + E * lane;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            y[e] = total == 0.0f ? 0.0f : y[e] / total;
+        if (E == 2)
+            *(uint32_t *)to = dgn::pack_bf16(y[0], y[E - 1]);
+        else
+            *to = (uint16_t)dgn::pack_bf16(y[0], 0.0f);
+    }
 }
 
 }  // namespace dga

@@ -167,17 +167,17 @@ struct AttendPlan {
     int64_t pieces;        // its workgroups at most, which is what its partial results take
     int64_t part_rows;
     int tile_rows;         // of the many-rows kernel (0: there cannot be sequences of more rows)
-    int64_t many_tiles;    // their tiles at most
-    int splits;            // workgroups that share a tile's keys
-    int64_t many_pieces;
+    int64_t many_tiles;    // their tiles, of all key heads, at most
+    int64_t most_pieces;   // of cut tiles (0: none is)
+    int64_t many_rows;     // rows of a piece's partial result
     int64_t bytes;         // of the workspace
     int64_t most_bytes;    // of the workspace of any call with at most these sizes
 };
 
 constexpr int kFewTarget = 1024;
 constexpr int kFewMinUnits = 1;
-constexpr int kManyTarget = 256;
-constexpr int kMaxSplits = 16;
+constexpr int64_t kMostPieces = 768;
+constexpr int64_t kUncutTiles = 4096;
 
 AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64_t D, int64_t max_q_len)
 {
@@ -186,7 +186,7 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
     const bool many = rows > dga::kFewRows;
     // Beside chunks, the few-rows kernel is for the sequences with a single token; one sequence alone takes one kernel.
     const int64_t few = !many ? rows : B > 1 && group <= dga::kFewRows ? group : 0;
-    a.tiles = few == 0 ? 0 : few <= 16 ? 1 : few <= 32 ? 2 : 4;
+    a.tiles = few == 0 ? 0 : few <= 16 ? 1 : 2;
     a.few_rows = 16 * a.tiles;
     if (a.tiles) {
         a.pieces = kFewTarget + B * heads;
@@ -196,13 +196,12 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
     a.most_bytes = (kFewTarget + B * heads) * std::min<int64_t>(dga::kFewRows, rows) * (D + 2) * 4;
     if (many) {
         a.tile_rows = dga::kTileRows;
-        a.many_tiles = (T * group + std::min(B, T) * (a.tile_rows - 1)) / a.tile_rows;
-        a.splits = (int)std::min<int64_t>(std::max<int64_t>(kManyTarget / (a.many_tiles * heads), 1), kMaxSplits);
-        a.many_pieces = a.many_tiles * heads * a.splits;
-        if (a.splits > 1)
-            a.bytes = std::max(a.bytes, a.many_pieces * a.tile_rows * (D + 2) * 4);
-        // With more than one share, a launch has at most kManyTarget workgroups.
-        a.most_bytes = std::max<int64_t>(a.most_bytes, (int64_t)kManyTarget * dga::kTileRows * (D + 2) * 4);
+        a.many_tiles = (T * group + std::min(B, T) * (a.tile_rows - 1)) / a.tile_rows * heads;
+        // Where there can be so many tiles, none is cut.
+        a.most_pieces = a.many_tiles < kUncutTiles ? kMostPieces : 0;
+        a.many_rows = std::min<int64_t>(a.tile_rows, rows);
+        a.bytes = std::max(a.bytes, a.most_pieces * a.many_rows * (D + 2) * 4);
+        a.most_bytes = std::max(a.most_bytes, kMostPieces * a.many_rows * (D + 2) * 4);
     }
     return a;
 }
@@ -220,8 +219,7 @@ int check_attend_sizes(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int
     if (T == 0 || B == 0)
         return DG_OK;
     const AttendPlan a = plan_attend(T, B, heads, q_heads / heads, D, max_q_len);
-    if (a.pieces > kMaxPieces || a.many_pieces > kMaxPieces || B * heads * a.part_rows > kMaxPieces ||
-        (a.splits > 1 && a.many_tiles * heads * a.tile_rows > kMaxPieces))
+    if (a.pieces > kMaxPieces || a.many_tiles > kMaxPieces / 3 || B * heads * a.part_rows > kMaxPieces)
         return DG_ERR_UNSUPPORTED;
     return DG_OK;
 }
@@ -240,10 +238,8 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
         const dim3 grid((unsigned)std::min<int64_t>(a.pieces, p.B * p.heads * std::max<int64_t>(most, 1)));
         if (a.tiles == 1)
             hipLaunchKernelGGL((dga::attend_few_kernel<D, 1>), grid, threads, 0, stream, p);
-        else if (a.tiles == 2)
-            hipLaunchKernelGGL((dga::attend_few_kernel<D, 2>), grid, threads, 0, stream, p);
         else
-            hipLaunchKernelGGL((dga::attend_few_kernel<D, 4>), grid, threads, 0, stream, p);
+            hipLaunchKernelGGL((dga::attend_few_kernel<D, 2>), grid, threads, 0, stream, p);
         int st = launched();
         if (st != DG_OK)
             return st;
@@ -255,16 +251,18 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
         }
     }
     if (a.tile_rows) {
-        p.splits = a.splits;
-        p.part_rows = a.tile_rows;
-        p.part_ml = p.part_o + a.many_pieces * a.tile_rows * D;
-        const dim3 grid((unsigned)a.many_pieces);
-        hipLaunchKernelGGL((dga::attend_many_kernel<D>), grid, dim3(dga::kManyThreads), 0, stream, p);
+        p.most_pieces = (int)a.most_pieces;
+        p.part_rows = (int)a.many_rows;
+        p.part_ml = p.part_o + a.most_pieces * a.many_rows * D;
+        hipLaunchKernelGGL((dga::attend_many_kernel<D>), dim3((unsigned)std::max(a.many_tiles, a.most_pieces)),
+                           dim3(dga::kManyThreads), 0, stream, p);
         int st = launched();
         if (st != DG_OK)
             return st;
-        if (a.splits > 1) {
-            hipLaunchKernelGGL((dga::join_many_kernel<D>), dim3((unsigned)(a.many_tiles * p.heads), (unsigned)a.tile_rows),
+        if (a.most_pieces) {
+            hipLaunchKernelGGL((dga::join_many_kernel<D>),
+                               dim3((unsigned)std::min(a.many_tiles, a.most_pieces / 2),
+                                    (unsigned)((a.many_rows + dga::kJoinRows - 1) / dga::kJoinRows)),
                                threads, 0, stream, p);
             return launched();
         }
