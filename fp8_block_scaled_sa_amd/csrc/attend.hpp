@@ -50,7 +50,8 @@ constexpr int kThreads = 256;
 constexpr int kUnit = 128;               // keys that a workgroup of the few-rows kernel takes at once
 constexpr int kFewRows = 32;             // most rows (tokens x heads of a group) of its sequences
 constexpr int kTileRows = 256;           // rows of a workgroup of the many-rows kernel
-constexpr int kJoinRows = 16;            // of a cut tile, that a workgroup joins
+constexpr int kJoinRows = 16;            // of a cut tile, that a workgroup joins at a time
+constexpr int kJoinGroups = 1024;        // workgroups that do
 constexpr int kTileKeys = 64;            // keys that a workgroup of the many-rows kernel takes at once
 constexpr float kNoMax = -1e30f;         // reference of a row that has seen nothing; finite, so that differences are
 constexpr float kSlack = 8.0f;           // how far x may pass its reference
@@ -65,6 +66,13 @@ struct Rows {
     int64_t head;
     const float *scales;
     int64_t s_page, s_token, s_head;
+};
+
+// Where pieces leave their partial results.
+struct Parts {
+    int rows;                            // of a piece
+    float *o;                            // [piece][rows][D], sums over p sV V
+    float *ml;                           // [piece][rows][2], reference and sum of p
 };
 
 struct AttendParams {
@@ -84,9 +92,8 @@ struct AttendParams {
     int few_rows;                        // sequences of up to so many rows are the few-rows kernel's
     int target, min_units;               // few rows: workgroups aimed at, and units that one takes at least
     int most_pieces;                     // many rows: workgroups up to which tiles may be cut (0: not at all)
-    int part_rows;                       // rows of a piece's partial result
-    float *part_o;                       // [piece][part_rows][D], sums over p sV V
-    float *part_ml;                      // [piece][part_rows][2], reference and sum of p
+    Parts few, many;                     // partial results of the two kernels
+    int few_joined;                      // workgroups of the joining launch that join the first kernel's
 };
 
 // A sequence as the device arrays give it; anything out of range counts as nothing.
@@ -659,12 +666,12 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 store_bf16<DT>(p.out + (int64_t)(w.s.start + token) * p.o_t +
                                    (int64_t)(w.head * (int)p.group.d + h) * p.o_h + col, y);
             } else {
-                const int64_t at = (int64_t)w.index * p.part_rows + r;
+                const int64_t at = (int64_t)w.index * p.few.rows + r;
 #pragma unroll
                 for (int t = 0; t < DT; t += 4)
-                    *(f32x4 *)(p.part_o + at * D + col + t) = f32x4{y[t], y[t + 1], y[t + 2], y[t + 3]};
+                    *(f32x4 *)(p.few.o + at * D + col + t) = f32x4{y[t], y[t + 1], y[t + 2], y[t + 3]};
                 if (col == 0)
-                    *(f32x2 *)(p.part_ml + 2 * at) = f32x2{most, total};
+                    *(f32x2 *)(p.few.ml + 2 * at) = f32x2{most, total};
             }
         }
         __syncthreads();
@@ -681,7 +688,7 @@ __device__ __forceinline__ void join(const AttendParams &p, int count, Index ind
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     float top = kNoMax;
     for (int i = lane; i < count; i += 64)
-        top = fmaxf(top, p.part_ml[2 * index(i)]);
+        top = fmaxf(top, p.few.ml[2 * index(i)]);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         top = fmaxf(top, __shfl_xor(top, d, 64));
@@ -689,10 +696,10 @@ __device__ __forceinline__ void join(const AttendParams &p, int count, Index ind
 #pragma unroll 4
     for (int i = wave; i < count; i += 4) {
         const int64_t at = index(i);
-        const f32x2 ml = *(const f32x2 *)(p.part_ml + 2 * at);
+        const f32x2 ml = *(const f32x2 *)(p.few.ml + 2 * at);
         const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
         total = __builtin_fmaf(ml[1], weight, total);
-        const float *o = p.part_o + at * D + E * lane;
+        const float *o = p.few.o + at * D + E * lane;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             y[e] = __builtin_fmaf(o[e], weight, y[e]);
@@ -716,11 +723,11 @@ __device__ __forceinline__ void join(const AttendParams &p, int count, Index ind
     }
 }
 
-// One row of a sequence (blockIdx.x: sequence and key head, blockIdx.y: row) that several pieces share.
+// One row of a sequence that several pieces share; rows of a sequence and head next to each other.
 template <int D>
-__global__ __launch_bounds__(kThreads) void join_few_kernel(AttendParams p)
+__device__ __forceinline__ void join_few(const AttendParams &p, int block)
 {
-    const int r = blockIdx.y, b = blockIdx.x / p.heads, head = blockIdx.x - b * p.heads;
+    const int of = block / p.few.rows, r = block - of * p.few.rows, b = of / p.heads, head = of - b * p.heads;
     Cut c;
     const int chunk = chunk_of(p, c);
     int upto = 0;
@@ -731,7 +738,7 @@ __global__ __launch_bounds__(kThreads) void join_few_kernel(AttendParams p)
     if (pieces < 2 || r >= rows)
         return;
     const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
-    join<D>(p, pieces, [&](int i) { return (int64_t)(before + i * p.heads + head) * p.part_rows + r; },
+    join<D>(p, pieces, [&](int i) { return (int64_t)(before + i * p.heads + head) * p.few.rows + r; },
             p.out + (int64_t)(start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h);
 }
 
@@ -787,7 +794,7 @@ __device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
     }
     if (p.most_pieces == 0)
         return 0.0f;
-    const float cost = 0.03f * (float)p.part_rows / kTileRows, heads = (float)p.heads;
+    const float cost = 0.03f * (float)p.many.rows / kTileRows, heads = (float)p.heads;
     float best = 0.0f;
     if (p.B == 1) {
         const float tiles = (float)lane_int(pieces, 0) * heads, keys = (float)lane_int(most, 0);
@@ -865,10 +872,9 @@ __device__ __forceinline__ bool find_tile(const AttendParams &p, int block, Tile
 }
 
 // The index-th cut tile (of all key heads), with the place of its first piece's partial result.
-__device__ __forceinline__ bool find_cut_tile(const AttendParams &p, int index, Tile &w)
+__device__ __forceinline__ bool find_cut_tile(const AttendParams &p, float rate, const Cuts &first, int index, Tile &w)
 {
-    Cuts c;
-    const float rate = cut_tiles(p, c);
+    Cuts c = first;
     int tiles_before = 0, pieces_before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 64) {
         if (b0)
@@ -1345,7 +1351,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
     // Registers i % 8 of all tiles hold consecutive elements.
     constexpr int E = 2 * DT;
     uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h;
-    const int64_t at = (int64_t)w.slot * p.part_rows + r - w.first;
+    const int64_t at = (int64_t)w.slot * p.many.rows + r - w.first;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int element = E * (8 * (i / 4) + 4 * hf + i % 4);
@@ -1363,49 +1369,62 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
         } else {
 #pragma unroll
             for (int e = 0; e < E; e += 4)
-                *(f32x4 *)(p.part_o + at * D + element + e) = f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
+                *(f32x4 *)(p.many.o + at * D + element + e) = f32x4{y[e], y[e + 1], y[e + 2], y[e + 3]};
         }
     }
     if (w.pieces > 1 && hf == 0)
-        *(f32x2 *)(p.part_ml + 2 * at) = f32x2{limit == kUnset ? kNoMax : ref, sum};
+        *(f32x2 *)(p.many.ml + 2 * at) = f32x2{limit == kUnset ? kNoMax : ref, sum};
 }
 
-// Rows of a cut tile (blockIdx.x: tile and key head, blockIdx.y: kJoinRows of them), a wave a row at a time.
+// The rows of the cut tiles, kJoinRows at a time, a wave a row.
 template <int D>
-__global__ __launch_bounds__(kThreads) void join_many_kernel(AttendParams p)
+__device__ __forceinline__ void join_many(const AttendParams &p, int block, int blocks)
 {
     constexpr int E = D / 64;
-    Tile w;
-    if (!find_cut_tile(p, blockIdx.x, w))
-        return;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int i = kJoinRows * blockIdx.y + wave; i < kJoinRows * ((int)blockIdx.y + 1) && w.first + i < w.s.rows; i += 4) {
-        const auto index = [&](int piece) { return (int64_t)(w.slot + piece * p.heads) * p.part_rows + i; };
-        float top = kNoMax;
-        for (int piece = 0; piece < w.pieces; ++piece)
-            top = fmaxf(top, p.part_ml[2 * index(piece)]);
-        float total = 0.0f, y[E] = {};
-#pragma unroll 4
-        for (int piece = 0; piece < w.pieces; ++piece) {
-            const int64_t at = index(piece);
-            const f32x2 ml = *(const f32x2 *)(p.part_ml + 2 * at);
-            const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
-            total = __builtin_fmaf(ml[1], weight, total);
-            const float *o = p.part_o + at * D + E * lane;
-#pragma unroll
+    const int shares = (p.many.rows + kJoinRows - 1) / kJoinRows;
+    Cuts c;
+    const float rate = cut_tiles(p, c);
+    Tile w;
+    for (; find_cut_tile(p, rate, c, block / shares, w); block += blocks) {
+        const int from = kJoinRows * (block % shares);
+        for (int i = from + wave; i < from + kJoinRows && w.first + i < w.s.rows; i += 4) {
+            const auto index = [&](int piece) { return (int64_t)(w.slot + piece * p.heads) * p.many.rows + i; };
+            float top = kNoMax;
+            for (int piece = 0; piece < w.pieces; ++piece)
+                top = fmaxf(top, p.many.ml[2 * index(piece)]);
+            float total = 0.0f, y[E] = {};
+    #pragma unroll 4
+            for (int piece = 0; piece < w.pieces; ++piece) {
+                const int64_t at = index(piece);
+                const f32x2 ml = *(const f32x2 *)(p.many.ml + 2 * at);
+                const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
+                total = __builtin_fmaf(ml[1], weight, total);
+                const float *o = p.many.o + at * D + E * lane;
+    #pragma unroll
+                for (int e = 0; e < E; ++e)
+                    y[e] = __builtin_fmaf(o[e], weight, y[e]);
+            }
+            const int r = w.first + i, token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
+            uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(w.head * (int)p.group.d + h) * p.o_h + E * lane;
+    #pragma unroll
             for (int e = 0; e < E; ++e)
-                y[e] = __builtin_fmaf(o[e], weight, y[e]);
+                y[e] = total == 0.0f ? 0.0f : y[e] / total;
+            if (E == 2)
+                *(uint32_t *)to = dgn::pack_bf16(y[0], y[E - 1]);
+            else
+                *to = (uint16_t)dgn::pack_bf16(y[0], 0.0f);
         }
-        const int r = w.first + i, token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
-        uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(w.head * (int)p.group.d + h) * p.o_h + E * lane;
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            y[e] = total == 0.0f ? 0.0f : y[e] / total;
-        if (E == 2)
-            *(uint32_t *)to = dgn::pack_bf16(y[0], y[E - 1]);
-        else
-            *to = (uint16_t)dgn::pack_bf16(y[0], 0.0f);
     }
+}
+
+template <int D>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p)
+{
+    if ((int)blockIdx.x < p.few_joined)
+        join_few<D>(p, blockIdx.x);
+    else
+        join_many<D>(p, blockIdx.x - p.few_joined, gridDim.x - p.few_joined);
 }
 
 }  // namespace dga

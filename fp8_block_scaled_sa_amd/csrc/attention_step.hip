@@ -165,11 +165,11 @@ struct AttendPlan {
     int tiles;             // 16-row tiles of the few-rows kernel (0: none of the sequences is its)
     int few_rows;          // rows up to which a sequence is its
     int64_t pieces;        // its workgroups at most, which is what its partial results take
-    int64_t part_rows;
+    int64_t part_rows;     // rows of a piece's partial result
     int tile_rows;         // of the many-rows kernel (0: there cannot be sequences of more rows)
     int64_t many_tiles;    // their tiles, of all key heads, at most
     int64_t most_pieces;   // of cut tiles (0: none is)
-    int64_t many_rows;     // rows of a piece's partial result
+    int64_t many_rows;
     int64_t bytes;         // of the workspace
     int64_t most_bytes;    // of the workspace of any call with at most these sizes
 };
@@ -200,8 +200,8 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
         // Where there can be so many tiles, none is cut.
         a.most_pieces = a.many_tiles < kUncutTiles ? kMostPieces : 0;
         a.many_rows = std::min<int64_t>(a.tile_rows, rows);
-        a.bytes = std::max(a.bytes, a.most_pieces * a.many_rows * (D + 2) * 4);
-        a.most_bytes = std::max(a.most_bytes, kMostPieces * a.many_rows * (D + 2) * 4);
+        a.bytes += a.most_pieces * a.many_rows * (D + 2) * 4;
+        a.most_bytes += kMostPieces * a.many_rows * (D + 2) * 4;
     }
     return a;
 }
@@ -219,7 +219,7 @@ int check_attend_sizes(int64_t T, int64_t B, int64_t q_heads, int64_t heads, int
     if (T == 0 || B == 0)
         return DG_OK;
     const AttendPlan a = plan_attend(T, B, heads, q_heads / heads, D, max_q_len);
-    if (a.pieces > kMaxPieces || a.many_tiles > kMaxPieces / 3 || B * heads * a.part_rows > kMaxPieces)
+    if (a.pieces > kMaxPieces || a.many_tiles > kMaxPieces / 3 || B * heads * a.part_rows > kMaxPieces - dga::kJoinGroups)
         return DG_ERR_UNSUPPORTED;
     return DG_OK;
 }
@@ -229,43 +229,38 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
 {
     const dim3 threads(dga::kThreads);
     p.few_rows = a.few_rows;
+    int st;
+    int64_t joined = 0;
+    float *parts = p.few.o;
     if (a.tiles) {
         p.target = kFewTarget;
         p.min_units = kFewMinUnits;
-        p.part_rows = (int)a.part_rows;
-        p.part_ml = p.part_o + a.pieces * a.part_rows * D;
+        p.few = dga::Parts{(int)a.part_rows, parts, parts + a.pieces * a.part_rows * D};
+        parts += a.pieces * a.part_rows * (D + 2);
         const int64_t most = (units + kFewMinUnits - 1) / kFewMinUnits;    // pieces of a sequence and head at most
         const dim3 grid((unsigned)std::min<int64_t>(a.pieces, p.B * p.heads * std::max<int64_t>(most, 1)));
         if (a.tiles == 1)
             hipLaunchKernelGGL((dga::attend_few_kernel<D, 1>), grid, threads, 0, stream, p);
         else
             hipLaunchKernelGGL((dga::attend_few_kernel<D, 2>), grid, threads, 0, stream, p);
-        int st = launched();
-        if (st != DG_OK)
+        if ((st = launched()) != DG_OK)
             return st;
-        if (most > 1) {
-            hipLaunchKernelGGL((dga::join_few_kernel<D>), dim3((unsigned)(p.B * p.heads), (unsigned)a.part_rows), threads,
-                               0, stream, p);
-            if ((st = launched()) != DG_OK)
-                return st;
-        }
+        if (most > 1)
+            joined = p.few_joined = (int)(p.B * p.heads * a.part_rows);
     }
     if (a.tile_rows) {
         p.most_pieces = (int)a.most_pieces;
-        p.part_rows = (int)a.many_rows;
-        p.part_ml = p.part_o + a.most_pieces * a.many_rows * D;
+        p.many = dga::Parts{(int)a.many_rows, parts, parts + a.most_pieces * a.many_rows * D};
         hipLaunchKernelGGL((dga::attend_many_kernel<D>), dim3((unsigned)std::max(a.many_tiles, a.most_pieces)),
                            dim3(dga::kManyThreads), 0, stream, p);
-        int st = launched();
-        if (st != DG_OK)
+        if ((st = launched()) != DG_OK)
             return st;
-        if (a.most_pieces) {
-            hipLaunchKernelGGL((dga::join_many_kernel<D>),
-                               dim3((unsigned)std::min(a.many_tiles, a.most_pieces / 2),
-                                    (unsigned)((a.many_rows + dga::kJoinRows - 1) / dga::kJoinRows)),
-                               threads, 0, stream, p);
-            return launched();
-        }
+        joined += std::min<int64_t>(dga::kJoinGroups, std::min(a.many_tiles, a.most_pieces / 2) *
+                                                          ((a.many_rows + dga::kJoinRows - 1) / dga::kJoinRows));
+    }
+    if (joined) {
+        hipLaunchKernelGGL((dga::join_kernel<D>), dim3((unsigned)joined), threads, 0, stream, p);
+        return launched();
     }
     return DG_OK;
 }
@@ -474,7 +469,7 @@ dg_status dg_fp8_paged_attention(const void *Q, int64_t q_stride_t, int64_t q_st
     p.window = window > kMaxContext ? 0 : (int)window;
     p.group = dgc::divisor((uint32_t)(q_heads / heads));
     p.scale_log2 = scale * 1.44269504088896340736f;
-    p.part_o = (float *)workspace;
+    p.few.o = (float *)workspace;
     const hipStream_t s = (hipStream_t)stream;
     return (dg_status)(D == 64 ? launch_attend<64>(p, a, units, s) : launch_attend<128>(p, a, units, s));
 }
