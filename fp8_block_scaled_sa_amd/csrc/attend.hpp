@@ -920,7 +920,7 @@ struct ManyLds {
     __align__(16) float kscales[2][kTileKeys];
     struct {
         uint32_t present[2];             // bits of the keys that are there
-        int references[2];               // exponent of V's reference
+        int references[2];               // exponent of V's reference, doubled, and 1 where `bad` has bits
         uint32_t bad[2];                 // bits of keys whose values are not finite, where some row does not see every key
         uint32_t unused[2];
     } __align__(16) about[2];
@@ -1084,7 +1084,7 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
         const float found = there >> (lane & 31) & 1 ? raw.scale : 0.0f, size = fabsf(found);
         const bool finite = size < __builtin_inff();
         // The other V wave's reference as of the tile before, or the two would differ for good.
-        reference = max(reference, t ? __builtin_amdgcn_readfirstlane(lds.about[(t + 1) & 1].references[1 - part]) : kNoScale);
+        reference = max(reference, t ? __builtin_amdgcn_readfirstlane(lds.about[(t + 1) & 1].references[1 - part]) >> 1 : kNoScale);
         if (__ballot(finite && size > power_of_2(reference))) {
             float most = finite ? size : 0.0f;
 #pragma unroll
@@ -1119,7 +1119,7 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
             lds.vscales[part][lane] = (_Float16)(factor == 0.0f ? 0.0f : found * factor);
         if (lane == 0) {
             lds.about[t & 1].bad[part] = bad;
-            lds.about[t & 1].references[part] = reference;
+            lds.about[t & 1].references[part] = 2 * reference + (bad != 0);
         }
         wave_sync();
         // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers. Element (D / 16) col + i
@@ -1267,7 +1267,8 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                     x[b][4 * i + c] = __builtin_fmaf(x[b][4 * i + c], ks[c], -ref);
             }
             const uint32_t there = (uint32_t)__builtin_amdgcn_readfirstlane((int)about[b]);
-            if (masked(first + 32 * b, there, wave_first, wave_last, p.window)) {
+            const int e2 = __builtin_amdgcn_readfirstlane((int)about[2 + b]), e = e2 >> 1;
+            if (masked(first + 32 * b, there, wave_first, wave_last, p.window) || (e2 & 1)) {
                 // A row that sees a key whose values are not finite (they are zeros now) becomes NaN. From this lane's
                 // first key on, keys [from, to] are seen, where they are there.
                 const uint32_t mine = there >> (4 * hf), bad = lds.about[t & 1].bad[b] >> (4 * hf);
@@ -1300,7 +1301,6 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                 part = parts[0] + parts[1];
             };
             weigh();
-            const int e = __builtin_amdgcn_readfirstlane((int)about[2 + b]);
             if (__ballot(part > limit) || e != exponent) {
                 // The sums shrink to a larger reference of V; for a smaller one (two waves bring in V, with a reference
                 // each) the weights do.

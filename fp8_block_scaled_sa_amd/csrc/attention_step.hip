@@ -419,11 +419,11 @@ dg_status dg_fp8_paged_attention(const void *Q, int64_t q_stride_t, int64_t q_st
         return (dg_status)st;
     if (table_width > kMaxContext / kc.page_size)
         return DG_ERR_UNSUPPORTED;
+    if (T == 0 || B == 0)
+        return DG_OK;
     const int64_t units = (table_width * kc.page_size + dga::kUnit - 1 + 31) / dga::kUnit;
     if (B * heads * (units + 1) > kInt32Max)
         return DG_ERR_UNSUPPORTED;
-    if (T == 0 || B == 0)
-        return DG_OK;
     if (!Q || !out || !kv_lens || !q_starts || (!block_table && table_width))
         return DG_ERR_NULL_POINTER;
     if ((st = check_cache(kc, false)) != DG_OK || (st = check_cache(vc, false)) != DG_OK ||

@@ -21,6 +21,9 @@ NO_DEVICE_TESTS = {
     "test_moe_step_abi.py::test_norm_accepted_and_empty",
     "test_moe_step_abi.py::test_gate_accepted_and_empty",
     "test_moe_step_abi.py::test_layer_accepted_and_empty",
+    "test_attention_step_abi.py::test_write_accepted_and_empty",
+    "test_attention_step_abi.py::test_read_accepted_and_empty",
+    "test_attention_step_abi.py::test_attention_accepted_and_empty",
 }
 
 

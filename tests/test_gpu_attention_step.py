@@ -12,9 +12,10 @@ Tolerances. A value rounded once is off by half a step of its type (torch.finfo(
              keys adds n 2^-24, numerator and denominator each. fp16 takes the weights, by 2^-11 off, in the numerator
              or (many rows) in both, which counts twice; there it also takes sV and sV V, 2^-11 each: 2^-9 in all. With
              A = sum p |v| / sum p an output is within (2^-9 + 4 e + 2^-19 + n 2^-23) A of the formula's before its
-             rounding to bf16. What fp16 rounds more coarsely, weights below 2^-21 of a row's largest and values whose
-             scale is below 2^-20 of the largest, is off by 2^-31 and 2^-35 of the largest at worst: n 2^-30 448 max
-             |sV|, far below 2^-9 A in these tests.
+             rounding to bf16. fp16's numbers below 2^-14 are off by up to 2^-25 instead. Of the weights: the largest of
+             a row is 2^7 or more, so this is 2^-32 of it, for n keys of values up to 448 M, M the largest |sV| (few
+             rows: the weight times sV / M', M' < 2 M a power of two, twice that). Of sV V (many rows) in units of
+             M' / 2^6: 2^-31 M'. Together below n 2^-31 448 M = n 2^-31 max |v|, which counts where scales lie apart.
 """
 import math
 
@@ -343,6 +344,7 @@ class Batch:
                 worst = torch.where(seen, e, 0.0).amax(1, keepdim=True) if n else torch.zeros_like(total)
                 out[rows, h] = o
                 tol[rows, h] = half(BF16) * o.abs() + (2.0 ** -9 + 4 * worst + 2.0 ** -19 + n * 2.0 ** -23) * a
+                tol[rows, h] += n * 2.0 ** -31 * vh.abs().amax() if n else 0.0
         return out, tol
 
     def check(self, got, **kw):
@@ -404,3 +406,242 @@ def test_attention_window(gpu_device, lengths, heads, kv_heads, D, page, window)
             s[b.table[i, :gone].long()] = math.nan
         b.table[i, :gone] = -1
     b.check(b.call(window=window), window=window)
+
+
+# ---------------------------------------------------------------- attention where it can go wrong
+
+EDGES = [  # (new tokens, tokens): none, more new tokens than tokens, none new
+    [(1, 0), (1, 1), (1, 2)], [(5, 3), (4, 0), (0, 7), (2, 2)], [(0, 0), (0, 5)],
+    [(300, 40), (70, 0), (0, 100), (257, 300)], [(70, 70), (1, 0), (40, 1)]]
+
+
+@pytest.mark.parametrize("lengths", EDGES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_rows_that_see_nothing_are_zero(gpu_device, lengths, D):
+    b = Batch(lengths, 8, 2, D, 16, 7, gap=1)
+    got = b.call()
+    b.check(got)
+    for i, (m, n) in enumerate(lengths):
+        rows = got[b.starts[i]:b.starts[i] + max(0, m - n)]
+        assert bool((rows == 0).all())
+
+
+def spoil(b, seed, bad_codes=True):
+    """Whatever no row sees holds NaN codes and scales: spare pages, and the places behind each sequence's end."""
+    pages, page = b.k[0].shape[:2]
+    used = torch.zeros((pages, page), dtype=torch.bool, device="cuda")
+    for i, (_, n) in enumerate(b.lengths):
+        j = torch.arange(min(n, b.width * page), device="cuda")
+        held = b.table[i].long()[j // page]
+        there = (held >= 0) & (held < pages)
+        used[held[there], (j % page)[there]] = True
+    for c, s in (b.k, b.v):
+        if bad_codes:
+            c[~used] = 0x7F
+        s[~used] = torch.tensor([math.nan, math.inf, -math.inf], device="cuda")[seed % 3]
+
+
+MIXES = [([(1, 700), (1, 33), (1, 128)], 8, 2, 128, 16), ([(4, 300), (2, 65)], 8, 1, 64, 48),
+         ([(90, 90), (1, 200), (130, 1000)], 8, 2, 128, 33), ([(200, 333)], 4, 1, 64, 7), ([(40, 300), (33, 64)] * 3, 8, 4, 128, 16)]
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+@pytest.mark.parametrize("seed", [0, 1, 2])
+def test_attention_of_what_is_not_seen(gpu_device, lengths, heads, kv_heads, D, page, seed):
+    """NaN and infinities behind the sequences' ends and in other pages; pages missing in the middle, by any number."""
+    b = Batch(lengths, heads, kv_heads, D, page, 8 + seed)
+    for i, (_, n) in enumerate(lengths):
+        need = -(-n // page)
+        gone = torch.arange(need, device="cuda")[seed::3]
+        pages = b.k[0].shape[0]
+        b.table[i, gone] = torch.tensor([-1, pages, 2 ** 31 - 1, -2 ** 31, -7, pages + 1], device="cuda",
+                                        dtype=torch.int32).repeat(need)[:len(gone)]
+    spoil(b, seed)
+    b.check(b.call())
+    b.check(b.call(window=50), window=50)
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_attention_with_values_not_finite_in_the_future(gpu_device, lengths, heads, kv_heads, D, page):
+    """The last key's value row and scale: the rows before it do not count it, the last row becomes NaN."""
+    b = Batch(lengths, heads, kv_heads, D, page, 9)
+    clean, tol = b.call(), b.reference()[1]
+    for what in range(3):
+        for i, (m, n) in enumerate(lengths):
+            at = int(b.table[i, (n - 1) // page]), (n - 1) % page
+            if what == 0:
+                b.v[0][at] = 0x7F
+            elif what == 1:
+                b.v[0][at] = 0
+                b.v[1][at] = math.nan
+            else:
+                b.v[1][at] = math.inf
+        got = b.call()
+        for i, (m, n) in enumerate(lengths):
+            rows, last = slice(b.starts[i], b.starts[i] + m - 1), b.starts[i] + m - 1
+            assert bool(torch.isfinite(got[rows]).all())
+            off = (got[rows].double() - clean[rows].double()).abs()
+            assert bool((off <= 2 * tol[rows]).all())
+            if what < 2:
+                assert bool(got[last].isnan().all())
+            else:
+                assert not bool(torch.isfinite(got[last]).all())
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_attention_with_a_key_not_finite(gpu_device, lengths, heads, kv_heads, D, page):
+    """A NaN in the first key that all rows see makes every row NaN, and no row of another sequence."""
+    b = Batch(lengths, heads, kv_heads, D, page, 10)
+    clean = b.call()
+    b.k[0][int(b.table[0, 0]), 0, :, 5] = 0xFF
+    got = b.call()
+    m = lengths[0][0]
+    assert bool(got[:m].isnan().all())
+    assert torch.equal(got[m:], clean[m:])
+
+
+# Scales of keys and values: equal, one of a few very large ones, tiny, of both signs, zero rows among them.
+SCALES = ["one", "large", "tiny", "spread", "falling", "rising", "negative", "zeros"]
+
+
+@pytest.mark.parametrize("kind", SCALES)
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", [
+    ([(1, 20), (1, 1), (1, 600)], 8, 2, 128, 16), ([(40, 40), (33, 33), (70, 75)], 1, 1, 64, 16),
+    ([(100, 128)], 4, 1, 128, 64), ([(40, 700), (64, 96)], 8, 2, 128, 16), ([(300, 2000)], 4, 1, 64, 48)])
+def test_attention_over_scales(gpu_device, lengths, heads, kv_heads, D, page, kind):
+    """V's scales from 2^-100 to 2^100, and up to 2^18 apart within a sequence."""
+    b = Batch(lengths, heads, kv_heads, D, page, 11)
+    s = b.v[1]
+    shape = s.shape
+    order = torch.zeros(shape[:2], dtype=F64, device="cuda")     # of a slot in its sequence
+    for i, (_, n) in enumerate(lengths):
+        j = torch.arange(n, device="cuda")
+        order[b.table[i].long()[j // page], j % page] = j.double() / max(n, 1)
+    order = order[..., None].expand(shape)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    u = torch.rand(shape, generator=g, device="cuda", dtype=F64)
+    new = {"one": torch.ones_like(u), "large": 2.0 ** 100 * (1 + u), "tiny": 2.0 ** -100 * (1 + u),
+           "spread": 2.0 ** (18 * u - 9), "falling": 2.0 ** (9 - 18 * order), "rising": 2.0 ** (18 * order - 9),
+           "negative": torch.where(u < 0.5, -1.0, 1.0) * (1 + u), "zeros": torch.ones_like(u)}[kind]
+    b.v = (b.v[0], new.float())
+    if kind == "zeros":
+        b.v[0][u < 0.3] = 0
+    got = b.call()
+    assert bool(torch.isfinite(got[b.starts[0]:b.starts[-1]]).all())
+    b.check(got)
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.07, 1.0, 1e-30, 3.0])
+def test_attention_scale(gpu_device, scale):
+    b = Batch([(1, 300), (70, 130), (3, 3)], 4, 1, 64, 16, 12)
+    b.q /= 8                             # weights that are not all on one key at the largest scale
+    b.check(b.call(scale=scale), scale=scale)
+
+
+def test_attention_of_large_scores(gpu_device):
+    """Scores beyond the range of exp, of both signs, rising and falling along the keys."""
+    for lengths in ([(1, 3000)], [(64, 64), (300, 2000)]):
+        b = Batch(lengths, 8, 2, 128, 16, 13)
+        order = torch.zeros(b.k[1].shape[:2], device="cuda")
+        for i, (_, n) in enumerate(lengths):
+            j = torch.arange(n, device="cuda")
+            order[b.table[i].long()[j // 16], j % 16] = j.float()
+        for sign in (1.0, -1.0):
+            ks = b.k[1].clone()
+            b.k[0][...] = torch.tensor([2.0], device="cuda").to(F8).view(torch.uint8)[0]
+            b.q[...] = 1.0
+            b.q[1::2] = -1.0
+            b.k = (b.k[0], (sign * order / 8)[..., None].expand(ks.shape).contiguous())
+            b.check(b.call())
+
+
+def test_attention_strides_and_what_lies_between(gpu_device):
+    """Q and out within wider tensors, heads before tokens too; rows of no sequence and of too long ones as they were."""
+    for lengths, longest in (([(1, 200), (1, 33)], 1), ([(3, 90), (9, 40), (1, 5)], 4), ([(70, 300), (130, 130), (1, 9)], 100)):
+        b = Batch(lengths, 8, 2, 128, 16, 14, gap=3)
+        T = b.q.shape[0]
+        want = b.call(out=torch.zeros_like(b.q))
+        wide = torch.full((T, 11, 136), 0.5, dtype=BF16, device="cuda")
+        wide[:, 2:10, :128] = b.q
+        b.q = wide[:, 2:10, :128]
+        for layout in ("tokens", "heads"):
+            buf = sentinel_bf16((T, 10, 144) if layout == "tokens" else (10, T, 144))
+            out = (buf if layout == "tokens" else buf.transpose(0, 1))[:, 1:9, 8:136]
+            image = buf.clone()
+            assert b.call(out=out, longest=longest) is out
+            for i, (m, _) in enumerate(lengths):
+                rows = slice(b.starts[i], b.starts[i] + m)
+                if m <= longest:
+                    assert torch.equal(out[rows], want[rows])
+                    out[rows] = (image if layout == "tokens" else image.transpose(0, 1))[rows, 1:9, 8:136]
+            assert same(buf, image)
+
+
+def test_attention_cache_strides(gpu_device):
+    """Keys and values as halves of each page, heads before tokens: the same results, bit for bit."""
+    for lengths in ([(1, 500), (1, 3)], [(90, 200), (1, 70)]):
+        b = Batch(lengths, 8, 2, 64, 16, 15)
+        want = b.call()
+        for dims in ((0, 1, 2, 3, 4), (0, 1, 3, 2, 4), (1, 0, 2, 3, 4), (3, 0, 1, 2, 4)):
+            both, s = torch.stack([b.k[0], b.v[0]], 1), torch.stack([b.k[1], b.v[1]], 1)
+            inverse = [dims.index(i) for i in range(5)]
+            both = both.permute(dims).contiguous().permute(inverse)
+            s = s.permute(dims[:4]).contiguous().permute(inverse[:4])
+            k, v = (both[:, 0], s[:, 0]), (both[:, 1], s[:, 1])
+            got = ops.dg_fp8_paged_attention(b.q, *k, *v, b.table, b.kv_lens, b.q_starts, b.longest, b.ws)
+            assert torch.equal(got, want)
+
+
+def test_attention_table_narrower_than_the_sequences_and_wider(gpu_device):
+    for width in (1, 3, 200):
+        b = Batch([(1, 100), (2, 31)], 4, 2, 64, 16, 16)
+        wide = torch.full((2, max(width, b.width) + 5), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+        wide[:, :b.width] = b.table
+        b.table, b.width = wide[:, :width], width
+        got = b.call()
+        # the sequences end where the table does
+        b.lengths = [(m, min(n, width * 16)) for m, n in b.lengths]
+        b.check(got)
+
+
+def test_attention_lengths_out_of_range_do_no_harm(gpu_device):
+    """Whatever the lengths and starts hold: no fault, nothing beside out and workspace written."""
+    for lengths in ([(1, 100), (1, 40), (1, 7)], [(70, 100), (1, 40), (90, 90)]):
+        b = Batch(lengths, 8, 2, 128, 16, 17)
+        T = b.q.shape[0]
+        for lens in ([2 ** 31 - 1] * 3, [-1, -2 ** 31, 5], [1 << 20, 0, 33]):
+            for starts in (b.starts, [0, 2 ** 31 - 1, -5, T], [-2 ** 31, 0, T, T + 1], [T, 0, T, 0], [T + 7, T + 8, T + 9, T + 10]):
+                b.kv_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+                b.q_starts = torch.tensor(starts, dtype=torch.int32, device="cuda")
+                buf = sentinel_bf16((T + 4, 8, 128))
+                image = buf.clone()
+                b.call(out=buf[2:T + 2])
+                torch.cuda.synchronize()
+                assert same(buf[:2], image[:2]) and same(buf[T + 2:], image[T + 2:])
+
+
+def test_attention_behind_32_bits(gpu_device):
+    """Pages further than 2^32 bytes into a cache that is keys and values at once; the write and the read there too."""
+    page, heads, D = 16, 1, 128
+    pages = (2 ** 32 + 2 ** 25) // (page * heads * D)
+    codes = torch.zeros((pages, page, heads, D), dtype=torch.uint8, device="cuda")
+    s = torch.ones((pages, page, heads), device="cuda")
+    for lengths in ([(1, 300)], [(70, 300)]):
+        b = Batch(lengths, 4, 1, D, page, 18)
+        b.v = b.k
+        want = b.call()
+        first = pages - b.k[0].shape[0]
+        codes[first:], s[first:] = b.k
+        b.k = b.v = codes, s
+        b.table = torch.where(b.table >= 0, b.table + first, b.table)
+        assert torch.equal(b.call(), want)
+    x = normal((3, heads, D), 1)
+    slots = torch.tensor([pages * page - 1, 2 ** 32 // D, 0], device="cuda")
+    other, s2 = torch.zeros_like(codes), torch.ones_like(s)
+    ops.dg_fp8_rope_cache_write(x, x, codes, s, other, s2, slots)
+    want = quantized(x.cpu())
+    at = slots // page, slots % page
+    assert torch.equal(codes[at].cpu(), want[0]) and torch.equal(s[at].cpu(), want[1])
+    assert torch.equal(other[at].cpu(), want[0]) and torch.equal(s2[at].cpu(), want[1])
+    got = ops.dg_fp8_cache_read(codes, s, slots, dtype=F32)
+    assert torch.equal(got.cpu(), want[0].view(F8).float() * want[1][..., None])
