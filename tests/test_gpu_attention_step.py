@@ -24,6 +24,7 @@ import torch
 
 from fp8_block_scaled_sa_amd import ops
 from tests.gpu_util import guards_intact, sentinel_bf16
+from tests.test_gpu_debug_build import both, debug_lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -645,3 +646,222 @@ def test_attention_behind_32_bits(gpu_device):
     assert torch.equal(other[at].cpu(), want[0]) and torch.equal(s2[at].cpu(), want[1])
     got = ops.dg_fp8_cache_read(codes, s, slots, dtype=F32)
     assert torch.equal(got.cpu(), want[0].view(F8).float() * want[1][..., None])
+
+
+# ---------------------------------------------------------------- a step's calls together
+
+def example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_decode_step.py")
+    spec = importlib.util.spec_from_file_location("moe_decode_step", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+@pytest.mark.parametrize("heads,kv_heads,page", [(4, 2, 16), (8, 1, 7), (16, 4, 64)])
+def test_example_attention_steps(gpu_device, heads, kv_heads, page):
+    """Prompts in chunks, then token by token, of sequences that join and leave: each step's attention against 64 bits
+    over what the cache holds then, the output product against 64 bits from the same codes."""
+    ex = example()
+    block = ex.AttentionBlock(hidden=384, heads=heads, kv_heads=kv_heads, pages=100, page_size=page, max_tokens=300,
+                              max_batch=3)
+    table = torch.randperm(99, device="cuda").int().view(3, 33)
+    most = 33 * page
+    at = [0, 0, 0]
+    for i, new in enumerate(([100, 3, 1], [120, 0, 1], [1, 1, 1], [1, 60, 1], [1, 1, 40], [1, 1, 1])):
+        new = [min(m, most - n) for m, n in zip(new, at)]
+        at = [n + m for n, m in zip(at, new)]
+        batch = ex.batch_of(table, page, new, at)
+        x, residual = normal((sum(new), 384), 20 + i).to(BF16), normal((sum(new), 384), 40 + i).to(BF16)
+        total = (x.float() + residual.float()).to(BF16)
+        copy = residual.clone()
+        o, q = block.attend(x, residual, **batch)
+        assert torch.equal(residual, total)
+        exact, size = block.reference(q, table, batch["kv_lens"], batch["q_starts"])
+        # scores below 64 in magnitude here, exact to 2^-24 132 64: 2^-11, and 2^-9 as above
+        assert bool(((o.double() - exact).abs() <= half(BF16) * exact.abs() + (2.0 ** -9 + 2.0 ** -10) * size).all())
+        out = block.step(x, copy, **batch)
+        codes, s = ops.dg_fp8_quantize_1x128(o.flatten(1))
+        want = (codes.view(F8).double() * s.double().repeat_interleave(128, 1)) @ ex.value(block.w_out, block.s_out).t()
+        assert float((out.double() - want).norm()) <= half(BF16) * float(want.norm())
+
+
+def test_step_of_padded_tokens(gpu_device):
+    """A batch padded to a fixed number of tokens and sequences (slots -1, no new tokens) gives the rows of the same
+    batch without padding, and leaves the cache as that does."""
+    T, Hq, H, D, page = 5, 8, 2, 128, 16
+    freqs, _ = ops.dg_rope_frequencies(D)
+    qkv = normal((64, Hq + 2 * H, D), 1).to(BF16)
+    results = []
+    for pad in (0, 59):
+        b = Batch([(1, 40), (3, 70), (1, 1)], Hq, H, D, page, 2)
+        n = T + pad
+        q, k, v = qkv[:n].clone().split([Hq, H, H], 1)
+        positions = torch.zeros(n, dtype=torch.int32, device="cuda")
+        positions[:T] = torch.tensor([39, 67, 68, 69, 0])
+        slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+        seq = torch.tensor([0, 1, 1, 1, 2], device="cuda")
+        slots[:T] = b.table[seq, positions[:T].long() // page].long() * page + positions[:T].long() % page
+        lens, starts = b.kv_lens, b.q_starts
+        table = b.table
+        if pad:
+            lens = torch.cat([lens, torch.zeros(6, dtype=torch.int32, device="cuda")])
+            starts = torch.cat([starts, torch.full((6,), T, dtype=torch.int32, device="cuda")])
+            table = torch.cat([table, torch.full((6, table.shape[1]), -1, dtype=torch.int32, device="cuda")])
+        q = ops.dg_fp8_rope_cache_write(k, v, *b.k, *b.v, slots, positions, freqs, q=q)
+        ws = ops.workspace(ops.dg_fp8_paged_attention_workspace_bytes(n, len(lens), Hq, H, D, 3))
+        out = ops.dg_fp8_paged_attention(q, *b.k, *b.v, table, lens, starts, 3, ws, out=torch.full_like(q, 0.25))
+        assert bool((out[T:] == 0.25).all())
+        b.q = q[:T]
+        b.check(out[:T])
+        results.append([out[:T], *b.k, *b.v])
+    assert all(same(x, y) for x, y in zip(*(r[1:] for r in results)))
+
+
+# ---------------------------------------------------------------- streams, graphs, builds
+
+KINDS = {  # lengths of calls through each kernel, and of the two together
+    "singles": ([(1, 700), (1, 3), (1, 1500)], 8, 2, 128), "few": ([(3, 300), (4, 900)], 8, 1, 64),
+    "cut": ([(40, 2000)], 8, 2, 128), "cut batch": ([(33, 900)] * 5, 4, 2, 64), "chunks": ([(300, 700), (90, 90)], 8, 2, 128),
+    "mixed": ([(1, 400)] * 4 + [(150, 600)], 8, 2, 128)}
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_on_a_stream(gpu_device, kind):
+    """`stream=`, and a side stream as the current one; the caller orders the streams."""
+    b = Batch(*KINDS[kind], 16, 21)
+    want = b.call()
+    main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    for _ in range(3):
+        b.ws.fill_(0xFF)
+        b.q = b.q.clone()
+        side.wait_stream(main)
+        got = b.call(stream=side)
+        main.wait_stream(side)
+        assert torch.equal(got, want)
+        with torch.cuda.stream(side):
+            again = b.call()
+        side.synchronize()
+        assert torch.equal(again, want)
+
+
+def test_write_and_read_on_a_stream(gpu_device):
+    T, H, D = 100, 2, 128
+    side = torch.cuda.Stream()
+    slots = torch.randperm(128, device="cuda")[:T]
+    freqs, _ = ops.dg_rope_frequencies(D)
+    results = []
+    for kw in ({}, dict(stream=side)):
+        x = normal((T, H, D), 3)
+        c = [*make_cache(8, 16, H, D, 1), *make_cache(8, 16, H, D, 2)]
+        positions = slots.int()
+        side.wait_stream(torch.cuda.current_stream())
+        q = ops.dg_fp8_rope_cache_write(x, x, *c, slots, positions, freqs, q=x, **kw)
+        results.append([q, *c, ops.dg_fp8_cache_read(c[0], c[1], slots, **kw)])
+        torch.cuda.current_stream().wait_stream(side)
+    assert all(same(a, b) for a, b in zip(*results))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_in_a_graph(gpu_device, kind):
+    """A captured step (write, attention, read), replayed with other lengths, pages and contents, and a second graph
+    that shares its workspace, with eager work between."""
+    lengths, heads, kv_heads, D = KINDS[kind]
+    b = Batch(lengths, heads, kv_heads, D, 16, 22)
+    T, page = b.q.shape[0], 16
+    freqs, _ = ops.dg_rope_frequencies(D)
+    kv = normal((2, T, kv_heads, D), 5)
+    slots = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    positions = torch.zeros(T, dtype=torch.int32, device="cuda")
+    outs = [torch.zeros_like(b.q), torch.zeros_like(b.q)]
+    turned = torch.zeros_like(b.q)
+    rows = torch.zeros((T, kv_heads, D), dtype=F32, device="cuda")
+
+    def step(out, window):
+        q = b.q
+        ops.dg_fp8_rope_cache_write(kv[0].to(BF16), kv[1].to(BF16), *b.k, *b.v, slots, positions, freqs, q=q, q_out=turned)
+        ops.dg_fp8_paged_attention(turned, *b.k, *b.v, b.table, b.kv_lens, b.q_starts, b.longest, b.ws, out=out,
+                                   window=window)
+        ops.dg_fp8_cache_read(*b.k, slots, out=rows)
+
+    step(outs[0], 0)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for i, window in enumerate((0, 77)):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step(outs[i], window)
+        graphs.append(graph)
+    torch.cuda.synchronize()
+    g = torch.Generator(device="cuda").manual_seed(9)
+    for turn in range(4):
+        # shorter sequences, other pages, other rows
+        lens = [max(m, (n * (4 - turn)) // 4) for m, n in lengths]
+        b.kv_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+        b.table.copy_(b.table.roll(1, 0) if turn % 2 else b.table)
+        b.q.copy_(torch.randn(b.q.shape, generator=g, device="cuda"))
+        kv.copy_(torch.randn(kv.shape, generator=g, device="cuda"))
+        for i, (m, _) in enumerate(lengths):
+            at = torch.arange(lens[i] - m, lens[i], device="cuda")
+            held = b.table[i].long()[at // page]
+            slots[b.starts[i]:b.starts[i + 1]] = torch.where(held >= 0, held * page + at % page, -1)
+            positions[b.starts[i]:b.starts[i + 1]] = at.int()
+        for i, window in enumerate((0, 77)):
+            for out in outs:
+                out.zero_()
+            b.ws.fill_(0xFF)
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            got, got_rows = outs[i].clone(), rows.clone()
+            outs[i].zero_()
+            rows.zero_()
+            step(outs[i], window)
+            torch.cuda.synchronize()
+            assert torch.equal(got, outs[i]) and torch.equal(got_rows, rows), "replay %d of graph %d" % (turn, i)
+            assert bool(got.any())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_attention_release_equals_O1(gpu_device, debug_lib, kind):  # noqa: F811
+    """And a hundred repeats, from a workspace of NaN bytes each."""
+    b = Batch(*KINDS[kind], 16, 23)
+    out = sentinel_bf16(b.q.shape)
+
+    def run():
+        b.ws.fill_(0xFF)
+        b.call(out=out)
+        torch.cuda.synchronize()
+        assert guards_intact(out)
+        return out.clone()
+    rel, dbg = both(debug_lib, run)
+    assert torch.equal(rel, dbg), "-O1 build differs from the release build"
+    for r in range(100):
+        assert torch.equal(run(), rel), "repeat %d differs" % r
+
+
+@pytest.mark.parametrize("T,D,dtype", [(1, 128, BF16), (61, 64, F32), (700, 128, BF16)])
+def test_write_and_read_release_equal_O1(gpu_device, debug_lib, T, D, dtype):  # noqa: F811
+    Hq, H = 8, 2
+    x = normal((T, Hq + 2 * H, D), 1).to(dtype)
+    q, k, v = x.split([Hq, H, H], 1)
+    slots = torch.randperm(1024, device="cuda")[:T]
+    positions = (7919 * slots).int()
+    freqs, _ = ops.dg_rope_frequencies(D)
+
+    def run():
+        c = [*make_cache(64, 16, H, D, 1), *make_cache(64, 16, H, D, 2)]
+        out = ops.dg_fp8_rope_cache_write(k, v, *c, slots, positions, freqs, q=q)
+        back = ops.dg_fp8_cache_read(c[2], c[3], slots, dtype=dtype)
+        torch.cuda.synchronize()
+        return [out, *c, back]
+    rel, dbg = both(debug_lib, run)
+    # (The library's sine and cosine may be compiled to other instructions: an fp32 step before the rounding.)
+    for a, b in zip(rel[3:], dbg[3:]):
+        assert same(a, b)
+    for _ in range(20):
+        assert all(same(a, b) for a, b in zip(run(), rel))
+    ref, size = rotated(q, positions, freqs, 1.0, False)
+    assert bool(((dbg[0].double() - ref).abs() <= half(BF16) * ref.abs() + 2.0 ** -19 * size).all())
