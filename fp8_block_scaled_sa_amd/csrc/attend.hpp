@@ -50,7 +50,7 @@ constexpr int kThreads = 256;
 constexpr int kUnit = 128;               // keys that a workgroup of the few-rows kernel takes at once
 constexpr int kFewRows = 32;             // most rows (tokens x heads of a group) of its sequences
 constexpr int kTileRows = 256;           // rows of a workgroup of the many-rows kernel
-constexpr int kJoinRows = 16;            // of a cut tile, that a workgroup joins at a time
+constexpr int kJoinRows = 4;             // of a cut tile, that a workgroup joins at a time
 constexpr int kJoinGroups = 1024;        // workgroups that do
 constexpr int kTileKeys = 64;            // keys that a workgroup of the many-rows kernel takes at once
 constexpr float kNoMax = -1e30f;         // reference of a row that has seen nothing; finite, so that differences are
@@ -93,7 +93,8 @@ struct AttendParams {
     int target, min_units;               // few rows: workgroups aimed at, and units that one takes at least
     int most_pieces;                     // many rows: workgroups up to which tiles may be cut (0: not at all)
     Parts few, many;                     // partial results of the two kernels
-    int few_joined;                      // workgroups of the joining launch that join the first kernel's
+    int few_joined;                      // workgroups of the joining launch that join the first kernel's,
+    int row_a_wave;                      // and whether each of their waves joins a row
 };
 
 // A sequence as the device arrays give it; anything out of range counts as nothing.
@@ -678,56 +679,62 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
     }
 }
 
-// Joins `count` partial results of a row, the i-th at index(i), and writes it:
-// the four waves of a workgroup take every fourth one each.
+// Joins this wave's share (every `waves`-th from `first` on) of `count` partial results of a row, the i-th at index(i).
 template <int D, typename Index>
-__device__ __forceinline__ void join(const AttendParams &p, int count, Index index, uint16_t *to)
+__device__ __forceinline__ void join_pieces(const Parts &parts, int count, int first, int waves, Index index, float &total,
+                                            float (&y)[D / 64])
 {
     constexpr int E = D / 64;
-    __shared__ float part[4][D + 1];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63;
     float top = kNoMax;
     for (int i = lane; i < count; i += 64)
-        top = fmaxf(top, p.few.ml[2 * index(i)]);
+        top = fmaxf(top, parts.ml[2 * index(i)]);
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         top = fmaxf(top, __shfl_xor(top, d, 64));
-    float total = 0.0f, y[E] = {};
-#pragma unroll 4
-    for (int i = wave; i < count; i += 4) {
+    total = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        y[e] = 0.0f;
+#pragma unroll 8
+    for (int i = first; i < count; i += waves) {
         const int64_t at = index(i);
-        const f32x2 ml = *(const f32x2 *)(p.few.ml + 2 * at);
+        const f32x2 ml = *(const f32x2 *)(parts.ml + 2 * at);
         const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
         total = __builtin_fmaf(ml[1], weight, total);
-        const float *o = p.few.o + at * D + E * lane;
+        const float *o = parts.o + at * D + E * lane;
 #pragma unroll
         for (int e = 0; e < E; ++e)
             y[e] = __builtin_fmaf(o[e], weight, y[e]);
     }
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        part[wave][E * lane + e] = y[e];
-    if (lane == 0)
-        part[wave][D] = total;
-    __syncthreads();
-    if (threadIdx.x < D / 2) {
-        total = (part[0][D] + part[1][D]) + (part[2][D] + part[3][D]);
-        float v[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int d = 2 * threadIdx.x + e;
-            const float all = (part[0][d] + part[1][d]) + (part[2][d] + part[3][d]);
-            v[e] = total == 0.0f ? 0.0f : all / total;
-        }
-        *(uint32_t *)(to + 2 * threadIdx.x) = dgn::pack_bf16(v[0], v[1]);
-    }
 }
 
-// One row of a sequence that several pieces share; rows of a sequence and head next to each other.
+// A joined row, E elements of it in each lane.
+template <int E>
+__device__ __forceinline__ void store_row(uint16_t *to, float total, const float (&y)[E])
+{
+    float v[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        v[e] = total == 0.0f ? 0.0f : y[e] / total;
+    to += E * (threadIdx.x & 63);
+    if (E == 2)
+        *(uint32_t *)to = dgn::pack_bf16(v[0], v[1]);
+    else
+        *to = (uint16_t)dgn::pack_bf16(v[0], 0.0f);
+}
+
+// One row of a sequence that several pieces share, by a wave; or by the four of a workgroup, for few rows.
 template <int D>
 __device__ __forceinline__ void join_few(const AttendParams &p, int block)
 {
-    const int of = block / p.few.rows, r = block - of * p.few.rows, b = of / p.heads, head = of - b * p.heads;
+    constexpr int E = D / 64;
+    __shared__ float part[4][D + 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = p.row_a_wave ? 4 * block + wave : block;
+    const int of = row / p.few.rows, r = row - of * p.few.rows, b = of / p.heads, head = of - b * p.heads;
+    if (b >= p.B)
+        return;
     Cut c;
     const int chunk = chunk_of(p, c);
     int upto = 0;
@@ -738,8 +745,27 @@ __device__ __forceinline__ void join_few(const AttendParams &p, int block)
     if (pieces < 2 || r >= rows)
         return;
     const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
-    join<D>(p, pieces, [&](int i) { return (int64_t)(before + i * p.heads + head) * p.few.rows + r; },
-            p.out + (int64_t)(start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h);
+    uint16_t *to = p.out + (int64_t)(start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h;
+    const auto index = [&](int i) { return (int64_t)(before + i * p.heads + head) * p.few.rows + r; };
+    float total, y[E];
+    if (p.row_a_wave) {
+        join_pieces<D>(p.few, pieces, 0, 1, index, total, y);
+        store_row(to, total, y);
+        return;
+    }
+    join_pieces<D>(p.few, pieces, wave, 4, index, total, y);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        part[wave][E * lane + e] = y[e];
+    if (lane == 0)
+        part[wave][D] = total;
+    __syncthreads();
+    if (wave)
+        return;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        y[e] = (part[0][E * lane + e] + part[1][E * lane + e]) + (part[2][E * lane + e] + part[3][E * lane + e]);
+    store_row(to, (part[0][D] + part[1][D]) + (part[2][D] + part[3][D]), y);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -766,6 +792,8 @@ __device__ __forceinline__ void lane_tiles(const AttendParams &p, int b, Cuts &c
     c.tiles = c.s.rows > p.few_rows ? (c.s.rows + kTileRows - 1) / kTileRows : 0;
     c.keys = c.tiles ? max(1, (c.s.n - (c.s.low & ~(kTileKeys - 1)) + kTileKeys - 1) / kTileKeys) : 0;
 }
+
+constexpr float kPieceStart = 3.0f, kPieceJoin = 0.15f;    // in units of the time of a tile of keys
 
 // Pieces of a tile of this lane's sequence, of about 1 / rate tiles of keys each.
 __device__ __forceinline__ int pieces_of(const Cuts &c, float rate) { return max(1, (int)((float)c.keys * rate + 0.5f)); }
@@ -798,11 +826,11 @@ __device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
     float best = 0.0f;
     if (p.B == 1) {
         const float tiles = (float)lane_int(pieces, 0) * heads, keys = (float)lane_int(most, 0);
-        float least = keys * __builtin_ceilf(tiles / 256.0f);
+        float least = (keys + kPieceStart) * __builtin_ceilf(tiles / 256.0f);
 #pragma unroll
         for (int rounds = 1; rounds <= 3; ++rounds) {
             const float parts = fminf(__builtin_floorf(256.0f * (float)rounds / tiles), keys);
-            const float time = (float)rounds * keys / parts + 2.0f + cost * tiles * parts;
+            const float time = (float)rounds * (keys / parts + kPieceStart) + 2.0f + kPieceJoin * parts + cost * tiles * parts;
             if (parts >= 2.0f && time < least) {
                 least = time;
                 best = parts / keys;
@@ -1381,7 +1409,7 @@ template <int D>
 __device__ __forceinline__ void join_many(const AttendParams &p, int block, int blocks)
 {
     constexpr int E = D / 64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wave = threadIdx.x >> 6;
     const int shares = (p.many.rows + kJoinRows - 1) / kJoinRows;
     Cuts c;
     const float rate = cut_tiles(p, c);
@@ -1390,30 +1418,11 @@ __device__ __forceinline__ void join_many(const AttendParams &p, int block, int 
         const int from = kJoinRows * (block % shares);
         for (int i = from + wave; i < from + kJoinRows && w.first + i < w.s.rows; i += 4) {
             const auto index = [&](int piece) { return (int64_t)(w.slot + piece * p.heads) * p.many.rows + i; };
-            float top = kNoMax;
-            for (int piece = 0; piece < w.pieces; ++piece)
-                top = fmaxf(top, p.many.ml[2 * index(piece)]);
-            float total = 0.0f, y[E] = {};
-    #pragma unroll 4
-            for (int piece = 0; piece < w.pieces; ++piece) {
-                const int64_t at = index(piece);
-                const f32x2 ml = *(const f32x2 *)(p.many.ml + 2 * at);
-                const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
-                total = __builtin_fmaf(ml[1], weight, total);
-                const float *o = p.many.o + at * D + E * lane;
-    #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    y[e] = __builtin_fmaf(o[e], weight, y[e]);
-            }
             const int r = w.first + i, token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
-            uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(w.head * (int)p.group.d + h) * p.o_h + E * lane;
-    #pragma unroll
-            for (int e = 0; e < E; ++e)
-                y[e] = total == 0.0f ? 0.0f : y[e] / total;
-            if (E == 2)
-                *(uint32_t *)to = dgn::pack_bf16(y[0], y[E - 1]);
-            else
-                *to = (uint16_t)dgn::pack_bf16(y[0], 0.0f);
+            float total, y[E];
+            join_pieces<D>(p.many, w.pieces, 0, 1, index, total, y);
+            store_row(p.out + (int64_t)(w.s.start + token) * p.o_t +
+                          (int64_t)(w.head * (int)p.group.d + h) * p.o_h, total, y);
         }
     }
 }

@@ -176,6 +176,7 @@ struct AttendPlan {
 
 constexpr int kFewTarget = 1024;
 constexpr int kFewMinUnits = 1;
+constexpr int64_t kRowAWave = 2048;
 constexpr int64_t kMostPieces = 768;
 constexpr int64_t kUncutTiles = 4096;
 
@@ -245,8 +246,11 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
             hipLaunchKernelGGL((dga::attend_few_kernel<D, 2>), grid, threads, 0, stream, p);
         if ((st = launched()) != DG_OK)
             return st;
-        if (most > 1)
-            joined = p.few_joined = (int)(p.B * p.heads * a.part_rows);
+        if (most > 1) {
+            joined = p.B * p.heads * a.part_rows;
+            p.row_a_wave = joined >= kRowAWave;
+            p.few_joined = (int)(joined = p.row_a_wave ? (joined + 3) / 4 : joined);
+        }
     }
     if (a.tile_rows) {
         p.most_pieces = (int)a.most_pieces;

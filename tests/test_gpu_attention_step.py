@@ -865,3 +865,11 @@ def test_write_and_read_release_equal_O1(gpu_device, debug_lib, T, D, dtype):  #
         assert all(same(a, b) for a, b in zip(run(), rel))
     ref, size = rotated(q, positions, freqs, 1.0, False)
     assert bool(((dbg[0].double() - ref).abs() <= half(BF16) * ref.abs() + 2.0 ** -19 * size).all())
+
+
+def test_attention_of_many_few_rows(gpu_device):
+    """More rows to join than workgroups that would take one each: a wave a row, whose last ones end in a workgroup."""
+    for lengths, heads, kv_heads, D in (([(4, 400 + 137 * i) for i in range(39)], 16, 8, 128),
+                                        ([(1, 300 + 61 * i) for i in range(67)], 35, 7, 64)):
+        b = Batch(lengths, heads, kv_heads, D, 16, 24)
+        b.check(b.call())
