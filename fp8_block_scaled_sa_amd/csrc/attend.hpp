@@ -10,19 +10,29 @@
 //
 // Roundings. The codes are exact in bf16 and fp16, so the products q . K are
 // exact bf16 products summed in fp32; both scales are applied in fp32. The
-// second product takes fp16: its weights p sV, whose rounding to 11 bits is the
-// only one before the output's (bf16 weights, with 8 bits, would add as much
-// error as the output's own rounding). fp16's range is kept by two references:
-// p is exp2(x - m) with a running m that lies at most 8 below the largest x
-// seen, and sV is divided by a power of two e that is at least the largest sV
-// seen; the weights are scaled by 2^7, so they reach up to 2^15, are rounded to
-// 11 bits down to 2^-29 of that and lost below 2^-40. Sums, references and the
-// outputs before their rounding are fp32.
+// second product takes fp16 (bf16 weights, with 8 bits, would add as much error
+// as the output's own rounding). The few-rows kernel rounds its weights p sV to
+// fp16's 11 bits and multiplies the codes; the many-rows kernel rounds p, sV and
+// sV V, once for all of a tile's rows, and sums the rounded p for the
+// denominator. Sums, references and the outputs before their rounding are fp32.
+// fp16's range is kept by two references. p is exp2(x - m) with a running m
+// whose weight was 2^7 when it was set; m moves when weights pass 2^15 or so,
+// so that rows rarely move their sums. sV is divided by a power of two that is
+// at least the largest |sV| seen. What lies below fp16's normal numbers is off
+// by 2^-25 instead of relatively: p below 2^-21 of a row's largest, sV V where sV
+// is below 2^-20 of the largest that the tile's rows were given.
 //
 // Masked keys never count, whatever their rows hold: their weight is set to 0,
 // and codes of V that are NaN there are replaced (0 * NaN would be NaN). A row
 // that sees a NaN code comes out as NaN: in that column, or in all of them where
 // the code lies in a tile that is masked for some rows.
+//
+// Which kernel. The cache's bytes bound few rows: each key is read once, at
+// 2 D + 8 bytes, and costs 4 D operations a row, so up to some 60 rows the read
+// takes longer. The few-rows kernel takes up to 32 (33 rows of 64 sequences, in
+// a form of it with four tiles of 16: 1087 us, its registers spilled; 397 us
+// here in the other). Both split keys over workgroups by the lengths on the
+// device, and one launch behind them joins what was split.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -217,7 +227,9 @@ __device__ __forceinline__ int units_of(const Sequence &s)
 // sequences fill the CUs evenly: `chunk` units a piece, as many as give
 // p.target pieces in all. Each wave finds its piece by itself from the
 // sequences' lengths (64 at a time, a scan over the lanes), without a planning
-// launch and without the host knowing them.
+// launch and without the host knowing them. Workgroups that follow each other go
+// to the XCDs in turn, so pieces are numbered such that the heads of a page, whose
+// rows lie next to each other, are read by one XCD.
 struct Cut {
     Sequence s;                          // of this lane, of 64
     int units, pieces, before;           // pieces of each of its heads; pieces of the lanes (and sequences) before
@@ -322,6 +334,13 @@ __device__ __forceinline__ void store_bf16(uint16_t *to, const float *v)
 // K's loads cover whole 128-byte lines, 8 lanes a row, and lanes l and l ^ 8
 // then exchange halves. V's pairs of keys are brought together byte by byte
 // (v_perm) before the conversion, which takes two codes at once.
+//
+// Two units are in flight, in registers of their own (one: 260 us for 64
+// sequences of up to 16384 tokens, 8 key heads of 8; two: 226 us, 5.1 TB/s, which
+// is the rate of a large copy). 208 registers for one tile of rows, two waves a
+// SIMD; with two tiles 256 and 14 spilled (16 sequences of 4 tokens up to 8192: 48
+// us, 62% of the copy's rate: a workgroup has four units or so, and the first
+// and the last are not hidden).
 template <int D, int NT>
 __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 {
@@ -796,7 +815,11 @@ __device__ __forceinline__ void lane_tiles(const AttendParams &p, int b, Cuts &c
 constexpr float kPieceStart = 3.0f, kPieceJoin = 0.15f;    // in units of the time of a tile of keys
 
 // Pieces of a tile of this lane's sequence, of about 1 / rate tiles of keys each.
-__device__ __forceinline__ int pieces_of(const Cuts &c, float rate) { return max(1, (int)((float)c.keys * rate + 0.5f)); }
+__device__ __forceinline__ int pieces_of(const Cuts &c, float rate)
+{
+#pragma clang fp contract(off)           // the joining kernel has to come to the same numbers
+    return max(1, (int)((float)c.keys * rate + 0.5f));
+}
 
 // How tiles are cut: the reciprocal of the tiles of keys of a piece, 0 for not at
 // all. Every workgroup comes to the same estimate from the lengths, in units of
@@ -805,9 +828,10 @@ __device__ __forceinline__ int pieces_of(const Cuts &c, float rate) { return max
 // ones, as many rounds as they fill; uneven ones their average and a part of the
 // longest. Cutting costs the joining launch's work (2), and for each piece its
 // partial result's way out and back. (16 sequences of 16 tokens, 8 heads of 8, up
-// to 8192 tokens: 370 us uncut, MEASURED us cut.)
+// to 8192 tokens: 370 us uncut, 197 us cut.)
 __device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
 {
+#pragma clang fp contract(off)
     const int lane = threadIdx.x & 63;
     float total = 0.0f;
     int most = 0, pieces = 0;
@@ -1190,6 +1214,15 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
 // (K to bf16, V times its scale to fp16) and store them to LDS while the other
 // waves compute the tile before; V transposed, its keys in the order in which
 // the first product leaves them. One barrier a tile.
+//
+// Bound by the matrix units and the clock that they leave: 2048 tokens of 64
+// heads over 32768 keys take 2.03 ms, 1065 TFLOP/s of 1155 to 1317 that large
+// bf16 products reach here. The same waves bringing in and computing took 2.39 ms
+// (conversion and exponentials beside each other), sums and queries in fewer
+// registers spilled (6.45 ms). 256 rows share each conversion; 768 threads and
+// 168 registers leave room for one workgroup a CU. A short sequence pays its
+// rows' moves of the reference (an eighth of the time of 2048 tokens by
+// themselves, 90 us) and 5 us before the first tile.
 template <int D>
 __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendParams p)
 {

@@ -174,9 +174,16 @@ struct AttendPlan {
     int64_t most_bytes;    // of the workspace of any call with at most these sizes
 };
 
+// Pieces that the few-rows kernel's work is cut into: four workgroups for each CU, of which two run at a time. (64
+// sequences up to 16384 tokens and 16 of 4 tokens up to 8192: 251 and 55 us with 512, 227 and 56 with 1024, 225 and 64
+// with 2048.)
 constexpr int kFewTarget = 1024;
 constexpr int kFewMinUnits = 1;
+// Rows from which on each wave of the joining launch takes one by itself; below, the four of a workgroup share it (one
+// token over 4000: 10.4 us, 12.4 with a wave a row; 4096 rows: 59 us, 56 with a wave a row).
 constexpr int64_t kRowAWave = 2048;
+// Workgroups up to which the many-rows kernel's tiles are cut, three rounds of one a CU, and tiles from which on none
+// is: sixteen rounds, of which a cut could fill up the last one only, and no joining launch.
 constexpr int64_t kMostPieces = 768;
 constexpr int64_t kUncutTiles = 4096;
 

@@ -696,10 +696,12 @@ dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
  *   these sizes or larger ones (DG_ERR_SCRATCH below what the call needs),
  *   16-byte aligned, contents arbitrary; calls that share one must be ordered
  * Values out of range in kv_lens and q_starts are clamped to what the table and
- * Q hold (no fault). The products are exact bf16 products with fp32 sums; the
- * weights of the second one are rounded to 11 bits; everything else is fp32 up
- * to the rounding of out. Deterministic: the split of the keys follows from the
- * lengths, and partial results are added in a fixed order.
+ * Q hold (no fault). The first product is one of exact bf16 values with fp32
+ * sums; the second one takes its weights, and but for few rows (new tokens x
+ * heads of a group) the scaled values, rounded to 11 bits; the rest is fp32 up
+ * to the rounding of out. Values whose |scale| is less than 2^-20 of the largest
+ * in the sequence lose further bits. Deterministic: the split of the keys
+ * follows from the lengths, and partial results are added in a fixed order.
  * Constraints: q_heads % heads == 0, both caches with the same sizes, window >=
  * 0, scale finite (DG_ERR_BAD_SHAPE); table_width * page_size at most 2^30, T *
  * q_heads below 2^31, B * heads * (table_width * page_size / 128 + 2) below

@@ -873,3 +873,14 @@ def test_attention_of_many_few_rows(gpu_device):
                                         ([(1, 300 + 61 * i) for i in range(67)], 35, 7, 64)):
         b = Batch(lengths, heads, kv_heads, D, 16, 24)
         b.check(b.call())
+
+
+@pytest.mark.parametrize("window", [0, 300])
+def test_attention_of_many_chunks(gpu_device, window):
+    """More sequences than a wave has lanes, whose tiles are cut, beside single tokens and sequences without new ones."""
+    lengths = [((40, 1, 33, 0)[i % 4], 900 + 11 * i) for i in range(131)]
+    b = Batch(lengths, 2, 1, 64, 16, 25)
+    got = b.call(window=window)
+    b.check(got, window=window)
+    b.ws.fill_(0xFF)
+    assert torch.equal(b.call(window=window), got)
