@@ -338,9 +338,10 @@ __device__ __forceinline__ void store_bf16(uint16_t *to, const float *v)
 // Two units are in flight, in registers of their own (one: 260 us for 64
 // sequences of up to 16384 tokens, 8 key heads of 8; two: 226 us, 5.1 TB/s, which
 // is the rate of a large copy). 208 registers for one tile of rows, two waves a
-// SIMD; with two tiles 256 and 14 spilled (16 sequences of 4 tokens up to 8192: 48
-// us, 62% of the copy's rate: a workgroup has four units or so, and the first
-// and the last are not hidden).
+// SIMD; with two tiles 256, of which the queries' would spill: they stay in LDS,
+// the same for all waves (16 sequences of 4 tokens up to 8192: 56 -> 54 us with
+// the joining launch, 62% of the copy's rate without it: a workgroup has four
+// units or so, and the first and the last are not hidden).
 template <int D, int NT>
 __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 {
@@ -353,6 +354,8 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
     __shared__ __align__(16) float scales[4][64];
     __shared__ float refs[4][2][16 * NT];
     __shared__ __align__(16) float sums[4][16][kPad];
+    // Queries of two tiles.
+    __shared__ __align__(16) u32x4 queries[NT > 1 ? NT * KS : 1][64];
 
     Piece w;
     if (!find_piece(p, blockIdx.x, w))
@@ -381,8 +384,16 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
             if (present)
                 v = *(const u32x4 *)(row + (D / 4) * g + 8 * t);
             q[nt][t] = __builtin_bit_cast(bf16x8, v);
+            if (NT > 1 && wave == t % 4)
+                queries[NT > 1 ? nt * KS + t : 0][lane] = v;
         }
     }
+    if (NT > 1)
+        __syncthreads();
+
+    const auto query = [&](int nt, int t) {
+        return NT > 1 ? __builtin_bit_cast(bf16x8, (u32x4)queries[NT > 1 ? nt * KS + t : 0][lane]) : q[nt][t];
+    };
 
     // What a unit brings: its codes, the scale of this lane's key, which keys are there, and the page of this lane's key
     // in the unit after the next.
@@ -535,7 +546,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                                  codes_to_bf16<false>(row[2 * t + 1]), codes_to_bf16<true>(row[2 * t + 1])};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    s[nt][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), q[nt][t],
+                    s[nt][sub] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), query(nt, t),
                                                                          s[nt][sub], 0, 0, 0);
             }
         }
@@ -622,11 +633,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
         odd.page = load_page(1);
         load(0, even);
         load(1, odd);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        if (NT == 1) {
 #pragma unroll
             for (int t = 0; t < KS; ++t)
-                asm volatile("" : "+v"(q[nt][t]));
+                asm volatile("" : "+v"(q[0][t]));
+        }
         // (No way out in the middle: where two ways join, loads are waited for as on the shorter one.)
         for (int u = 0; u + 1 < units; u += 2) {
             attend(u, even);
