@@ -10,22 +10,26 @@
 //
 // Roundings. The codes are exact in bf16 and fp16, so the products q . K are
 // exact bf16 products summed in fp32; both scales are applied in fp32. The
-// second product takes fp16 (bf16 weights, with 8 bits, would add as much error
-// as the output's own rounding). The few-rows kernel rounds its weights p sV to
-// fp16's 11 bits and multiplies the codes; the many-rows kernel rounds p, sV and
-// sV V, once for all of a tile's rows, and sums the rounded p for the
-// denominator. Sums, references and the outputs before their rounding are fp32.
-// fp16's range is kept by two references. p is exp2(x - m) with a running m
-// whose weight was 2^7 when it was set; m moves when weights pass 2^15 or so,
-// so that rows rarely move their sums. sV is divided by a power of two that is
-// at least the largest |sV| seen. What lies below fp16's normal numbers is off
-// by 2^-25 instead of relatively: p below 2^-21 of a row's largest, sV V where sV
-// is below 2^-20 of the largest that the tile's rows were given.
+// second product takes the weights w_j = p_j sV_j in fp16 (11 bits, off by 2^-11;
+// bf16's 8 would add as much error as the output's own rounding) and the codes.
+// The denominator's exponentials, all sums, the references and the outputs
+// before their rounding are fp32.
+// fp16's range is kept by one reference for each row: p is exp2(x - m), and m
+// follows the row's largest weight, not its largest p: the largest |w| was 2^7
+// when m was set, and m moves when one passes 2^15, so that rows rarely move
+// their sums. So what a row does not see, or sees with next to no weight, has no
+// say in how its other weights are rounded, whatever its scale. Weights below
+// fp16's normal numbers are off by 2^-25, 2^-32 of the row's largest. p takes up
+// fp32's exponents for this: with the row's largest weight on a key of scale s
+// it lies about 2^7 / s. Scales below 2^-100 count as 0, so that it stays finite,
+// and what lies below 2^-133 s of that key's p drops out.
 //
-// Masked keys never count, whatever their rows hold: their weight is set to 0,
-// and codes of V that are NaN there are replaced (0 * NaN would be NaN). A row
-// that sees a NaN code comes out as NaN: in that column, or in all of them where
-// the code lies in a tile that is masked for some rows.
+// Masked keys never count, whatever their rows hold: their p is set to 0, scales
+// that are not finite and codes of V that are NaN there are replaced (0 * NaN
+// would be NaN). A row that sees a NaN code comes out as NaN: in that column, or
+// in all of them where the code lies in a tile that is masked for some rows; a
+// row that sees a scale that is not finite, in all of them. A row of zeros has
+// the scale 1, which says nothing about values beside it: it counts as 2^-100.
 //
 // Which kernel. The cache's bytes bound few rows: each key is read once, at
 // 2 D + 8 bytes, and costs 4 D operations a row, so up to some 60 rows the read
@@ -37,6 +41,8 @@
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "cache.hpp"
 
@@ -64,10 +70,10 @@ constexpr int kJoinRows = 4;             // of a cut tile, that a workgroup join
 constexpr int kJoinGroups = 1024;        // workgroups that do
 constexpr int kTileKeys = 64;            // keys that a workgroup of the many-rows kernel takes at once
 constexpr float kNoMax = -1e30f;         // reference of a row that has seen nothing; finite, so that differences are
-constexpr float kSlack = 8.0f;           // how far x may pass its reference
-constexpr float kMostWeight = 0x1p15f;   // how far the sum of a lane's weights of a tile may go (fp16 ends at 65504)
+constexpr float kTopWeight = 7.0f;       // log2 of a row's largest weight when its reference is set
+constexpr float kMostWeight = 0x1p15f;   // how far a weight may go before the reference moves (fp16 ends at 65504)
 constexpr float kUnset = -1.0f;          // limit of a row whose reference has not been set
-constexpr int kNoScale = -100;           // exponent below which sV's reference does not go
+constexpr float kLeastScale = 0x1p-100f; // of values; what lies below counts as 0
 
 // One of the two caches: rows of 16-byte multiples, addressed in units of 16 bytes.
 struct Rows {
@@ -182,20 +188,6 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ uint32_t times(uint32_t two, f16x2 by)
-{
-    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, two) * by);
-}
-
-__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-
-// Exponent of the least power of two that is not below s (finite, at least 0): up to 128, for which power_of_2 is infinite.
-__device__ __forceinline__ int exponent_above(float s)
-{
-    const uint32_t bits = __float_as_uint(s);
-    return (int)(bits >> 23) - 127 + ((bits & 0x7fffffu) != 0);
-}
-
 __device__ __forceinline__ bool has_nan_code(uint32_t codes)  // 0x7f or 0xff among four
 {
     return (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
@@ -206,6 +198,60 @@ __device__ __forceinline__ uint32_t without_nan_codes(uint32_t codes)
 {
     const uint32_t nan = (((codes & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
     return codes & ~(nan * 0xffu);
+}
+
+// The value that lane I of a lane's 16 has: an operand of the instruction that takes it.
+template <int I>
+__device__ __forceinline__ float from_lane(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), 0x150 + I, 0xF, 0xF, true));
+}
+
+// f(0), f(1), .. f(N - 1), with the numbers as types.
+template <typename F, int... I>
+__device__ __forceinline__ void for_each(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>()), ...);
+}
+
+// Whether a scale of values can go into weights as it is.
+__device__ __forceinline__ bool usable(float scale)
+{
+    return fabsf(scale) >= kLeastScale && fabsf(scale) < __builtin_inff();
+}
+
+// Bits of the 32 keys whose codes are all zeros; a lane holds (some elements of) the keys 16 (i / 4) + 4 (lane / 16) + i % 4.
+template <int VW>
+__device__ __forceinline__ uint32_t rows_of_zeros(const uint32_t (&codes)[8][VW])
+{
+    uint32_t zeros = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        uint32_t some = 0;
+#pragma unroll
+        for (int l = 0; l < VW; ++l)
+            some |= codes[i][l] & 0x7f7f7f7fu;
+        const uint64_t lanes = __ballot(some != 0);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            zeros |= (uint32_t)((lanes >> (16 * g) & 0xffff) == 0) << (16 * (i / 4) + 4 * g + i % 4);
+    }
+    return zeros;
+}
+
+// A row's move to a reference at which its largest weight is 2^kTopWeight: by how much (exactly, as x is moved too).
+__device__ __forceinline__ float move_reference(float &ref, float top)
+{
+    const float next = ref + (top - kTopWeight), by = next - ref;
+    ref = next;
+    return by;
+}
+
+// exp2(2 half) v, for exponentials whose sum lies far from 1: the factor alone could leave fp32's range.
+__device__ __forceinline__ float scaled(float v, float half)
+{
+    const float f = __builtin_amdgcn_exp2f(half);
+    return v * f * f;
 }
 
 // ---------------------------------------------------------------- few rows
@@ -447,11 +493,10 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 
     f32x4 o[NT][DT];
     float ref[NT], limit[NT], sum[NT];
-    int exponent = kNoScale;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         ref[nt] = sum[nt] = 0.0f;
-        limit[nt] = -__builtin_inff();
+        limit[nt] = pos[nt] >= 0 ? kUnset : kMostWeight;
 #pragma unroll
         for (int t = 0; t < DT; ++t)
             o[nt][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -461,27 +506,11 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
         const uint32_t there = raw.there;
         const float found = raw.scale;
         const int first = key0 + u * kUnit;
+        // Scales that cannot be weighed with are replaced; their keys are looked at below.
+        const bool mine = values && (there >> (lane & 31) & 1);
         const bool masked = there != 0xffffffffu || first + 31 > w.s.n - w.s.m ||
-                            (p.window && first <= w.s.n - 1 - p.window);
-
-        // V's reference covers the unit's finite scales.
-        const float size = fabsf(found);
-        const bool counts = values && (there >> (lane & 31) & 1) && size < __builtin_inff();
-        if (__ballot(counts && size > power_of_2(exponent))) {
-            float most = counts ? size : 0.0f;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2)
-                most = fmaxf(most, __shfl_xor(most, d, 64));
-            const int e = max(exponent_above(most), exponent);
-            const float shrink = exponent - e < -126 ? 0.0f : power_of_2(exponent - e);
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int t = 0; t < DT; ++t)
-                    o[nt][t] *= shrink;
-            exponent = e;
-        }
-        scales[wave][lane] = values ? found * power_of_2(7 - exponent) : found * p.scale_log2;
+                            (p.window && first <= w.s.n - 1 - p.window) || __ballot(mine && !usable(found)) != 0;
+        scales[wave][lane] = !values ? found * p.scale_log2 : usable(found) ? found : kLeastScale;
         wave_sync();
         float ks[8], vs[8];
 #pragma unroll
@@ -495,23 +524,29 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
             }
         }
         wave_sync();
+        if (__ballot(mine && found == 1.0f)) {
+            const uint32_t zeros = rows_of_zeros(raw.v) >> (4 * g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                vs[i] = (zeros >> (16 * (i / 4) + i % 4) & 1) && vs[i] == 1.0f ? kLeastScale : vs[i];
+        }
 
-        // This lane's keys whose values are not finite: codes and scales are replaced by zeros, and a row that sees one
-        // becomes NaN.
+        // This lane's keys whose values are not finite: codes are replaced by zeros, and a row that sees one becomes NaN.
         uint32_t bad = 0;
         if (masked) {
+            const uint32_t infinite = (uint32_t)(__ballot(mine && !(fabsf(found) < __builtin_inff())) >> 32) >> (4 * g);
+            const uint32_t none = (uint32_t)(__ballot(mine && fabsf(found) < kLeastScale) >> 32);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const bool here = there >> (4 * g) >> (16 * (i / 4) + i % 4) & 1;
+                const int at = 16 * (i / 4) + i % 4;
+                const bool here = (there & ~none) >> (4 * g) >> at & 1;
                 bool nan = false;
 #pragma unroll
                 for (int l = 0; l < VW; ++l) {
                     nan |= has_nan_code(raw.v[i][l]);
                     raw.v[i][l] = here ? without_nan_codes(raw.v[i][l]) : 0;
                 }
-                const bool finite = fabsf(vs[i]) < __builtin_inff();
-                vs[i] = finite ? vs[i] : 0.0f;
-                if (!finite || (__ballot(nan) >> (16 * g) & 0xffff) != 0)
+                if ((infinite >> at & 1) || (__ballot(nan) >> (16 * g) & 0xffff) != 0)
                     bad |= 1u << i;
             }
         }
@@ -571,34 +606,42 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                         sum[nt] = __builtin_nanf("");
                 }
             }
-            float most = x[0];
+            float most, part;
+            const auto weigh = [&]() {
+                most = part = 0.0f;
+                float y[8];
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
-                most = fmaxf(most, x[i]);
+                for (int i = 0; i < 8; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(x[i]);
+                    part += e;
+                    y[i] = e * vs[i];
+                    most = fmaxf(most, fabsf(y[i]));
+                }
+                const u32x4 packed = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
+                weights[nt] = __builtin_bit_cast(f16x8, packed);
+            };
+            weigh();
             if (__ballot(most > limit[nt])) {
-                const float top = max_across(most);
-                const bool moves = top > limit[nt];
-                const float by = moves ? top : 0.0f;
-                const float shrink = limit[nt] == kSlack ? __builtin_amdgcn_exp2f(-by) : 1.0f;
-                sum[nt] *= shrink;
+                float top = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    top = fmaxf(top, x[i] + __builtin_amdgcn_logf(fabsf(vs[i])));
+                top = max_across(top);
+                const bool moves = max_across(most) > limit[nt] && top > -__builtin_inff();
+                const float by = moves ? move_reference(ref[nt], top) : 0.0f;
+                const float half = limit[nt] == kUnset ? 0.0f : -0.5f * by;
+                const float shrink = scaled(1.0f, half);
+                sum[nt] = scaled(sum[nt], half);
 #pragma unroll
                 for (int t = 0; t < DT; ++t)
                     o[nt][t] *= shrink;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     x[i] -= by;
-                ref[nt] += by;
-                limit[nt] = moves ? kSlack : limit[nt];
+                limit[nt] = moves ? kMostWeight : limit[nt];
+                weigh();
             }
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float e = __builtin_amdgcn_exp2f(x[i]);
-                sum[nt] += e;
-                y[i] = e * vs[i];
-            }
-            const u32x4 packed = {pack_f16(y[0], y[1]), pack_f16(y[2], y[3]), pack_f16(y[4], y[5]), pack_f16(y[6], y[7])};
-            weights[nt] = __builtin_bit_cast(f16x8, packed);
+            sum[nt] += part;
         }
 
         // O^T += V^T P^T
@@ -653,7 +696,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const float all = sum_across(sum[nt]);
-        ref[nt] = limit[nt] == kSlack ? ref[nt] : kNoMax;
+        ref[nt] = limit[nt] == kUnset ? kNoMax : ref[nt];
         if (g == 0) {
             refs[wave][0][16 * nt + c] = ref[nt];
             refs[wave][1][16 * nt + c] = all;
@@ -668,7 +711,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             top = fmaxf(top, refs[i][0][16 * nt + c]);
-        const float factor = __builtin_amdgcn_exp2f(ref[nt] - top) * power_of_2(exponent - 7);
+        const float factor = __builtin_amdgcn_exp2f(ref[nt] - top);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -684,7 +727,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 most = fmaxf(most, refs[i][0][r]);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                total += refs[i][1][r] * __builtin_amdgcn_exp2f(refs[i][0][r] - most);
+                total += scaled(refs[i][1][r], 0.5f * (refs[i][0][r] - most));
             float y[DT];
 #pragma unroll
             for (int t = 0; t < DT; ++t)
@@ -731,7 +774,7 @@ __device__ __forceinline__ void join_pieces(const Parts &parts, int count, int f
         const int64_t at = index(i);
         const f32x2 ml = *(const f32x2 *)(parts.ml + 2 * at);
         const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
-        total = __builtin_fmaf(ml[1], weight, total);
+        total += scaled(ml[1], 0.5f * (ml[0] - top));
         const float *o = parts.o + at * D + E * lane;
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -984,14 +1027,12 @@ struct ManyLds {
     __align__(16) uint8_t k[2][kTileKeys * kRowBytes<D>];
     __align__(16) uint8_t v[2][D * kColumnBytes];
     __align__(16) float kscales[2][kTileKeys];
+    float vscales[2][kTileKeys];
     struct {
         uint32_t present[2];             // bits of the keys that are there
-        int references[2];               // exponent of V's reference, doubled, and 1 where `bad` has bits
-        uint32_t bad[2];                 // bits of keys whose values are not finite, where some row does not see every key
-        uint32_t unused[2];
+        uint32_t bad[2];                 // bits of keys whose values are not finite, where they were looked at
     } __align__(16) about[2];
     __align__(16) uint32_t offsets[4][kHalf];            // of the rows that a wave loads next
-    __align__(16) _Float16 vscales[2][kHalf];            // in units of the reference's 2^-6
 };
 
 // The keys of a workgroup.
@@ -1105,7 +1146,7 @@ __device__ __forceinline__ void bring_k(const AttendParams &p, const Keys &k, co
     bring(k.tiles, rider, load, store, even, odd);
 }
 
-// V: codes times their scale to fp16, transposed.
+// V: codes to fp16, transposed.
 template <int D>
 __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, const int32_t *table, int head, int part,
                                         ManyLds<D> &lds)
@@ -1121,7 +1162,6 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
         uint32_t there;
         int page;                        // of the tile after the next
     } even, odd;
-    int reference = kNoScale;
     const auto load = [&](int t, Raw &raw) {
         uint32_t offset;
         raw.there = rider.place(t, raw.page, offset, raw.scale);
@@ -1147,26 +1187,23 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
     };
     const auto store = [&](int t, Raw &raw) {
         const uint32_t there = raw.there;
-        const float found = there >> (lane & 31) & 1 ? raw.scale : 0.0f, size = fabsf(found);
-        const bool finite = size < __builtin_inff();
-        // The other V wave's reference as of the tile before, or the two would differ for good.
-        reference = max(reference, t ? __builtin_amdgcn_readfirstlane(lds.about[(t + 1) & 1].references[1 - part]) >> 1 : kNoScale);
-        if (__ballot(finite && size > power_of_2(reference))) {
-            float most = finite ? size : 0.0f;
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2)
-                most = fmaxf(most, __shfl_xor(most, d, 64));
-            reference = max(__builtin_amdgcn_readfirstlane(exponent_above(most)), reference);
+        const float found = raw.scale;
+        const bool mine = there >> (lane & 31) & 1;
+        // Scales that cannot be weighed with are replaced.
+        float scale = mine && usable(found) ? found : kLeastScale;
+        if (__ballot(mine && found == 1.0f)) {
+            const uint32_t zeros = rows_of_zeros(raw.codes);
+            scale = (zeros >> (lane & 31) & 1) && scale == 1.0f ? kLeastScale : scale;
         }
         uint32_t bad = 0;
-        float factor = power_of_2(6 - reference);
-        if (masked(rider.first(t), there, k.pos_first, k.pos_last, p.window)) {
-            // What is not there becomes zeros (0 * NaN would be NaN), and so do NaN codes and scales that are not
-            // finite, whose keys are noted.
+        if (masked(rider.first(t), there, k.pos_first, k.pos_last, p.window) || __ballot(mine && !usable(found))) {
+            // What is not there becomes zeros (0 * NaN would be NaN), and so do NaN codes; keys that hold them or have
+            // scales that are not finite are noted.
+            const uint32_t none = (uint32_t)__ballot(mine && fabsf(found) < kLeastScale);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int key = 16 * (i / 4) + i % 4;    // of group 0
-                const bool here = there >> (4 * group) >> key & 1;
+                const bool here = (there & ~none) >> (4 * group) >> key & 1;
                 bool nan = false;
 #pragma unroll
                 for (int l = 0; l < VW; ++l) {
@@ -1178,22 +1215,17 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
                 for (int g = 0; g < 4; ++g)
                     bad |= (uint32_t)((some >> (16 * g) & 0xffff) != 0) << (key + 4 * g);
             }
-            bad |= (uint32_t)__ballot(!finite);
-            factor = finite ? factor : 0.0f;
+            bad |= (uint32_t)__ballot(mine && !(fabsf(found) < __builtin_inff()));
         }
         if (lane < kHalf)
-            lds.vscales[part][lane] = (_Float16)(factor == 0.0f ? 0.0f : found * factor);
-        if (lane == 0) {
+            lds.vscales[t & 1][kHalf * part + lane] = scale;
+        if (lane == 0)
             lds.about[t & 1].bad[part] = bad;
-            lds.about[t & 1].references[part] = 2 * reference + (bad != 0);
-        }
-        wave_sync();
         // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers. Element (D / 16) col + i
         // has row 16 i + col, so that lanes write consecutive rows.
         uint8_t *to = lds.v[t & 1] + col * kColumnBytes + 2 * kHalf * part + 16 * (group & 1) + 8 * (group >> 1);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const f16x4 vs = *(const f16x4 *)&lds.vscales[part][16 * r + 4 * group];
 #pragma unroll
             for (int l = 0; l < VW; ++l) {
                 uint32_t both[2][2];     // keys 0, 1 and 2, 3; elements 0, 1 and 2, 3
@@ -1208,13 +1240,11 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
                     u32x2 v;
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        v[i] = times(d % 2 ? codes_to_f16<true>(both[i][d / 2]) : codes_to_f16<false>(both[i][d / 2]),
-                                     f16x2{vs[2 * i], vs[2 * i + 1]});
+                        v[i] = d % 2 ? codes_to_f16<true>(both[i][d / 2]) : codes_to_f16<false>(both[i][d / 2]);
                     *(u32x2 *)(to + 16 * (4 * l + d) * kColumnBytes + 32 * r) = v;
                 }
             }
         }
-        wave_sync();
     };
     bring(k.tiles, rider, load, store, even, odd);
 }
@@ -1298,9 +1328,8 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
     const int wave_last = r0 < w.s.rows ? base + (int)quotient(min(r0 + 32, w.s.rows) - 1, p.group) : -1;
 
     f32x16 o[DT];
-    // Weights are exp2(x - ref), 2^7 where ref was set; past `limit` for the sum of a lane's weights of 32 keys it moves.
+    // A weight past `limit` moves the reference.
     float ref = 0.0f, limit = pos >= 0 ? kUnset : kMostWeight, sum = 0.0f;
-    int exponent = kNoScale;             // of V's reference in o
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -1342,11 +1371,11 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                     x[b][4 * i + c] = __builtin_fmaf(x[b][4 * i + c], ks[c], -ref);
             }
             const uint32_t there = (uint32_t)__builtin_amdgcn_readfirstlane((int)about[b]);
-            const int e2 = __builtin_amdgcn_readfirstlane((int)about[2 + b]), e = e2 >> 1;
-            if (masked(first + 32 * b, there, wave_first, wave_last, p.window) || (e2 & 1)) {
+            const uint32_t unfit = (uint32_t)__builtin_amdgcn_readfirstlane((int)about[2 + b]);
+            if (masked(first + 32 * b, there, wave_first, wave_last, p.window) || unfit) {
                 // A row that sees a key whose values are not finite (they are zeros now) becomes NaN. From this lane's
                 // first key on, keys [from, to] are seen, where they are there.
-                const uint32_t mine = there >> (4 * hf), bad = lds.about[t & 1].bad[b] >> (4 * hf);
+                const uint32_t mine = there >> (4 * hf), bad = unfit >> (4 * hf);
                 const int to = pos - (first + 32 * b) - 4 * hf, from = p.window ? to - p.window + 1 : -kTileKeys;
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
@@ -1360,52 +1389,46 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
             // The next half's scores, while this one's weights are formed.
             if (b == 0)
                 multiply_k(1);
-            // The weights in fp16, as the second product takes them, and their sum.
+            // The weights in fp16, as the second product takes them, and the sum of the exponentials. The values' scales
+            // of a lane's 16 keys lie in the 16 lanes around it, which takes one register instead of 16.
+            const float scale = lds.vscales[t & 1][32 * b + 8 * (lane >> 2 & 3) + 4 * hf + (lane & 3)];
             u32x4 weights[2];
-            float part;
+            float part, most;
             const auto weigh = [&]() {
-                float parts[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t two =
-                        pack_f16(__builtin_amdgcn_exp2f(x[b][2 * i]), __builtin_amdgcn_exp2f(x[b][2 * i + 1]));
+                part = most = 0.0f;
+                for_each([&](auto pair) {
+                    constexpr int i = pair.value;
+                    const float e0 = __builtin_amdgcn_exp2f(x[b][2 * i]), e1 = __builtin_amdgcn_exp2f(x[b][2 * i + 1]);
+                    part += e0;
+                    part += e1;
+                    const float y0 = e0 * from_lane<2 * i>(scale), y1 = e1 * from_lane<2 * i + 1>(scale);
+                    most = fmaxf(fmaxf(most, fabsf(y0)), fabsf(y1));
+                    uint32_t two = pack_f16(y0, y1);
+                    // Here and now, or all exponentials wait in registers for their sum, and others are spilled.
+                    asm volatile("" : "+v"(two), "+v"(part));
                     weights[i / 4][i % 4] = two;
-                    parts[i % 2] = __builtin_amdgcn_fdot2(__builtin_bit_cast(f16x2, two),
-                                                          f16x2{(_Float16)1.0f, (_Float16)1.0f}, parts[i % 2], false);
-                }
-                part = parts[0] + parts[1];
+                }, std::make_integer_sequence<int, 8>());
             };
             weigh();
-            if (__ballot(part > limit) || e != exponent) {
-                // The sums shrink to a larger reference of V; for a smaller one (two waves bring in V, with a reference
-                // each) the weights do.
-                const float change = exponent - e < -126 ? 0.0f : power_of_2(min(exponent - e, 0));
-                const _Float16 lower = (_Float16)(e - exponent < -126 ? 0.0f : power_of_2(min(e - exponent, 0)));
-                exponent = max(exponent, e);
-                float top = x[b][0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i)
-                    top = fmaxf(top, x[b][i]);
+            if (__ballot(most > limit)) {
+                const float log = __builtin_amdgcn_logf(fabsf(scale));
+                float top = -__builtin_inff();
+                for_each([&](auto i) { top = fmaxf(top, x[b][i.value] + from_lane<i.value>(log)); }, std::make_integer_sequence<int, 16>());
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const int over = part > limit, other = __shfl_xor(over, 32, 64);    // of the row's other half
+                const int over = most > limit, other = __shfl_xor(over, 32, 64);    // of the row's other half
                 const bool moves = (over | other) != 0 && top > -__builtin_inff();
-                const float by = moves ? top - 7.0f : 0.0f;
-                float shrink = limit == kUnset ? 1.0f : __builtin_amdgcn_exp2f(-by);
-                sum *= shrink;
-                shrink *= change;
+                const float by = moves ? move_reference(ref, top) : 0.0f;
+                const float half = limit == kUnset ? 0.0f : -0.5f * by;
+                const float shrink = scaled(1.0f, half);
+                sum = scaled(sum, half);
 #pragma unroll
                 for (int d = 0; d < DT; ++d)
                     o[d] *= shrink;
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     x[b][i] -= by;
-                ref += by;
                 limit = moves ? kMostWeight : limit;
                 weigh();
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    weights[i / 4][i % 4] = __builtin_bit_cast(
-                        uint32_t, __builtin_bit_cast(f16x2, (uint32_t)weights[i / 4][i % 4]) * f16x2{lower, lower});
             }
             sum += part;
 #pragma unroll
@@ -1422,7 +1445,6 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
     sum += __shfl_xor(sum, 32, 64);
     if (!row_present)
         return;
-    const float factor = power_of_2(exponent - 6);
     // Registers i % 8 of all tiles hold consecutive elements.
     constexpr int E = 2 * DT;
     uint16_t *to = p.out + (int64_t)(w.s.start + token) * p.o_t + (int64_t)(head * (int)p.group.d + h) * p.o_h;
@@ -1435,7 +1457,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-                y[2 * d + e] = o[d][i + 8 * e] * factor;
+                y[2 * d + e] = o[d][i + 8 * e];
         if (w.pieces == 1) {
 #pragma unroll
             for (int e = 0; e < E; ++e)

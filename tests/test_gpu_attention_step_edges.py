@@ -1,0 +1,156 @@
+"""Attention over a paged cache of e4m3 codes where scales of values lie far apart: keys that a row does not see, and
+those that it gives next to no weight, do not touch what the others give it.
+
+Tolerances: those of tests/test_gpu_attention_step.py, but for the last one, of weights below fp16's normal numbers. A
+weight p |sV| is off by 2^-25 there where the largest that its row sees is 2^7 or more; and it may drop out in fp32,
+below 2^-126 of an exponential that is 2^7 / sV or more where it counts most: with |sV| below 2^101 that is 2^-25 of the
+weight again. With M = max p |sV| / sum p over the keys that the row sees and codes below 2^9 in magnitude, n keys are
+off by n 2 2^-32 2^9 M = n 2^-22 M together. A row of zeros counts in M with 2^-100, which the kernels take for its
+scale: where the others' are hardly larger, its weight is the row's largest and theirs are rounded beside it. bf16's numbers below
+2^-126 are 2^-133 apart, so the rounding of an output is off by up to 2^-134 there, which is more than 2^-8 of it (the
+smallest outputs here are about 2^-125).
+"""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_attention_step import BF16, F64, MIXES, Batch, half, values
+
+pytestmark = pytest.mark.gpu
+
+
+def reference(b, window=0):
+    """Outputs of a Batch in 64 bits and how far each may be off, from what its row sees alone."""
+    scale, page, pages = b.D ** -0.5, b.page, b.k[0].shape[0]
+    group = b.q.shape[1] // b.k[0].shape[2]
+    out = torch.full(b.q.shape, math.nan, dtype=F64, device="cuda")
+    tol = torch.zeros_like(out)
+    for i, (m, n) in enumerate(b.lengths):
+        if m == 0:
+            continue
+        j = torch.arange(n, device="cuda")
+        held = b.table[i].long()[j // page]
+        there = (held >= 0) & (held < pages)
+        held = torch.where(there, held, 0)
+        k, v = (values(c[held, j % page], s[held, j % page]) for c, s in (b.k, b.v))
+        weigh = torch.where((v != 0).any(-1), b.v[1][held, j % page].double().abs(), 2.0 ** -100)
+        pos = torch.arange(n - m, n, device="cuda")[:, None]
+        seen = (j <= pos) & there
+        if window:
+            seen &= j > pos - window
+        rows = slice(b.starts[i], b.starts[i] + m)
+        for h in range(b.q.shape[1]):
+            q, kh, vh, w = b.q[rows, h].double(), k[:, h // group], v[:, h // group], weigh[:, h // group]
+            x = torch.where(seen, scale * (q @ kh.t()), -math.inf)
+            p = torch.softmax(x, 1).nan_to_num(0.0)
+            # how far each weight may be off by its score, which moves numerator and denominator
+            pe = p * 2 * (b.D + 4) * 2.0 ** -24 * scale * (q.abs() @ kh.abs().t())
+            out[rows, h] = p @ vh
+            a = p @ vh.abs()
+            tol[rows, h] = half(BF16) * out[rows, h].abs() + 2.0 ** -134 * (a > 0)
+            tol[rows, h] += (2.0 ** -9 + 2.0 ** -19 + n * 2.0 ** -23) * a + pe @ vh.abs() + pe.sum(1, keepdim=True) * a
+            tol[rows, h] += n * 2.0 ** -22 * (p * w).amax(1, keepdim=True)
+    return out, tol
+
+
+def hold(got, ref, tol, rows):
+    off = (got[rows].double() - ref[rows]).abs()
+    assert bool((off <= tol[rows]).all()), "off by %.3g more than allowed" % float((off - tol[rows]).amax())
+
+
+def last_key(b, i):
+    """Page and offset of a sequence's last token."""
+    n = b.lengths[i][1]
+    return int(b.table[i, (n - 1) // b.page]), (n - 1) % b.page
+
+
+@pytest.mark.parametrize("power", [22, 30, 100, 127])
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES + [([(8, 20)], 2, 1, 128, 16), ([(20, 20)], 1, 1, 64, 16)])
+def test_a_large_scale_in_the_future(gpu_device, lengths, heads, kv_heads, D, page, power):
+    """The last key's values have a scale of 2^power: for the rows before it they are not there."""
+    b = Batch(lengths, heads, kv_heads, D, page, 31)
+    clean, (ref, tol) = b.call(), reference(b)
+    for i in range(len(lengths)):
+        b.v[1][last_key(b, i)] = 2.0 ** power
+    got = b.call()
+    after = reference(b) if power <= 100 else None
+    for i, (m, _) in enumerate(lengths):
+        rows = slice(b.starts[i], b.starts[i] + m - 1)
+        hold(got, ref, tol, rows)
+        assert torch.equal(got[rows], clean[rows])
+        if after:
+            hold(got, *after, slice(b.starts[i] + m - 1, b.starts[i] + m))
+
+
+@pytest.mark.parametrize("power", [22, 30, 100])
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_a_large_scale_that_has_left_the_window(gpu_device, lengths, heads, kv_heads, D, page, power):
+    """The first key that the first row sees: the first row's alone, in a window."""
+    b = Batch(lengths, heads, kv_heads, D, page, 32)
+    for i, (m, n) in enumerate(lengths):
+        j = max(0, n - m - 49)
+        b.v[1][int(b.table[i, j // page]), j % page] = 2.0 ** power
+    got = b.call(window=50)
+    hold(got, *reference(b, 50), slice(b.starts[0], b.starts[-1]))
+
+
+@pytest.mark.parametrize("power", [30, 60, 100])
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_a_large_scale_of_next_to_no_weight(gpu_device, lengths, heads, kv_heads, D, page, power):
+    """A key that every row sees and gives a weight of about exp(-150); scales of the others on both sides of 1."""
+    b = Batch(lengths, heads, kv_heads, D, page, 33)
+    b.q[...] = b.q.abs().clamp(0.25, 4.0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    b.v[1].mul_(2.0 ** torch.randint(-8, 9, b.v[1].shape, generator=g, device="cuda"))
+    for i, (m, n) in enumerate(lengths):
+        j = max(0, n - m - 20)
+        at = int(b.table[i, j // page]), j % page
+        b.k[0][at] = 0xFE                # -448
+        b.k[1][at] = 150 / (0.25 * 448 * D ** 0.5)
+        b.v[1][at] = 2.0 ** power
+    hold(b.call(), *reference(b), slice(b.starts[0], b.starts[-1]))
+
+
+@pytest.mark.parametrize("power", [-20, -35, -60, -90])
+@pytest.mark.parametrize("where", ["first", "spread"])
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_rows_of_zeros_beside_small_values(gpu_device, lengths, heads, kv_heads, D, page, where, power):
+    """Values of scales about 2^power, and rows of zeros, which have the scale 1: the first 150 keys of each sequence
+    but its last, or every third one."""
+    b = Batch(lengths, heads, kv_heads, D, page, 34)
+    b.v[1].mul_(2.0 ** power)
+    for i, (m, n) in enumerate(lengths):
+        j = torch.arange(n, device="cuda")
+        j = j[:min(150, n - 1)] if where == "first" else j[::3]
+        at = b.table[i].long()[j // page], j % page
+        b.v[0][at] = torch.tensor([0x00, 0x80], dtype=torch.uint8, device="cuda").repeat(D // 2)
+        b.v[1][at] = 1.0
+    hold(b.call(), *reference(b), slice(b.starts[0], b.starts[-1]))
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_pieces_whose_scales_lie_apart(gpu_device, lengths, heads, kv_heads, D, page):
+    """Scales from 2^-60 to 2^100 in runs of 64 keys, of both signs: largest first, largest last and in between."""
+    for turn in range(3):
+        b = Batch(lengths, heads, kv_heads, D, page, 35)
+        for i, (m, n) in enumerate(lengths):
+            j = torch.arange(n, device="cuda")
+            power = torch.tensor([[100, -60, 30, 0], [-60, 0, 30, 100], [0, 100, -60, 30]][turn], device="cuda")[j // 64 % 4]
+            at = b.table[i].long()[j // page], j % page
+            b.v[1][at] = torch.where(j % 5 == 0, -1.0, 1.0)[:, None] * 2.0 ** power.float()[:, None]
+        hold(b.call(), *reference(b), slice(b.starts[0], b.starts[-1]))
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_scales_of_nothing(gpu_device, lengths, heads, kv_heads, D, page):
+    """Scales of 0 and below 2^-100 count as 0, among others and by themselves."""
+    for small in (0.0, 2.0 ** -101, 2.0 ** -149):
+        b = Batch(lengths, heads, kv_heads, D, page, 36)
+        some = torch.arange(b.v[1].numel(), device="cuda").view(b.v[1].shape) % 3 == 0
+        b.v[1][some] = small
+        got = b.call()
+        b.v[1][some] = 0.0
+        hold(got, *reference(b), slice(b.starts[0], b.starts[-1]))
+        b.v[1][...] = small
+        assert bool((b.call()[b.starts[0]:b.starts[-1]] == 0).all())
