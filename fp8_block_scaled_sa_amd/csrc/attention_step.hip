@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <math.h>
+#include <numeric>
 #include <stdint.h>
 
 #include "attend.hpp"
@@ -40,6 +41,57 @@ bool rows_apart(std::initializer_list<Dim> dims, int64_t inner)
         span += (d[i].size - 1) * d[i].stride;
     }
     return true;
+}
+
+// A dimension of two sets of rows: how far an index of the second may lie from one of the first.
+struct Step {
+    int64_t stride, low, high;
+};
+
+Step step(Dim first, Dim second)
+{
+    if (first.size <= 1 || first.stride == 0)
+        return second.size <= 1 || second.stride == 0 ? Step{0, 0, 0} : Step{second.stride, 0, second.size - 1};
+    if (second.size <= 1 || second.stride == 0 || first.stride == second.stride)
+        return Step{first.stride, 1 - first.size, second.size <= 1 || second.stride == 0 ? 0 : second.size - 1};
+    // All that the two strides can come to.
+    return Step{std::gcd(first.stride, second.stride), -((int64_t)1 << 40), (int64_t)1 << 40};
+}
+
+// Whether a row of one set may come within `inner` elements of one of the other, `offset` behind it where all indices
+// are 0. Steps with strides falling. Exact where the dimensions nest; where a step has more indices than these to look
+// at, they do not.
+bool rows_meet(const Step *steps, int n, int64_t offset, int64_t inner)
+{
+    if (n == 0)
+        return offset > -inner && offset < inner;
+    if (steps->stride == 0)
+        return rows_meet(steps + 1, n - 1, offset, inner);
+    constexpr int64_t kFar = (int64_t)1 << 60;
+    int64_t reach = inner, more;
+    for (int i = 1; i < n; ++i)
+        if (__builtin_mul_overflow(std::max(-steps[i].low, steps[i].high), steps[i].stride, &more) || more > kFar ||
+            (reach += more) > kFar)
+            return true;
+    // |offset + i stride| < reach
+    const auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    const int64_t first = std::max(steps->low, floor_div(-reach - offset, steps->stride) + 1);
+    const int64_t last = std::min(steps->high, -floor_div(offset - reach, steps->stride) - 1);
+    constexpr int64_t kTries = 16;
+    if (last - first >= kTries)
+        return true;
+    for (int64_t i = first; i <= last; ++i)
+        if (rows_meet(steps + 1, n - 1, offset + i * steps->stride, inner))
+            return true;
+    return false;
+}
+
+bool rows_meet(std::initializer_list<Step> steps, int64_t offset, int64_t inner)
+{
+    Step s[3];
+    const int n = (int)(std::copy(steps.begin(), steps.end(), s) - s);
+    std::sort(s, s + n, [](const Step &a, const Step &b) { return a.stride > b.stride; });
+    return rows_meet(s, n, offset, inner);
 }
 
 int check_head_dim(int64_t D)
@@ -324,13 +376,21 @@ dg_status dg_fp8_rope_cache_write(const void *Q, int64_t q_stride_t, int64_t q_s
                            rot ? extent(freqs, 8, rot / 2 - 1) : none};
     const Extent outs[5] = {codes_extent(kc), codes_extent(vc), scales_extent(kc), scales_extent(vc),
                             Q ? rows_extent(Q_out, 2, T, qo_stride_t, q_heads, qo_stride_h, D) : none};
-    // Q_out may be Q itself (each row is read before it is written), also where Q, K and V are columns of one tensor.
+    // Q_out may be Q itself (each row is read before it is written), also where Q, K and V are columns of one tensor, but
+    // not where a row of K or V is one of Q.
     const bool in_place = Q && Q_out == Q && size == 2 && (T == 1 || qo_stride_t == q_stride_t) &&
                           (q_heads == 1 || qo_stride_h == q_stride_h);
     for (int i = 0; i < 5; ++i)
         for (int j = 0; j < 6; ++j)
             if (overlaps(outs[i], ins[j]) && !(i == 4 && in_place && j < 3))
                 return DG_ERR_ALIASING;
+    const auto among_queries = [&](const void *X, int64_t x_t, int64_t x_h) {
+        return rows_meet({step({T, q_stride_t}, {T, x_t}), step({q_heads, q_stride_h}, {heads, x_h})},
+                         ((const uint8_t *)X - (const uint8_t *)Q) / size, D);
+    };
+    if (in_place && ((overlaps(outs[4], ins[1]) && among_queries(K, k_stride_t, k_stride_h)) ||
+                     (overlaps(outs[4], ins[2]) && among_queries(V, v_stride_t, v_stride_h))))
+        return DG_ERR_ALIASING;
     // The two caches may be halves of one tensor, page by page or row by row; codes and scales lie apart.
     if (kc.codes == vc.codes || kc.scales == vc.scales)
         return DG_ERR_ALIASING;

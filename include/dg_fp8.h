@@ -644,8 +644,9 @@ typedef struct dg_fp8_cache {
  * caches with the same sizes; bases 16-byte aligned, strides of Q, K, V, Q_out
  * multiples of 16 bytes and at most 2^28 elements; q_heads at most 65536, T
  * below 2^24 (DG_ERR_UNSUPPORTED). Q_out may be Q itself (bf16, same address
- * and strides; then K and V may be other columns of the same tensor), and lies
- * apart from everything else otherwise; the caches lie apart from the inputs.
+ * and strides; then K and V may be other columns of the same tensor, with rows
+ * apart from Q's), and lies apart from everything else otherwise; the caches lie
+ * apart from the inputs (DG_ERR_ALIASING).
  * Deterministic; T = 0 returns DG_OK.
  */
 dg_status dg_fp8_rope_cache_write(const void *Q, int64_t q_stride_t, int64_t q_stride_h,
