@@ -9,6 +9,7 @@
 #include <math.h>
 #include <numeric>
 #include <stdint.h>
+#include <utility>
 
 #include "attend.hpp"
 #include "cache.hpp"
@@ -48,50 +49,63 @@ struct Step {
     int64_t stride, low, high;
 };
 
-Step step(Dim first, Dim second)
-{
-    if (first.size <= 1 || first.stride == 0)
-        return second.size <= 1 || second.stride == 0 ? Step{0, 0, 0} : Step{second.stride, 0, second.size - 1};
-    if (second.size <= 1 || second.stride == 0 || first.stride == second.stride)
-        return Step{first.stride, 1 - first.size, second.size <= 1 || second.stride == 0 ? 0 : second.size - 1};
-    // All that the two strides can come to.
-    return Step{std::gcd(first.stride, second.stride), -((int64_t)1 << 40), (int64_t)1 << 40};
-}
+constexpr int64_t kFar = (int64_t)1 << 60;
 
-// Whether a row of one set may come within `inner` elements of one of the other, `offset` behind it where all indices
-// are 0. Steps with strides falling. Exact where the dimensions nest; where a step has more indices than these to look
-// at, they do not.
-bool rows_meet(const Step *steps, int n, int64_t offset, int64_t inner)
+// Whether blocks of two sets may meet, of `first` and `second` elements, the second set's `offset` behind the first's
+// where all indices are 0. Steps with strides falling, none 0. Exact where the dimensions nest; where a step has more
+// indices than these to look at, they do not.
+bool blocks_meet(const Step *steps, int n, int64_t offset, int64_t first, int64_t second)
 {
     if (n == 0)
-        return offset > -inner && offset < inner;
-    if (steps->stride == 0)
-        return rows_meet(steps + 1, n - 1, offset, inner);
-    constexpr int64_t kFar = (int64_t)1 << 60;
-    int64_t reach = inner, more;
+        return offset > -second && offset < first;
+    int64_t reach = std::max(first, second), more;
     for (int i = 1; i < n; ++i)
         if (__builtin_mul_overflow(std::max(-steps[i].low, steps[i].high), steps[i].stride, &more) || more > kFar ||
             (reach += more) > kFar)
             return true;
     // |offset + i stride| < reach
     const auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
-    const int64_t first = std::max(steps->low, floor_div(-reach - offset, steps->stride) + 1);
-    const int64_t last = std::min(steps->high, -floor_div(offset - reach, steps->stride) - 1);
+    const int64_t from = std::max(steps->low, floor_div(-reach - offset, steps->stride) + 1);
+    const int64_t to = std::min(steps->high, -floor_div(offset - reach, steps->stride) - 1);
     constexpr int64_t kTries = 16;
-    if (last - first >= kTries)
+    if (to - from >= kTries)
         return true;
-    for (int64_t i = first; i <= last; ++i)
-        if (rows_meet(steps + 1, n - 1, offset + i * steps->stride, inner))
+    for (int64_t i = from; i <= to; ++i)
+        if (blocks_meet(steps + 1, n - 1, offset + i * steps->stride, first, second))
             return true;
     return false;
 }
 
-bool rows_meet(std::initializer_list<Step> steps, int64_t offset, int64_t inner)
+// Whether a row of one set may meet one of the other, both of `inner` elements: not where a reading of the strides
+// shows them apart. Strides that differ are read as blocks as long as the dimension reaches, or as all places that the
+// two can come to.
+bool rows_meet(std::initializer_list<std::pair<Dim, Dim>> dims, int64_t offset, int64_t inner)
 {
-    Step s[3];
-    const int n = (int)(std::copy(steps.begin(), steps.end(), s) - s);
-    std::sort(s, s + n, [](const Step &a, const Step &b) { return a.stride > b.stride; });
-    return rows_meet(s, n, offset, inner);
+    for (const bool blocks : {true, false}) {
+        Step steps[3];
+        int n = 0;
+        int64_t first = inner, second = inner, more, and_more;
+        for (const auto &[a, b] : dims) {
+            const int64_t s = a.size > 1 ? a.stride : 0, t = b.size > 1 ? b.stride : 0;
+            if (s == 0 && t == 0)
+                continue;
+            if (s == 0 || t == 0 || s == t) {
+                steps[n++] = Step{std::max(s, t), s ? 1 - a.size : 0, t ? b.size - 1 : 0};
+            } else if (!blocks) {
+                steps[n++] = Step{std::gcd(s, t), -((int64_t)1 << 40), (int64_t)1 << 40};
+            } else {
+                if (__builtin_mul_overflow(a.size - 1, s, &more) || __builtin_mul_overflow(b.size - 1, t, &and_more) ||
+                    more > kFar || and_more > kFar)
+                    return true;
+                first = std::min(first + more, kFar);
+                second = std::min(second + and_more, kFar);
+            }
+        }
+        std::sort(steps, steps + n, [](const Step &a, const Step &b) { return a.stride > b.stride; });
+        if (!blocks_meet(steps, n, offset, first, second))
+            return false;
+    }
+    return true;
 }
 
 int check_head_dim(int64_t D)
@@ -385,14 +399,24 @@ dg_status dg_fp8_rope_cache_write(const void *Q, int64_t q_stride_t, int64_t q_s
             if (overlaps(outs[i], ins[j]) && !(i == 4 && in_place && j < 3))
                 return DG_ERR_ALIASING;
     const auto among_queries = [&](const void *X, int64_t x_t, int64_t x_h) {
-        return rows_meet({step({T, q_stride_t}, {T, x_t}), step({q_heads, q_stride_h}, {heads, x_h})},
+        return rows_meet({{{T, q_stride_t}, {T, x_t}}, {{q_heads, q_stride_h}, {heads, x_h}}},
                          ((const uint8_t *)X - (const uint8_t *)Q) / size, D);
     };
     if (in_place && ((overlaps(outs[4], ins[1]) && among_queries(K, k_stride_t, k_stride_h)) ||
                      (overlaps(outs[4], ins[2]) && among_queries(V, v_stride_t, v_stride_h))))
         return DG_ERR_ALIASING;
-    // The two caches may be halves of one tensor, page by page or row by row; codes and scales lie apart.
-    if (kc.codes == vc.codes || kc.scales == vc.scales)
+    // The two caches may be halves of one tensor, page by page or row by row, with no row in both; codes and scales lie
+    // apart.
+    if ((overlaps(outs[0], outs[1]) &&
+         rows_meet({{{kc.pages, kc.stride_page}, {vc.pages, vc.stride_page}},
+                    {{kc.page_size, kc.stride_token}, {vc.page_size, vc.stride_token}},
+                    {{heads, kc.stride_head}, {heads, vc.stride_head}}},
+                   (const uint8_t *)vc.codes - (const uint8_t *)kc.codes, D)) ||
+        (overlaps(outs[2], outs[3]) &&
+         rows_meet({{{kc.pages, kc.s_stride_page}, {vc.pages, vc.s_stride_page}},
+                    {{kc.page_size, kc.s_stride_token}, {vc.page_size, vc.s_stride_token}},
+                    {{heads, kc.s_stride_head}, {heads, vc.s_stride_head}}},
+                   vc.scales - kc.scales, 1)))
         return DG_ERR_ALIASING;
     for (int i = 0; i < 2; ++i)
         for (int j = 2; j < 4; ++j)

@@ -609,7 +609,8 @@ int64_t dg_fp8_moe_layer_workspace_bytes(int64_t T, int64_t top_k, int64_t H, in
  * and at most 2^40, codes of a head spanning less than 64 GiB
  * (DG_ERR_UNSUPPORTED above). Any order of the dimensions is fine (heads before
  * tokens, keys and values as halves of each page). A cache that is written has
- * rows and scales that lie apart in some nesting of the strides.
+ * rows and scales that lie apart in some nesting of the strides, and apart from
+ * those of the other cache that the call writes.
  */
 typedef struct dg_fp8_cache {
     void *codes;

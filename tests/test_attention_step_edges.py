@@ -2,7 +2,7 @@
 the host, none of these calls reaches a device."""
 import pytest
 
-from tests.test_attention_step_abi import ALIASING, D, GOT_TO_THE_DEVICE, HEADS, K, Q, V, write
+from tests.test_attention_step_abi import ALIASING, D, GOT_TO_THE_DEVICE, HEADS, K, KC, KS, PAGE, Q, V, write
 
 # (64 tokens, 4 query heads and 2 key heads of 128 elements of 2 bytes)
 IN_PLACE = dict(QO=Q, q_t=1024, qo_t=1024)
@@ -33,3 +33,34 @@ def test_write_in_place_accepted():
                     q_h=3 * 64 * D, qo_h=3 * 64 * D, q_heads=HEADS),
                dict(K=Q + 4 * 2 * D, V=Q + 6 * 2 * D, T=1), dict(K=Q + 1024 * 2 * 64, k_t=1024), dict(K=K, V=V)):
         assert write(**{**IN_PLACE, **kw}) in GOT_TO_THE_DEVICE
+
+
+# A cache [8, 16, 2, 128] of codes and [8, 16, 2] of scales: strides of a page, a token and a head.
+P, PS = PAGE * HEADS * D, PAGE * HEADS
+
+
+@pytest.mark.parametrize("vc", [
+    dict(codes=KC + 16), dict(codes=KC - 16), dict(codes=KC + D), dict(codes=KC + HEADS * D), dict(codes=KC + P),
+    dict(codes=KC - 7 * P), dict(codes=KC + 7 * P + 15 * HEADS * D + D), dict(scales=KS + 4), dict(scales=KS - 4),
+    dict(scales=KS + 4 * HEADS), dict(scales=KS + 4 * PS), dict(scales=KS + 4 * (8 * PS - 1)),
+    dict(codes=KC + P, stride_page=2 * P), dict(codes=KC + D, stride_token=2 * HEADS * D, stride_page=2 * P),
+    dict(codes=KC + 16, stride_head=PAGE * D, stride_token=D)])
+def test_write_refuses_caches_among_each_other(vc):
+    assert write(vc=vc) == ALIASING
+
+
+def test_write_accepts_halves_of_one_tensor():
+    pages = dict(stride_page=2 * P, s_stride_page=2 * PS)
+    rows = dict(stride_page=2 * P, stride_token=2 * HEADS * D, s_stride_page=2 * PS, s_stride_token=2 * HEADS)
+    heads = dict(rows, stride_head=2 * D, s_stride_head=2)
+    first = dict(stride_head=PAGE * D, stride_token=D, s_stride_head=PAGE, s_stride_token=1)    # heads before tokens
+    for strides, codes, scales in ((pages, P, PS), (rows, HEADS * D, HEADS), (heads, D, 1), ({}, 8 * P, 8 * PS),
+                                   (pages, 5 * P, 5 * PS), (rows, 7 * HEADS * D, 7 * HEADS),
+                                   (dict(first, **pages), P, PS),
+                                   (dict(first, stride_page=2 * P, stride_head=2 * PAGE * D, s_stride_page=2 * PS,
+                                         s_stride_head=2 * PAGE), PAGE * D, PAGE)):
+        for sign in (1, -1):
+            vc = dict(codes=KC + sign * codes, scales=KS + sign * 4 * scales)
+            assert write(kc=strides, vc=dict(strides, **vc)) in GOT_TO_THE_DEVICE
+    # keys with tokens before heads, values with heads before tokens
+    assert write(kc=pages, vc=dict(first, **pages, codes=KC + P, scales=KS + 4 * PS)) in GOT_TO_THE_DEVICE
