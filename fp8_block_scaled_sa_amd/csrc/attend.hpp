@@ -107,7 +107,7 @@ struct AttendParams {
     float scale_log2;                    // scale / ln 2
     int few_rows;                        // sequences of up to so many rows are the few-rows kernel's
     int target, min_units;               // few rows: workgroups aimed at, and units that one takes at least
-    int most_pieces;                     // many rows: workgroups up to which tiles may be cut (0: not at all)
+    int most_pieces;                     // many rows: workgroups up to which tiles may be cut
     Parts few, many;                     // partial results of the two kernels
     int few_joined;                      // workgroups of the joining launch that join the first kernel's,
     int row_a_wave;                      // and whether each of their waves joins a row
@@ -901,8 +901,6 @@ __device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
         pieces += c.tiles;
         most = max(most, c.keys);
     }
-    if (p.most_pieces == 0)
-        return 0.0f;
     const float cost = 0.03f * (float)p.many.rows / kTileRows, heads = (float)p.heads;
     float best = 0.0f;
     if (p.B == 1) {
@@ -951,7 +949,12 @@ __device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
 __device__ __forceinline__ bool find_tile(const AttendParams &p, int block, Tile &w)
 {
     Cuts c;
-    const float rate = cut_tiles(p, c);
+    float rate = 0.0f;
+    // Tiles are cut into up to most_pieces pieces; behind them lie uncut ones, or nothing.
+    if (block < p.most_pieces)
+        rate = cut_tiles(p, c);
+    else
+        lane_tiles(p, threadIdx.x & 63, c);
     int before = 0;
     for (int b0 = 0; b0 < p.B; b0 += 64) {
         if (b0)
@@ -1001,7 +1004,7 @@ __device__ __forceinline__ bool find_cut_tile(const AttendParams &p, float rate,
             w.head = at - tile * p.heads;
             w.first = (lane_int(c.tiles, l) - 1 - tile) * kTileRows;
             w.slot = lane_int(upto - all, l) + tile * w.pieces * p.heads + w.head;
-            return true;
+            return w.slot >= 0 && w.slot + (w.pieces - 1) * p.heads < p.most_pieces;
         }
         tiles_before = lane_int(tiles_upto, 63);
         pieces_before = lane_int(upto, 63);

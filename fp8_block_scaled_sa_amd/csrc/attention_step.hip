@@ -234,8 +234,7 @@ struct AttendPlan {
     int64_t part_rows;     // rows of a piece's partial result
     int tile_rows;         // of the many-rows kernel (0: there cannot be sequences of more rows)
     int64_t many_tiles;    // their tiles, of all key heads, at most
-    int64_t most_pieces;   // of cut tiles (0: none is)
-    int64_t many_rows;
+    int64_t many_rows;     // rows of a cut tile's partial result
     int64_t bytes;         // of the workspace
     int64_t most_bytes;    // of the workspace of any call with at most these sizes
 };
@@ -248,10 +247,11 @@ constexpr int kFewMinUnits = 1;
 // Rows from which on each wave of the joining launch takes one by itself; below, the four of a workgroup share it (one
 // token over 4000: 10.4 us, 12.4 with a wave a row; 4096 rows: 59 us, 56 with a wave a row).
 constexpr int64_t kRowAWave = 2048;
-// Workgroups up to which the many-rows kernel's tiles are cut, three rounds of one a CU, and tiles from which on none
-// is: sixteen rounds, of which a cut could fill up the last one only, and no joining launch.
+// Workgroups up to which the many-rows kernel's tiles are cut, three rounds of one a CU. How many tiles there are, and
+// whether they are cut, is found on the device: the host knows sizes for which there can be thousands (500 single tokens
+// and a chunk of 64, 8 heads of 8: 2248) where there are few (16): 100 tokens each and the chunk's 32768 take 1087 us
+// uncut, 348 us cut.
 constexpr int64_t kMostPieces = 768;
-constexpr int64_t kUncutTiles = 4096;
 
 AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64_t D, int64_t max_q_len)
 {
@@ -270,11 +270,11 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
     a.most_bytes = (kFewTarget + B * heads) * std::min<int64_t>(dga::kFewRows, rows) * (D + 2) * 4;
     if (many) {
         a.tile_rows = dga::kTileRows;
-        a.many_tiles = (T * group + std::min(B, T) * (a.tile_rows - 1)) / a.tile_rows * heads;
-        // Where there can be so many tiles, none is cut.
-        a.most_pieces = a.many_tiles < kUncutTiles ? kMostPieces : 0;
+        // Sequences that have tiles have more rows than the few-rows kernel's.
+        const int64_t sequences = std::min(std::min(B, T), T * group / (a.few_rows + 1));
+        a.many_tiles = (T * group + sequences * (a.tile_rows - 1)) / a.tile_rows * heads;
         a.many_rows = std::min<int64_t>(a.tile_rows, rows);
-        a.bytes += a.most_pieces * a.many_rows * (D + 2) * 4;
+        a.bytes += kMostPieces * a.many_rows * (D + 2) * 4;
         a.most_bytes += kMostPieces * a.many_rows * (D + 2) * 4;
     }
     return a;
@@ -326,13 +326,13 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
         }
     }
     if (a.tile_rows) {
-        p.most_pieces = (int)a.most_pieces;
-        p.many = dga::Parts{(int)a.many_rows, parts, parts + a.most_pieces * a.many_rows * D};
-        hipLaunchKernelGGL((dga::attend_many_kernel<D>), dim3((unsigned)std::max(a.many_tiles, a.most_pieces)),
+        p.most_pieces = (int)kMostPieces;
+        p.many = dga::Parts{(int)a.many_rows, parts, parts + kMostPieces * a.many_rows * D};
+        hipLaunchKernelGGL((dga::attend_many_kernel<D>), dim3((unsigned)std::max(a.many_tiles, kMostPieces)),
                            dim3(dga::kManyThreads), 0, stream, p);
         if ((st = launched()) != DG_OK)
             return st;
-        joined += std::min<int64_t>(dga::kJoinGroups, std::min(a.many_tiles, a.most_pieces / 2) *
+        joined += std::min<int64_t>(dga::kJoinGroups, std::min(a.many_tiles, kMostPieces / 2) *
                                                           ((a.many_rows + dga::kJoinRows - 1) / dga::kJoinRows));
     }
     if (joined) {

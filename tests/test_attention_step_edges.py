@@ -2,7 +2,8 @@
 the host, none of these calls reaches a device."""
 import pytest
 
-from tests.test_attention_step_abi import ALIASING, D, GOT_TO_THE_DEVICE, HEADS, K, KC, KS, PAGE, Q, V, write
+from tests.test_attention_step_abi import (ALIASING, D, GOT_TO_THE_DEVICE, HEADS, K, KC, KS, PAGE, Q, SCRATCH, V, attend, write,
+                                            ws_bytes)
 
 # (64 tokens, 4 query heads and 2 key heads of 128 elements of 2 bytes)
 IN_PLACE = dict(QO=Q, q_t=1024, qo_t=1024)
@@ -64,3 +65,30 @@ def test_write_accepts_halves_of_one_tensor():
             assert write(kc=strides, vc=dict(strides, **vc)) in GOT_TO_THE_DEVICE
     # keys with tokens before heads, values with heads before tokens
     assert write(kc=pages, vc=dict(first, **pages, codes=KC + P, scales=KS + 4 * PS)) in GOT_TO_THE_DEVICE
+
+
+# ---------------------------------------------------------------- attention's workspace
+
+def needed(**kw):
+    """Workspace bytes that an attention call needs: with fewer it is refused for them, with as many for its output in
+    the queries' place."""
+    low, high = -1, ws_bytes(**kw)
+    strides = dict(q_t=kw["q_heads"] * D, o_t=kw["q_heads"] * D, out=Q)
+    sizes = dict(T=kw["T"], B=kw["B"], q_heads=kw["q_heads"], longest=kw["longest"],
+                 kc=dict(heads=kw["heads"]), vc=dict(heads=kw["heads"]))
+    assert attend(**sizes, **strides, ws_bytes=high) == ALIASING
+    while high - low > 1:
+        mid = (low + high) // 2
+        status = attend(**sizes, **strides, ws_bytes=mid)
+        assert status in (SCRATCH, ALIASING)
+        low, high = (mid, high) if status == SCRATCH else (low, mid)
+    return high
+
+
+@pytest.mark.parametrize("singles", [1, 100, 500, 5000])
+def test_chunks_are_cut_beside_any_number_of_single_tokens(singles):
+    """A chunk's tiles of rows can be cut, for which the workspace has room, whatever else is in the batch."""
+    alone = needed(T=64, B=1, q_heads=64, heads=8, longest=64)
+    assert alone >= 768 * 256 * (D + 2) * 4
+    others = needed(T=singles, B=singles, q_heads=64, heads=8, longest=1)
+    assert needed(T=singles + 64, B=singles + 1, q_heads=64, heads=8, longest=64) >= alone + others

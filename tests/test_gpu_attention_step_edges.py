@@ -154,3 +154,18 @@ def test_scales_of_nothing(gpu_device, lengths, heads, kv_heads, D, page):
         hold(got, *reference(b), slice(b.starts[0], b.starts[-1]))
         b.v[1][...] = small
         assert bool((b.call()[b.starts[0]:b.starts[-1]] == 0).all())
+
+
+# ---------------------------------------------------------------- large batches
+
+@pytest.mark.parametrize("window", [0, 700])
+@pytest.mark.parametrize("lengths,checked", [
+    ([(1, 30 + i % 50) for i in range(500)] + [(64, 5000)], [0, 63, 64, 499, 500]),
+    ([(64, 5000)] + [(1, 30 + i % 50) for i in range(500)], [0, 1, 64, 500]),
+    ([(1, 200), (40, 3000)] + [(1, 30 + i % 50) for i in range(700)] + [(300, 900), (1, 1)], [0, 1, 2, 64, 701, 702, 703])])
+def test_chunks_beside_hundreds_of_single_tokens(gpu_device, lengths, checked, window):
+    b = Batch(lengths, 64, 8, 64, 16, 41)
+    got = b.call(window=window)
+    for i in checked:
+        b.lengths = [(m if j == i else 0, n) for j, (m, n) in enumerate(lengths)]
+        hold(got, *reference(b, window), slice(b.starts[i], b.starts[i] + lengths[i][0]))
