@@ -15,9 +15,13 @@ import math
 import pytest
 import torch
 
-from tests.test_gpu_attention_step import BF16, F64, MIXES, Batch, half, values
+from fp8_block_scaled_sa_amd import DGError
+from tests.gpu_util import guards_intact, sentinel_bf16
+from tests.test_gpu_attention_step import BF16, F64, KINDS, MIXES, Batch, half, values
 
 pytestmark = pytest.mark.gpu
+
+ALIASING, SCRATCH = 7, 8
 
 
 def reference(b, window=0):
@@ -169,3 +173,69 @@ def test_chunks_beside_hundreds_of_single_tokens(gpu_device, lengths, checked, w
     for i in checked:
         b.lengths = [(m if j == i else 0, n) for j, (m, n) in enumerate(lengths)]
         hold(got, *reference(b, window), slice(b.starts[i], b.starts[i] + lengths[i][0]))
+
+
+@pytest.mark.parametrize("lengths", [[(2100, 2100)], [(700, 700), (1400, 1500), (1, 40)]])
+def test_thousands_of_tiles(gpu_device, lengths):
+    """64 key heads of 8 query heads each: more than 4096 tiles of 256 rows."""
+    b = Batch(lengths, 512, 64, 64, 16, 42)
+    got = b.call()
+    hold(got, *reference(b), slice(b.starts[0], b.starts[-1]))
+    b.ws.fill_(0xFF)
+    assert torch.equal(b.call(), got)
+
+
+# ---------------------------------------------------------------- workspace
+
+def needed(b):
+    """Bytes of workspace without which a Batch's call is refused: with them it is refused for its output in the
+    queries' place."""
+    def status(n):
+        with pytest.raises(DGError) as e:
+            b.call(out=b.q, ws=b.ws[:n])
+        return e.value.status
+    low, high = 0, b.ws.numel()
+    assert status(low) == SCRATCH and status(high) == ALIASING
+    while high - low > 1:
+        mid = (low + high) // 2
+        low, high = (mid, high) if status(mid) == SCRATCH else (low, mid)
+    return high
+
+
+def guarded(b):
+    """The workspace as just the bytes that the call needs, and a check that what lies around them is as it was."""
+    n = needed(b)
+    buf = torch.full((n + 2 * 65536,), 0xA5, dtype=torch.uint8, device="cuda")
+    b.ws = buf[65536:65536 + n]
+
+    def intact():
+        torch.cuda.synchronize()
+        return bool((buf[:65536] == 0xA5).all()) and bool((buf[65536 + n:] == 0xA5).all())
+    return intact
+
+
+@pytest.mark.parametrize("lengths,heads,kv_heads,D", list(KINDS.values()) + [
+    ([(1, 100 + i) for i in range(131)], 8, 8, 64), ([(1, 16000)], 32, 1, 128), ([(16, 5000)] * 3, 4, 2, 64),
+    ([(33, 9000)], 2, 2, 128), ([(40, 900 + 11 * i) for i in range(70)] + [(1, 300)] * 9, 2, 1, 64)])
+def test_workspace_of_just_the_bytes_that_a_call_needs(gpu_device, lengths, heads, kv_heads, D):
+    b = Batch(lengths, heads, kv_heads, D, 16, 43)
+    want = b.call()
+    intact = guarded(b)
+    for _ in range(3):
+        assert torch.equal(b.call(), want) and intact()
+
+
+@pytest.mark.parametrize("lengths", [[(1, 100), (1, 40), (1, 7)], [(70, 100), (1, 40), (90, 90)], [(300, 3000)],
+                                     [(1, 50)] * 70 + [(40, 2000)]])
+def test_workspace_whatever_the_lengths(gpu_device, lengths):
+    """Lengths and starts out of range and out of order write nothing beside the workspace and the output."""
+    b = Batch(lengths, 8, 2, 128, 16, 44)
+    intact = guarded(b)
+    T, n = b.q.shape[0], len(lengths)
+    for lens in ([2 ** 31 - 1] * n, [-1, -2 ** 31, 5] * n, [1 << 20, 0, 33] * n):
+        for starts in (b.starts, [0, T] * n, [0, 2 ** 31 - 1, -5, T] * n, [-2 ** 31, 0, T, T + 1] * n, [T, 0, T, 0] * n):
+            b.kv_lens = torch.tensor(lens[:n], dtype=torch.int32, device="cuda")
+            b.q_starts = torch.tensor(starts[:n + 1], dtype=torch.int32, device="cuda")
+            out = sentinel_bf16(b.q.shape)
+            b.call(out=out)
+            assert intact() and guards_intact(out)
