@@ -15,9 +15,10 @@ import math
 import pytest
 import torch
 
-from fp8_block_scaled_sa_amd import DGError
+from fp8_block_scaled_sa_amd import DGError, ops
 from tests.gpu_util import guards_intact, sentinel_bf16
-from tests.test_gpu_attention_step import BF16, F64, KINDS, MIXES, Batch, half, values
+from tests.test_gpu_attention_step import BF16, F32, F64, KINDS, MIXES, Batch, half, make_cache, normal, same, values
+from tests.test_gpu_debug_build import both, debug_lib  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -239,3 +240,21 @@ def test_workspace_whatever_the_lengths(gpu_device, lengths):
             out = sentinel_bf16(b.q.shape)
             b.call(out=out)
             assert intact() and guards_intact(out)
+
+
+@pytest.mark.parametrize("T,D,dtype,interleaved", [(1, 128, BF16, False), (61, 64, F32, True), (700, 128, BF16, False),
+                                                   (700, 128, F32, False), (300, 64, BF16, True)])
+def test_write_release_equals_O1_in_every_output(gpu_device, debug_lib, T, D, dtype, interleaved):  # noqa: F811
+    """Turned queries, the keys' codes and scales and the values', bit for bit."""
+    Hq, H = 8, 2
+    q, k, v = normal((T, Hq + 2 * H, D), 1).to(dtype).split([Hq, H, H], 1)
+    slots = torch.randperm(1024, device="cuda")[:T]
+    freqs, _ = ops.dg_rope_frequencies(D)
+
+    def run():
+        c = [*make_cache(64, 16, H, D, 1), *make_cache(64, 16, H, D, 2)]
+        out = ops.dg_fp8_rope_cache_write(k, v, *c, slots, (7919 * slots).int(), freqs, q=q, interleaved=interleaved)
+        torch.cuda.synchronize()
+        return [out, *c]
+    rel, dbg = both(debug_lib, run)
+    assert all(same(a, b) for a, b in zip(rel, dbg))
