@@ -684,8 +684,8 @@ dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
  *   x_j = scale * q . k_j     for the keys j <= p, and j > p - window if window > 0
  *   out = bf16( sum_j exp(x_j) v_j / sum_j exp(x_j) )
  * A row that sees no key (p < 0, or no page) is 0. Keys in pages outside [0,
- * pages), and past the table's width, are not seen: pages that every window has
- * left may be given back, with -1 in the table. What a row does not see never
+ * pages) are not seen: pages that every window has left may be given back, with
+ * -1 in the table. What a row does not see never
  * counts, whatever the cache holds there; a NaN code in a value that it sees
  * makes it NaN in that column, or in all of them, a scale that is not finite in
  * all of them.
@@ -698,8 +698,9 @@ dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
  *   workspace  of dg_fp8_paged_attention_workspace_bytes bytes or more for
  *   these sizes or larger ones (DG_ERR_SCRATCH below what the call needs),
  *   16-byte aligned, contents arbitrary; calls that share one must be ordered
- * Values out of range in kv_lens and q_starts are clamped to what the table and
- * Q hold (no fault). The first product is one of exact bf16 values with fp32
+ * Values out of range do no harm: kv_lens count as the nearest number from 0 to
+ * table_width * page_size (a longer sequence ends where its table does, its new
+ * tokens there), q_starts as the nearest from 0 to T. The first product is one of exact bf16 values with fp32
  * sums; the second one takes its weights, exp(x_j) times the value's scale,
  * rounded to 11 bits, those below 2^-21 of the row's largest to 2^-32 of it; the
  * rest is fp32 up to the rounding of out. Scales of values below 2^-100 in
