@@ -621,7 +621,9 @@ def dg_rope_frequencies(rot, base=10000.0, scaling=None, stretch=1.0, original=4
                 divided by stretch, the fastest left)
       "parts"   pairs that turn less than `slow` times over the original context
                 divided by stretch, those that turn more than `fast` times left,
-                linear in the turns between; factor 0.1 ln(stretch) + 1.
+                linear in the turns between; factor 0.1 ln(stretch) + 1. (Models
+                whose pairs between are linear in the pair's number, often with
+                rounded ends, have other frequencies there: give theirs.)
     Returns (freqs, factor)."""
     if rot <= 0 or rot % 2:
         raise ValueError("rot must be even and positive")
