@@ -74,6 +74,7 @@ constexpr float kTopWeight = 7.0f;       // log2 of a row's largest weight when 
 constexpr float kMostWeight = 0x1p15f;   // how far a weight may go before the reference moves (fp16 ends at 65504)
 constexpr float kUnset = -1.0f;          // limit of a row whose reference has not been set
 constexpr float kLeastScale = 0x1p-100f; // of values; what lies below counts as 0
+constexpr float kSumUnit = 0x1p-20f;     // in which exponentials are summed: 2^30 of up to 2^115 stay in fp32's range
 
 // One of the two caches: rows of 16-byte multiples, addressed in units of 16 bytes.
 struct Rows {
@@ -88,7 +89,7 @@ struct Rows {
 struct Parts {
     int rows;                            // of a piece
     float *o;                            // [piece][rows][D], sums over p sV V
-    float *ml;                           // [piece][rows][2], reference and sum of p
+    float *ml;                           // [piece][rows][2], reference and sum of p in kSumUnit
 };
 
 struct AttendParams {
@@ -641,7 +642,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 limit[nt] = moves ? kMostWeight : limit[nt];
                 weigh();
             }
-            sum[nt] += part;
+            sum[nt] = __builtin_fmaf(part, kSumUnit, sum[nt]);
         }
 
         // O^T += V^T P^T
@@ -736,7 +737,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
 #pragma unroll
                 for (int t = 0; t < DT; ++t)
-                    y[t] = total == 0.0f ? 0.0f : y[t] / total;
+                    y[t] = total == 0.0f ? 0.0f : y[t] * kSumUnit / total;
                 store_bf16<DT>(p.out + (int64_t)(w.s.start + token) * p.o_t +
                                    (int64_t)(w.head * (int)p.group.d + h) * p.o_h + col, y);
             } else {
@@ -789,7 +790,7 @@ __device__ __forceinline__ void store_row(uint16_t *to, float total, const float
     float v[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        v[e] = total == 0.0f ? 0.0f : y[e] / total;
+        v[e] = total == 0.0f ? 0.0f : y[e] * kSumUnit / total;
     to += E * (threadIdx.x & 63);
     if (E == 2)
         *(uint32_t *)to = dgn::pack_bf16(v[0], v[1]);
@@ -1433,7 +1434,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                 limit = moves ? kMostWeight : limit;
                 weigh();
             }
-            sum += part;
+            sum = __builtin_fmaf(part, kSumUnit, sum);
 #pragma unroll
             for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -1464,7 +1465,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
         if (w.pieces == 1) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                y[e] = sum == 0.0f ? 0.0f : y[e] / sum;
+                y[e] = sum == 0.0f ? 0.0f : y[e] * kSumUnit / sum;
             store_bf16<E>(to + element, y);
         } else {
 #pragma unroll

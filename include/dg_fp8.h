@@ -685,10 +685,9 @@ dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
  *   out = bf16( sum_j exp(x_j) v_j / sum_j exp(x_j) )
  * A row that sees no key (p < 0, or no page) is 0. Keys in pages outside [0,
  * pages) are not seen: pages that every window has left may be given back, with
- * -1 in the table. What a row does not see never
- * counts, whatever the cache holds there; a NaN code in a value that it sees
- * makes it NaN in that column, or in all of them, a scale that is not finite in
- * all of them.
+ * -1 in the table. What a row does not see never counts, whatever the cache
+ * holds there; a NaN code in a value that it sees makes it NaN in that column, or
+ * in all of them, a scale that is not finite in all of them.
  *   Q, out  bf16 [T, q_heads, head_dim], strides of tokens and heads
  *   block_table [B, table_width] int32, row stride table_stride
  *   kv_lens [B], q_starts [B + 1] int32, ascending (all three device memory: no
@@ -700,15 +699,14 @@ dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
  *   16-byte aligned, contents arbitrary; calls that share one must be ordered
  * Values out of range do no harm: kv_lens count as the nearest number from 0 to
  * table_width * page_size (a longer sequence ends where its table does, its new
- * tokens there), q_starts as the nearest from 0 to T. The first product is one of exact bf16 values with fp32
- * sums; the second one takes its weights, exp(x_j) times the value's scale,
- * rounded to 11 bits, those below 2^-21 of the row's largest to 2^-32 of it; the
- * rest is fp32 up to the rounding of out. Scales of values below 2^-100 in
- * magnitude count as 0 (with scales below 2^-90 alone, sums over more than 4096
- * keys may leave fp32's range and the row comes out as 0); and where the row's
- * largest weight has a scale s, keys whose exp(x_j) is below 2^-133 s of that
- * one's do not count. Deterministic: the split of the keys follows from the
- * lengths, and partial results are added in a fixed order.
+ * tokens there), q_starts as the nearest from 0 to T.
+ * The first product is one of exact bf16 values with fp32 sums; the second one
+ * takes its weights, exp(x_j) times the value's scale, rounded to 11 bits, those
+ * below 2^-21 of the row's largest to 2^-32 of it; the rest is fp32 up to the
+ * rounding of out. Scales of values below 2^-100 in magnitude count as 0; where
+ * the row's largest weight has a scale s, keys whose exp(x_j) is below 2^-133 s
+ * of that one's do not count. Deterministic: the split of the keys follows from
+ * the lengths, and partial results are added in a fixed order.
  * Constraints: q_heads % heads == 0, both caches with the same sizes, window >=
  * 0, scale finite (DG_ERR_BAD_SHAPE); table_width * page_size at most 2^30, T *
  * q_heads below 2^31, B * heads * (table_width * page_size / 128 + 2) below

@@ -258,3 +258,36 @@ def test_write_release_equals_O1_in_every_output(gpu_device, debug_lib, T, D, dt
         return [out, *c]
     rel, dbg = both(debug_lib, run)
     assert all(same(a, b) for a, b in zip(rel, dbg))
+
+
+# ---------------------------------------------------------------- long sequences
+
+@pytest.mark.parametrize("m,n", [(300, 1 << 21), (1, 1 << 21), (300, 40000)])
+def test_a_long_run_of_zeros(gpu_device, m, n):
+    """Values that are zeros but for 100 rows near the end, scores that fall by 7.9 powers of two for 32 keys of each 64:
+    as much as exponentials and their sum can grow without a move of the reference. All rows and keys of a kind alike, so
+    the outputs are ratios of counts; they are off as above, where n keys' sums are off by n 2^-24 each."""
+    heads, D, page = 8, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    pages = -(-n // page)
+    q = torch.ones((m, heads, D), dtype=BF16, device="cuda")
+    k = torch.full((pages, page, 1, D), 0x38, dtype=torch.uint8, device="cuda")            # 1.0
+    v = torch.zeros_like(k)
+    j = torch.arange(pages * page, device="cuda")
+    low = j // 32 % 2 == 0
+    ks = torch.where(low, -7.9 * math.log(2) / D ** 0.5, 0.0).view(pages, page, 1).float()
+    some = (j >= n - m - 100) & (j < n - m)
+    v.view(-1, D)[some] = 0x38
+    vs = torch.where(some, 0.75, 1.0).view(pages, page, 1)
+    table = torch.randperm(pages, generator=g, device="cuda").int()
+    at = torch.empty_like(table).long()
+    at[table.long()] = torch.arange(pages, device="cuda")
+    k, v, ks, vs = (t[at].contiguous() for t in (k, v, ks, vs))
+    ws = ops.workspace(ops.dg_fp8_paged_attention_workspace_bytes(m, 1, heads, 1, D, m))
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+    got = ops.dg_fp8_paged_attention(q, k, ks, v, vs, table[None], lens, starts, m, ws)
+    p = torch.where(low, 2.0 ** -7.9, 1.0).double()[:n]
+    want = 0.75 * (p * some[:n]).sum() / p.cumsum(0)[n - m:]
+    off = (got.double() - want[:, None, None]).abs()
+    assert bool((off <= (half(BF16) + 2.0 ** -9 + 2.0 ** -19 + n * 2.0 ** -23) * want[:, None, None]).all())
