@@ -107,7 +107,7 @@ struct AttendParams {
     Divisor group;                       // query heads of a key head
     float scale_log2;                    // scale / ln 2
     int few_rows;                        // sequences of up to so many rows are the few-rows kernel's
-    int target, min_units;               // few rows: workgroups aimed at, and units that one takes at least
+    int target;                          // few rows: workgroups aimed at
     int most_pieces;                     // many rows: workgroups up to which tiles may be cut
     Parts few, many;                     // partial results of the two kernels
     int few_joined;                      // workgroups of the joining launch that join the first kernel's,
@@ -301,7 +301,7 @@ __device__ __forceinline__ int chunk_of(const AttendParams &p, Cut &c)
         all += max(0, lane_units(p, b0 + lane, s));
     }
     all = lane_int(scan(all), 63) * p.heads;
-    return max(p.min_units, (all + p.target - 1) / p.target);
+    return max(1, (all + p.target - 1) / p.target);
 }
 
 // Cuts the sequences from b0 on; returns the pieces up to and with them.

@@ -232,7 +232,7 @@ struct AttendPlan {
     int few_rows;          // rows up to which a sequence is its
     int64_t pieces;        // its workgroups at most, which is what its partial results take
     int64_t part_rows;     // rows of a piece's partial result
-    int tile_rows;         // of the many-rows kernel (0: there cannot be sequences of more rows)
+    bool many;             // whether there can be sequences of more rows, the many-rows kernel's
     int64_t many_tiles;    // their tiles, of all key heads, at most
     int64_t many_rows;     // rows of a cut tile's partial result
     int64_t bytes;         // of the workspace
@@ -243,7 +243,6 @@ struct AttendPlan {
 // sequences up to 16384 tokens and 16 of 4 tokens up to 8192: 251 and 55 us with 512, 227 and 56 with 1024, 225 and 64
 // with 2048.)
 constexpr int kFewTarget = 1024;
-constexpr int kFewMinUnits = 1;
 // Rows from which on each wave of the joining launch takes one by itself; below, the four of a workgroup share it (one
 // token over 4000: 10.4 us, 12.4 with a wave a row; 4096 rows: 59 us, 56 with a wave a row).
 constexpr int64_t kRowAWave = 2048;
@@ -257,7 +256,7 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
 {
     AttendPlan a = {};
     const int64_t longest = std::min(max_q_len, T), rows = longest * group;
-    const bool many = rows > dga::kFewRows;
+    const bool many = a.many = rows > dga::kFewRows;
     // Beside chunks, the few-rows kernel is for the sequences with a single token; one sequence alone takes one kernel.
     const int64_t few = !many ? rows : B > 1 && group <= dga::kFewRows ? group : 0;
     a.tiles = few == 0 ? 0 : few <= 16 ? 1 : 2;
@@ -269,11 +268,10 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
     }
     a.most_bytes = (kFewTarget + B * heads) * std::min<int64_t>(dga::kFewRows, rows) * (D + 2) * 4;
     if (many) {
-        a.tile_rows = dga::kTileRows;
         // Sequences that have tiles have more rows than the few-rows kernel's.
         const int64_t sequences = std::min(std::min(B, T), T * group / (a.few_rows + 1));
-        a.many_tiles = (T * group + sequences * (a.tile_rows - 1)) / a.tile_rows * heads;
-        a.many_rows = std::min<int64_t>(a.tile_rows, rows);
+        a.many_tiles = (T * group + sequences * (dga::kTileRows - 1)) / dga::kTileRows * heads;
+        a.many_rows = std::min<int64_t>(dga::kTileRows, rows);
         a.bytes += kMostPieces * a.many_rows * (D + 2) * 4;
         a.most_bytes += kMostPieces * a.many_rows * (D + 2) * 4;
     }
@@ -308,24 +306,23 @@ int launch_attend(dga::AttendParams &p, const AttendPlan &a, int64_t units, hipS
     float *parts = p.few.o;
     if (a.tiles) {
         p.target = kFewTarget;
-        p.min_units = kFewMinUnits;
         p.few = dga::Parts{(int)a.part_rows, parts, parts + a.pieces * a.part_rows * D};
         parts += a.pieces * a.part_rows * (D + 2);
-        const int64_t most = (units + kFewMinUnits - 1) / kFewMinUnits;    // pieces of a sequence and head at most
-        const dim3 grid((unsigned)std::min<int64_t>(a.pieces, p.B * p.heads * std::max<int64_t>(most, 1)));
+        // A sequence and head has a piece for each unit at most.
+        const dim3 grid((unsigned)std::min<int64_t>(a.pieces, p.B * p.heads * std::max<int64_t>(units, 1)));
         if (a.tiles == 1)
             hipLaunchKernelGGL((dga::attend_few_kernel<D, 1>), grid, threads, 0, stream, p);
         else
             hipLaunchKernelGGL((dga::attend_few_kernel<D, 2>), grid, threads, 0, stream, p);
         if ((st = launched()) != DG_OK)
             return st;
-        if (most > 1) {
+        if (units > 1) {
             joined = p.B * p.heads * a.part_rows;
             p.row_a_wave = joined >= kRowAWave;
             p.few_joined = (int)(joined = p.row_a_wave ? (joined + 3) / 4 : joined);
         }
     }
-    if (a.tile_rows) {
+    if (a.many) {
         p.most_pieces = (int)kMostPieces;
         p.many = dga::Parts{(int)a.many_rows, parts, parts + kMostPieces * a.many_rows * D};
         hipLaunchKernelGGL((dga::attend_many_kernel<D>), dim3((unsigned)std::max(a.many_tiles, kMostPieces)),
