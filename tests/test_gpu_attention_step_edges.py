@@ -176,6 +176,15 @@ def test_chunks_beside_hundreds_of_single_tokens(gpu_device, lengths, checked, w
         hold(got, *reference(b, window), slice(b.starts[i], b.starts[i] + lengths[i][0]))
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(8, 8), (4, 1), (16, 2), (28, 4), (16, 1), (17, 1), (32, 1), (33, 1)])
+def test_few_tokens_beside_a_chunk(gpu_device, heads, kv_heads):
+    """Sequences of all numbers of rows about the two tiles of the few-rows kernel, and the chunk first or last."""
+    few = [(m, 100 + 37 * m) for m in (1, 2, 3, 4, 5, 8, 9, 15, 16, 17, 31, 32, 33)]
+    for lengths in (few + [(70, 400)], [(70, 400)] + few):
+        b = Batch(lengths, heads, kv_heads, 64, 16, 45)
+        hold(b.call(), *reference(b), slice(b.starts[0], b.starts[-1]))
+
+
 @pytest.mark.parametrize("lengths", [[(2100, 2100)], [(700, 700), (1400, 1500), (1, 40)]])
 def test_thousands_of_tiles(gpu_device, lengths):
     """64 key heads of 8 query heads each: more than 4096 tiles of 256 rows."""
