@@ -248,7 +248,7 @@ constexpr int kFewTarget = 1024;
 constexpr int64_t kRowAWave = 2048;
 // Workgroups up to which the many-rows kernel's tiles are cut, three rounds of one a CU. How many tiles there are, and
 // whether they are cut, is found on the device: the host knows sizes for which there can be thousands (500 single tokens
-// and a chunk of 64, 8 heads of 8: 1224) where there are few (16): 100 tokens each and the chunk's 32768 take 1087 us
+// and a chunk of 64, 8 heads of 8: 2248) where there are few (16): 100 tokens each and the chunk's 32768 take 1087 us
 // uncut, 348 us cut.
 constexpr int64_t kMostPieces = 768;
 
@@ -259,9 +259,11 @@ AttendPlan plan_attend(int64_t T, int64_t B, int64_t heads, int64_t group, int64
     const bool many = a.many = rows > dga::kFewRows;
     // Beside chunks, the few-rows kernel has all sequences of up to 32 rows, which a tile of 256 would pay for in full
     // (16 sequences of 4 tokens up to 8192 beside a chunk of 512, 8 heads of 8: 366 us with up to 16 rows, 249 with 32;
-    // 60 of 4 up to 2000 beside 300: 141 and 91). Single tokens lose little with it (64 up to 8192 beside 512: 333 and
-    // 341; 30 beside 1000: 254 and 257). One sequence alone takes one kernel.
-    const int64_t few = !many ? rows : B > 1 && group <= dga::kFewRows ? dga::kFewRows : 0;
+    // 60 of 4 up to 2000 beside 300: 141 and 91); but where the longest leaves no more than a token for each other one,
+    // it has these alone, in its form of one tile if that holds them (64 single tokens up to 8192 beside a chunk of 512:
+    // 333 us, 341 in the form of two; 500 of 100 beside 64 over 32768: 348 and 398). One sequence alone takes one kernel.
+    const int64_t beside = T - longest < B ? group : dga::kFewRows;
+    const int64_t few = !many ? rows : B > 1 && group <= dga::kFewRows ? beside : 0;
     a.tiles = few == 0 ? 0 : few <= 16 ? 1 : 2;
     a.few_rows = 16 * a.tiles;
     if (a.tiles) {
