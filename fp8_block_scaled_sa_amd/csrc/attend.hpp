@@ -766,16 +766,24 @@ __device__ __forceinline__ void join_pieces(const Parts &parts, int count, int f
 #pragma unroll
     for (int d = 1; d < 64; d *= 2)
         top = fmaxf(top, __shfl_xor(top, d, 64));
+    // (By the lanes: as two more products for each piece in the loop below it took twice as long, 66 pieces of 256 rows
+    // 19.7 us instead of 8.6.)
     total = 0.0f;
+    for (int i = lane; i < count; i += 64)
+        if (i % waves == first) {
+            const f32x2 ml = *(const f32x2 *)(parts.ml + 2 * index(i));
+            total += scaled(ml[1], 0.5f * (ml[0] - top));
+        }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2)
+        total += __shfl_xor(total, d, 64);
 #pragma unroll
     for (int e = 0; e < E; ++e)
         y[e] = 0.0f;
 #pragma unroll 8
     for (int i = first; i < count; i += waves) {
         const int64_t at = index(i);
-        const f32x2 ml = *(const f32x2 *)(parts.ml + 2 * at);
-        const float weight = __builtin_amdgcn_exp2f(ml[0] - top);
-        total += scaled(ml[1], 0.5f * (ml[0] - top));
+        const float weight = __builtin_amdgcn_exp2f(parts.ml[2 * at] - top);
         const float *o = parts.o + at * D + E * lane;
 #pragma unroll
         for (int e = 0; e < E; ++e)
