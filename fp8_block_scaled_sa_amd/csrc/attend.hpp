@@ -221,7 +221,7 @@ __device__ __forceinline__ bool usable(float scale)
     return fabsf(scale) >= kLeastScale && fabsf(scale) < __builtin_inff();
 }
 
-// Bits of the 32 keys whose codes are all zeros; a lane holds (some elements of) the keys 16 (i / 4) + 4 (lane / 16) + i % 4.
+// Bits of the 32 keys whose codes are all zeros; a lane holds some elements of the keys 16 (i / 4) + 4 (lane / 16) + i % 4.
 template <int VW>
 __device__ __forceinline__ uint32_t rows_of_zeros(const uint32_t (&codes)[8][VW])
 {
@@ -383,12 +383,15 @@ __device__ __forceinline__ void store_bf16(uint16_t *to, const float *v)
 // (v_perm) before the conversion, which takes two codes at once.
 //
 // Two units are in flight, in registers of their own (one: 260 us for 64
-// sequences of up to 16384 tokens, 8 key heads of 8; two: 226 us, 5.1 TB/s, which
-// is the rate of a large copy). 208 registers for one tile of rows, two waves a
-// SIMD; with two tiles 256, of which the queries' would spill: they stay in LDS,
-// the same for all waves (16 sequences of 4 tokens up to 8192: 56 -> 54 us with
-// the joining launch, 62% of the copy's rate without it: a workgroup has four
-// units or so, and the first and the last are not hidden).
+// sequences of up to 16384 tokens, 8 key heads of 8; two: 226 us, 5.1 TB/s of
+// 6.6 to 7.2 that kernels which only load reach here; 512 sequences of 4096 tokens
+// 5.8 TB/s). What it reads from HBM is what it needs, 1.17 GB; matrix units and
+// VALU are busy for 7% and 37% of the time. 198 registers for one tile of rows,
+// two waves a SIMD; with two tiles 250, where the queries' would spill: they stay
+// in LDS, the same for all waves (16 sequences of 4 tokens up to 8192: 56 -> 54 us
+// with the joining launch, 62% of a copy's rate without it: a workgroup has four
+// units or so, and the first and the last are not hidden). The look for rows of
+// zeros costs a cache whose scales are all 1 a few percent (222 -> 229 us).
 template <int D, int NT>
 __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
 {
@@ -886,15 +889,19 @@ __device__ __forceinline__ int pieces_of(const Cuts &c, float rate)
 
 // How tiles are cut: the reciprocal of the tiles of keys of a piece, 0 for not at
 // all. Every workgroup comes to the same estimate from the lengths, in units of
-// the time that a workgroup takes for one tile of keys (1.8 us): pieces that fill
-// the 256 CUs at most once take as long as the longest; one sequence's, equal
-// ones, as many rounds as they fill; uneven ones their average and a part of the
-// longest. Cutting costs the joining launch's work (2), and for each piece its
-// partial result's way out and back. (16 sequences of 16 tokens, 8 heads of 8, up
-// to 8192 tokens: 370 us uncut, 197 us cut; chunks of 100 tokens over 30000 and
-// 500 over 600 in one batch: 1310 and 132; a prompt of 300 by itself, which is not
-// worth a cut: 25 without the joining launch, 28 with it. More candidates than
-// powers of two gained up to 15% for some batches and lost as much for others.)
+// the time that a workgroup takes for one tile of keys (2.1 us; 1.9 where no row
+// moves its reference): pieces that fill the 256 CUs at most once take as long as
+// the longest; one sequence's, equal ones, as many rounds as they fill; uneven
+// ones their average and a part of the longest. Cutting costs the joining launch's
+// work (2), and for each piece its partial result's way out and back. Measured,
+// 8 heads of 8, uncut and cut: 16 sequences of 16 tokens up to 8192, 366 and 150
+// us; chunks of 100 tokens over 30000 and 500 over 600 in one batch, 1330 and 221;
+// 512 tokens of 32 heads over 32768, 990 and 323; a prompt of 300 by itself, 29.5
+// and 29.8, is not worth a cut. A piece's start is more than kPieceStart says:
+// 512 tokens of 64 heads over 4096 to 32768 keys, in two pieces each, take 51 us
+// and 2.1 for each tile of a piece, 39 and 1.9 with keys that are all the same.
+// (More candidates than powers of two gained up to 15% for some batches and lost
+// as much for others.)
 __device__ __forceinline__ float cut_tiles(const AttendParams &p, Cuts &first)
 {
 #pragma clang fp contract(off)
@@ -1271,14 +1278,18 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
 // waves compute the tile before; V transposed, its keys in the order in which
 // the first product leaves them. One barrier a tile.
 //
-// Bound by the matrix units and the clock that they leave: 2048 tokens of 64
-// heads over 32768 keys take 2.03 ms, 1065 TFLOP/s of 1155 to 1317 that large
-// bf16 products reach here. The same waves bringing in and computing took 2.39 ms
-// (conversion and exponentials beside each other), sums and queries in fewer
-// registers spilled (6.45 ms). 256 rows share each conversion; 768 threads and
-// 168 registers leave room for one workgroup a CU. A short sequence pays its
-// rows' moves of the reference (an eighth of the time of 2048 tokens by
-// themselves, 90 us) and 5 us before the first tile.
+// Bound by the matrix units and the vector instructions beside them: 2048 tokens
+// of 64 heads over 32768 keys take 2.09 to 2.18 ms, 977 to 1019 TFLOP/s of 1155
+// to 1317 that large bf16 products reach here, with the matrix units busy for
+// 45% of the cycles and the VALU for 56%, at 1.9 GHz. With V times its scale in
+// fp16 on the way into LDS, and weights without it, it took 2.03 ms, but a row's
+// accuracy then hung on the scales of keys that it does not see; the scale in the
+// weights costs a product and a sum for each. The same waves bringing in and
+// computing took 2.39 ms (conversion and exponentials beside each other), sums and
+// queries in fewer registers spilled (6.45 ms). 256 rows share each conversion;
+// 768 threads and 168 registers leave room for one workgroup a CU. A short
+// sequence pays its rows' moves of the reference: a prompt of 2048 tokens by
+// itself takes 121 us, 92 with keys that are all the same.
 template <int D>
 __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendParams p)
 {
@@ -1425,7 +1436,8 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
             if (__ballot(most > limit)) {
                 const float log = __builtin_amdgcn_logf(fabsf(scale));
                 float top = -__builtin_inff();
-                for_each([&](auto i) { top = fmaxf(top, x[b][i.value] + from_lane<i.value>(log)); }, std::make_integer_sequence<int, 16>());
+                for_each([&](auto i) { top = fmaxf(top, x[b][i.value] + from_lane<i.value>(log)); },
+                         std::make_integer_sequence<int, 16>());
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
                 const int over = most > limit, other = __shfl_xor(over, 32, 64);    // of the row's other half
                 const bool moves = (over | other) != 0 && top > -__builtin_inff();
