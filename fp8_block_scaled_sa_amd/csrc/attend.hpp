@@ -21,15 +21,18 @@
 // say in how its other weights are rounded, whatever its scale. Weights below
 // fp16's normal numbers are off by 2^-25, 2^-32 of the row's largest. p takes up
 // fp32's exponents for this: with the row's largest weight on a key of scale s
-// it lies about 2^7 / s. Scales below 2^-100 count as 0, so that it stays finite,
-// and what lies below 2^-133 s of that key's p drops out.
+// it lies about 2^19 / s (sV goes into weights in units of 2^12). It is kept below
+// 2^115, so weights are rounded as beside one of the largest p and a scale of
+// 2^-96 where that is more than the row's largest; scales below 2^-114 count as 0;
+// and what lies below 2^-145 s of that key's p drops out (2^-26 at the largest
+// scale that bf16 values have).
 //
 // Masked keys never count, whatever their rows hold: their p is set to 0, scales
 // that are not finite and codes of V that are NaN there are replaced (0 * NaN
 // would be NaN). A row that sees a NaN code comes out as NaN: in that column, or
 // in all of them where the code lies in a tile that is masked for some rows; a
 // row that sees a scale that is not finite, in all of them. A row of zeros has
-// the scale 1, which says nothing about values beside it: it counts as 2^-100.
+// the scale 1, which says nothing about values beside it: it counts as 2^-114.
 //
 // Which kernel. The cache's bytes bound few rows: each key is read once, at
 // 2 D + 8 bytes, and costs 4 D operations a row, so up to some 60 rows the read
@@ -72,8 +75,12 @@ constexpr float kNoMax = -1e30f;         // reference of a row that has seen not
 constexpr float kTopWeight = 7.0f;       // log2 of a row's largest weight when its reference is set
 constexpr float kMostWeight = 0x1p15f;   // how far a weight may go before the reference moves (fp16 ends at 65504)
 constexpr float kUnset = -1.0f;          // limit of a row whose reference has not been set
-constexpr float kLeastScale = 0x1p-100f; // of values; what lies below counts as 0
-constexpr float kSumUnit = 0x1p-20f;     // in which exponentials are summed: 2^30 of up to 2^115 stay in fp32's range
+constexpr float kMostSum = 0x1p120f;     // how far a lane's exponentials of a tile may go
+constexpr float kTopExponential = 115.0f;  // log2 of a row's largest when its reference is set, at most
+constexpr float kScaleUnit = 0x1p-12f;   // of values' scales in weights
+constexpr float kLeastScale = 0x1p-114f; // of values; what lies below counts as 0
+constexpr float kSumUnit = 0x1p-20f;     // in which exponentials are summed: 2^26 times 2^120 stays in fp32's range
+constexpr float kOutUnit = kSumUnit / kScaleUnit;      // of sums of weights over those of exponentials
 
 // One of the two caches: rows of 16-byte multiples, addressed in units of 16 bytes.
 struct Rows {
@@ -87,7 +94,7 @@ struct Rows {
 // Where pieces leave their partial results.
 struct Parts {
     int rows;                            // of a piece
-    float *o;                            // [piece][rows][D], sums over p sV V
+    float *o;                            // [piece][rows][D], sums over p sV V, sV in kScaleUnit
     float *ml;                           // [piece][rows][2], reference and sum of p in kSumUnit
 };
 
@@ -239,10 +246,11 @@ __device__ __forceinline__ uint32_t rows_of_zeros(const uint32_t (&codes)[8][VW]
     return zeros;
 }
 
-// A row's move to a reference at which its largest weight is 2^kTopWeight: by how much (exactly, as x is moved too).
-__device__ __forceinline__ float move_reference(float &ref, float top)
+// A row's move to a reference at which its largest weight is 2^kTopWeight, or its largest exponential as large as it may
+// be: by how much (exactly, as x is moved too).
+__device__ __forceinline__ float move_reference(float &ref, float top_weight, float top_exponential)
 {
-    const float next = ref + (top - kTopWeight), by = next - ref;
+    const float next = ref + fmaxf(top_weight - kTopWeight, top_exponential - kTopExponential), by = next - ref;
     ref = next;
     return by;
 }
@@ -513,7 +521,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
         const bool mine = values && (there >> (lane & 31) & 1);
         const bool masked = there != 0xffffffffu || first + 31 > w.s.n - w.s.m ||
                             (p.window && first <= w.s.n - 1 - p.window) || __ballot(mine && !usable(found)) != 0;
-        scales[wave][lane] = !values ? found * p.scale_log2 : usable(found) ? found : kLeastScale;
+        scales[wave][lane] = !values ? found * p.scale_log2 : (usable(found) ? found : kLeastScale) * kScaleUnit;
         wave_sync();
         float ks[8], vs[8];
 #pragma unroll
@@ -531,7 +539,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
             const uint32_t zeros = rows_of_zeros(raw.v) >> (4 * g);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                vs[i] = (zeros >> (16 * (i / 4) + i % 4) & 1) && vs[i] == 1.0f ? kLeastScale : vs[i];
+                vs[i] = (zeros >> (16 * (i / 4) + i % 4) & 1) && vs[i] == kScaleUnit ? kLeastScale * kScaleUnit : vs[i];
         }
 
         // This lane's keys whose values are not finite: codes are replaced by zeros, and a row that sees one becomes NaN.
@@ -624,14 +632,18 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 weights[nt] = __builtin_bit_cast(f16x8, packed);
             };
             weigh();
-            if (__ballot(most > limit[nt])) {
-                float top = -__builtin_inff();
+            if (__ballot(most > limit[nt] || part > kMostSum)) {
+                float top = -__builtin_inff(), top_x = top;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 8; ++i) {
                     top = fmaxf(top, x[i] + __builtin_amdgcn_logf(fabsf(vs[i])));
+                    top_x = fmaxf(top_x, x[i]);
+                }
                 top = max_across(top);
-                const bool moves = max_across(most) > limit[nt] && top > -__builtin_inff();
-                const float by = moves ? move_reference(ref[nt], top) : 0.0f;
+                top_x = max_across(top_x);
+                const float over = most > limit[nt] || part > kMostSum ? 1.0f : 0.0f;
+                const bool moves = max_across(over) > 0.0f && top > -__builtin_inff();
+                const float by = moves ? move_reference(ref[nt], top, top_x) : 0.0f;
                 const float half = limit[nt] == kUnset ? 0.0f : -0.5f * by;
                 const float shrink = scaled(1.0f, half);
                 sum[nt] = scaled(sum[nt], half);
@@ -739,7 +751,7 @@ __global__ __launch_bounds__(kThreads, 2) void attend_few_kernel(AttendParams p)
                 const int token = (int)quotient(r, p.group), h = r - token * (int)p.group.d;
 #pragma unroll
                 for (int t = 0; t < DT; ++t)
-                    y[t] = total == 0.0f ? 0.0f : y[t] * kSumUnit / total;
+                    y[t] = total == 0.0f ? 0.0f : y[t] * kOutUnit / total;
                 store_bf16<DT>(p.out + (int64_t)(w.s.start + token) * p.o_t +
                                    (int64_t)(w.head * (int)p.group.d + h) * p.o_h + col, y);
             } else {
@@ -800,7 +812,7 @@ __device__ __forceinline__ void store_row(uint16_t *to, float total, const float
     float v[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        v[e] = total == 0.0f ? 0.0f : y[e] * kSumUnit / total;
+        v[e] = total == 0.0f ? 0.0f : y[e] * kOutUnit / total;
     to += E * (threadIdx.x & 63);
     if (E == 2)
         *(uint32_t *)to = dgn::pack_bf16(v[0], v[1]);
@@ -1236,7 +1248,7 @@ __device__ __forceinline__ void bring_v(const AttendParams &p, const Keys &k, co
             bad |= (uint32_t)__ballot(mine && !(fabsf(found) < __builtin_inff()));
         }
         if (lane < kHalf)
-            lds.vscales[t & 1][kHalf * part + lane] = scale;
+            lds.vscales[t & 1][kHalf * part + lane] = scale * kScaleUnit;
         if (lane == 0)
             lds.about[t & 1].bad[part] = bad;
         // Keys 4 x + i of each 16 go to chunk x % 2, half x / 2: the order of S^T's registers. Element (D / 16) col + i
@@ -1432,15 +1444,18 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
                 }, std::make_integer_sequence<int, 8>());
             };
             weigh();
-            if (__ballot(most > limit)) {
+            if (__ballot(most > limit || part > kMostSum)) {
                 const float log = __builtin_amdgcn_logf(fabsf(scale));
-                float top = -__builtin_inff();
-                for_each([&](auto i) { top = fmaxf(top, x[b][i.value] + from_lane<i.value>(log)); },
-                         std::make_integer_sequence<int, 16>());
+                float top = -__builtin_inff(), top_x = top;
+                for_each([&](auto i) {
+                    top = fmaxf(top, x[b][i.value] + from_lane<i.value>(log));
+                    top_x = fmaxf(top_x, x[b][i.value]);
+                }, std::make_integer_sequence<int, 16>());
                 top = fmaxf(top, __shfl_xor(top, 32, 64));
-                const int over = most > limit, other = __shfl_xor(over, 32, 64);    // of the row's other half
-                const bool moves = (over | other) != 0 && top > -__builtin_inff();
-                const float by = moves ? move_reference(ref, top) : 0.0f;
+                top_x = fmaxf(top_x, __shfl_xor(top_x, 32, 64));
+                const int over = most > limit || part > kMostSum, other = __shfl_xor(over, 32, 64);
+                const bool moves = (over | other) != 0 && top > -__builtin_inff();      // the row's other half too
+                const float by = moves ? move_reference(ref, top, top_x) : 0.0f;
                 const float half = limit == kUnset ? 0.0f : -0.5f * by;
                 const float shrink = scaled(1.0f, half);
                 sum = scaled(sum, half);
@@ -1484,7 +1499,7 @@ __global__ __launch_bounds__(kManyThreads, 3) void attend_many_kernel(AttendPara
         if (w.pieces == 1) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                y[e] = sum == 0.0f ? 0.0f : y[e] * kSumUnit / sum;
+                y[e] = sum == 0.0f ? 0.0f : y[e] * kOutUnit / sum;
             store_bf16<E>(to + element, y);
         } else {
 #pragma unroll

@@ -702,11 +702,12 @@ dg_status dg_fp8_cache_read(const dg_fp8_cache *cache, const int64_t *slots,
  * tokens there), q_starts as the nearest from 0 to T.
  * The first product is one of exact bf16 values with fp32 sums; the second one
  * takes its weights, exp(x_j) times the value's scale, rounded to 11 bits, those
- * below 2^-21 of the row's largest to 2^-32 of it; the rest is fp32 up to the
- * rounding of out. Scales of values below 2^-100 in magnitude count as 0; where
- * the row's largest weight has a scale s, keys whose exp(x_j) is below 2^-133 s
- * of that one's do not count. Deterministic: the split of the keys follows from
- * the lengths, and partial results are added in a fixed order.
+ * below 2^-21 of the row's largest to 2^-32 of it, or of 2^-96 times its largest
+ * exp(x_j) where that is more; the rest is fp32 up to the rounding of out. Scales
+ * of values below 2^-114 in magnitude count as 0; where the row's largest weight
+ * has a scale s, keys whose exp(x_j) is below 2^-145 s of that one's do not count.
+ * Deterministic: the split of the keys follows from the lengths, and partial
+ * results are added in a fixed order.
  * Constraints: q_heads % heads == 0, both caches with the same sizes, window >=
  * 0, scale finite (DG_ERR_BAD_SHAPE); table_width * page_size at most 2^30, T *
  * q_heads below 2^31, B * heads * (table_width * page_size / 128 + 2) below

@@ -2,13 +2,13 @@
 those that it gives next to no weight, do not touch what the others give it.
 
 Tolerances: those of tests/test_gpu_attention_step.py, but for the last one, of weights below fp16's normal numbers. A
-weight p |sV| is off by 2^-25 there where the largest that its row sees is 2^7 or more; and it may drop out in fp32,
-below 2^-126 of an exponential that is 2^7 / sV or more where it counts most: with |sV| below 2^101 that is 2^-25 of the
-weight again. With M = max p |sV| / sum p over the keys that the row sees and codes below 2^9 in magnitude, n keys are
-off by n 2 2^-32 2^9 M = n 2^-22 M together. A row of zeros counts in M with 2^-100, which the kernels take for its
-scale: where the others' are hardly larger, its weight is the row's largest and theirs are rounded beside it. bf16's numbers below
-2^-126 are 2^-133 apart, so the rounding of an output is off by up to 2^-134 there, which is more than 2^-8 of it (the
-smallest outputs here are about 2^-125).
+weight p |sV| is off by 2^-25 there where the largest that its row sees is 2^7 or more, in units of 2^12 for sV; and it
+may drop out in fp32, below 2^-126 of an exponential that is 2^19 / |sV| or more where it counts most: with |sV| up to
+2^113 that is 2^-25 of the weight again. With M = max p |sV| / sum p over the keys that the row sees and codes below 2^9
+in magnitude, n keys are off by n 2 2^-32 2^9 M = n 2^-22 M together. Above 2^113 what drops out grows in proportion:
+`widen`. Exponentials end at 2^115, where 2^-25 of a weight is 2^-25 2^12 / 2^115 = 2^-32 2^-96 of p |sV| for the largest
+p: in M no scale counts as less than 2^-96, whatever it is. bf16's numbers below 2^-126 are 2^-133 apart, so the rounding
+of an output is off by up to 2^-134 there, which is more than 2^-8 of it (the smallest outputs here are about 2^-125).
 """
 import math
 
@@ -25,7 +25,7 @@ pytestmark = pytest.mark.gpu
 ALIASING, SCRATCH = 7, 8
 
 
-def reference(b, window=0):
+def reference(b, window=0, widen=1.0):
     """Outputs of a Batch in 64 bits and how far each may be off, from what its row sees alone."""
     scale, page, pages = b.D ** -0.5, b.page, b.k[0].shape[0]
     group = b.q.shape[1] // b.k[0].shape[2]
@@ -39,7 +39,7 @@ def reference(b, window=0):
         there = (held >= 0) & (held < pages)
         held = torch.where(there, held, 0)
         k, v = (values(c[held, j % page], s[held, j % page]) for c, s in (b.k, b.v))
-        weigh = torch.where((v != 0).any(-1), b.v[1][held, j % page].double().abs(), 2.0 ** -100)
+        weigh = torch.where((v != 0).any(-1), b.v[1][held, j % page].double().abs(), 0.0).clamp(min=2.0 ** -96)
         pos = torch.arange(n - m, n, device="cuda")[:, None]
         seen = (j <= pos) & there
         if window:
@@ -55,7 +55,7 @@ def reference(b, window=0):
             a = p @ vh.abs()
             tol[rows, h] = half(BF16) * out[rows, h].abs() + 2.0 ** -134 * (a > 0)
             tol[rows, h] += (2.0 ** -9 + 2.0 ** -19 + n * 2.0 ** -23) * a + pe @ vh.abs() + pe.sum(1, keepdim=True) * a
-            tol[rows, h] += n * 2.0 ** -22 * (p * w).amax(1, keepdim=True)
+            tol[rows, h] += widen * n * 2.0 ** -22 * (p * w).amax(1, keepdim=True)
     return out, tol
 
 
@@ -147,10 +147,23 @@ def test_pieces_whose_scales_lie_apart(gpu_device, lengths, heads, kv_heads, D, 
         hold(b.call(), *reference(b), slice(b.starts[0], b.starts[-1]))
 
 
+@pytest.mark.parametrize("power", [-112, -106, -100, 105, 112, 118])
+@pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
+def test_scales_at_the_ends(gpu_device, lengths, heads, kv_heads, D, page, power):
+    """All scales within a factor of two at the ends of what fp32 holds."""
+    b = Batch(lengths, heads, kv_heads, D, page, 37)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    b.v = (b.v[0], 2.0 ** power * (1 + torch.rand(b.v[1].shape, generator=g, device="cuda")))
+    got = b.call()
+    rows = slice(b.starts[0], b.starts[-1])
+    assert bool(got[rows].any(-1).all())
+    hold(got, *reference(b, widen=2.0 ** max(0, power + 1 - 113)), rows)
+
+
 @pytest.mark.parametrize("lengths,heads,kv_heads,D,page", MIXES)
 def test_scales_of_nothing(gpu_device, lengths, heads, kv_heads, D, page):
-    """Scales of 0 and below 2^-100 count as 0, among others and by themselves."""
-    for small in (0.0, 2.0 ** -101, 2.0 ** -149):
+    """Scales of 0 and below 2^-114 count as 0, among others and by themselves."""
+    for small in (0.0, 2.0 ** -115, 2.0 ** -149):
         b = Batch(lengths, heads, kv_heads, D, page, 36)
         some = torch.arange(b.v[1].numel(), device="cuda").view(b.v[1].shape) % 3 == 0
         b.v[1][some] = small
